@@ -316,6 +316,80 @@ int moe_layer_down(void* stream, const moe_layer* L, const moe_plan* P, const vo
  * blocks' sum fields (fp16 s widened) follow the scales, 256-byte aligned. */
 int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
 
+/* ---- Around the layer: the norm before it, routers of other kinds, and the shared expert (the
+ * dense half that every token takes) in 8-bit integers. Each call takes one token or thousands.
+ *
+ * Conventions beside those at the top: row strides (ld*) count elements and are at least the row
+ * length; any stride and any row alignment an element type allows is accepted (16-byte aligned rows
+ * are fastest). Row elements past the row length and rows past the last are neither read nor
+ * written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
+ * NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
+ * as their outputs do not. Outputs may not overlap inputs unless a comment says so. Results do not
+ * depend on the number of rows of the call: a row gives the same bits alone and among others.
+ *
+ * int8 rows ("i8"): a row of n float32 values y is kept as int8 codes q and one float32 scale d by
+ * the q8_1 rule with the row as the block: d = max|y| / 127 (float32), q = clamp(round-half-away(
+ * y / d), +-127) with the float32 quotient; d = 0 gives zero codes; a row holding an infinity or a
+ * NaN gives d = NaN and zero codes. The value a code stands for is q * d. */
+typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element types of rows */
+#define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
+#define MOE_MAX_MATMUL_K 131071   /* max K of moe_matmul_i8: K * 128 * 128 stays below 2^31 */
+
+/* RMS norm with the residual's addition and outputs in 8 bits, beside moe_quantize_q8_1. Per row:
+ *   r = x + res, rounded to float32 and then to the type of x (r = x when res is NULL);
+ *   y = float32(r * w / sqrt(mean(r^2) + eps)), evaluated in 64 bits and rounded once.
+ * x, res, res_out: `dtype`. weight [n]: w_dtype. Outputs, each written when its pointer is not NULL (at
+ * least one must be): res_out = r (it may be the same rows as x or as res: same pointer and
+ * stride); yout = y in y_dtype (the float rows moe_layer_decode and a router's product take); q and scale
+ * (both or neither) = i8 rows of y, for moe_matmul_i8; q8_1 = q8_1 blocks of y, byte for byte
+ * moe_quantize_q8_1 of the float32 y (rows of n/32 blocks, 4-byte aligned; n % 32 == 0), for
+ * moe_prefill_gate_up. Errors: MOE_E_ARG (null or misaligned pointer, bad type, stride, eps not
+ * finite and positive, overlap), MOE_E_SHAPE (n not in 1..MOE_MAX_ROW, or n % 32 with q8_1). */
+int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const void* res, int64_t ldres,
+                    int w_dtype, const void* weight, float eps, int rows, int n, void* res_out,
+                    int64_t ldro, int y_dtype, void* yout, int64_t ldy, int8_t* q, int64_t ldq, float* scale,
+                    void* q8_1);
+
+/* Router with scores of either kind, a balance bias, limited groups and optional renormalisation,
+ * beside moe_route_topk (softmax over float32 logits alone). Per token, over its E logits l:
+ *   s_e = exp(l_e) / sum exp(l)  (MOE_SCORE_SOFTMAX)  or  1 / (1 + exp(-l_e))  (MOE_SCORE_SIGMOID);
+ *   c_e = s_e + bias_e (bias float32 [E], finite; NULL: none), in 64 bits;
+ *   the E experts form n_groups runs of E / n_groups; a group's score is the sum of its group_top
+ *   (1 or 2) largest c; the keep_groups best groups stay (n_groups = 1: all experts);
+ *   ids = the k experts of those groups with the largest c, largest first (without a bias: by logit,
+ *   the same order also where scores round to one value); w = their s (not c), divided by their sum
+ *   when renorm = 1, times `factor`. Ties go to the lower index, for experts and for groups.
+ * A logit of -infinity or NaN masks its expert: s = 0, it adds nothing to its group's score (a group
+ * of masked experts comes after every other), and it is chosen only after every unmasked expert
+ * of the groups kept, lowest index first. A token with every expert masked gets weights 0. +infinity
+ * counts as the largest finite float32. The selection is that of 64-bit arithmetic; w is float32.
+ * logits [T][ld] in `dtype`; ids int32 [T][k], w float32 [T][k], as moe_build_plan and
+ * moe_prefill_plan take them. 1 <= E <= 1024, n_groups <= 64 and a divisor of E, 1 <= k <= 32 and
+ * k <= keep_groups * (E / n_groups), group_top <= E / n_groups; else MOE_E_ARG. */
+typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score;
+int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, int T, int E, int k, int score,
+                     const float* bias, int n_groups, int keep_groups, int group_top, int renorm,
+                     float factor, int32_t* ids, float* w);
+
+/* SwiGLU into i8 rows, beside moe_swiglu_q8_1: h = float32(g / (1 + exp(-g)) * u), evaluated in 64 bits
+ * and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in `dtype` of strides ldg
+ * and ldu (the two halves of one product's rows: u = g + n, both strides that product's).
+ * Errors: MOE_E_ARG (null or misaligned pointer, bad type or stride), MOE_E_SHAPE (n not in
+ * 1..MOE_MAX_ROW). */
+int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const void* u, int64_t ldu, int rows,
+                  int n, int8_t* q, int64_t ldq, float* scale);
+
+/* Matrix product of int8 rows with a scale per token and per channel, beside moe_prefill_gate_up /
+ * _down (the shared expert's products; the dense layers around): for m < M, n < N
+ *   C[m][n] = float32(sum_k a[m][k] b[n][k]) * sa[m] * sb[n], float32 products in that order,
+ * the sum exact in 32-bit integers (codes -128..127), plus C's previous value when accumulate = 1
+ * (one float32 sum, the routed experts' Y for example), rounded to c_dtype.
+ * a [M][lda], b [N][ldb] (weights, one row a channel), sa [M], sb [N] float32, C [M][ldc]. M = 0 or N = 0 does
+ * nothing. Errors: MOE_E_ARG (null or misaligned pointer, negative size, bad type or stride),
+ * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K). */
+int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb,
+                  const float* sb, int M, int N, int K, int c_dtype, void* C, int64_t ldc, int accumulate);
+
 /* The achievable-bandwidth reference the decode launches are measured against (not a step of the
  * method): one launch of `grid` workgroups of 256 threads reads the `bytes` at buf once with
  * 16-byte non-temporal loads, eight in flight per lane, the workgroups striding over the whole

@@ -26,11 +26,14 @@ EXPORTS = ("moe_route_topk", "moe_build_plan", "moe_quantize_q8_1", "moe_repack"
            "moe_layer_down",
            "moe_workspace_layout", "moe_prefill_plan", "moe_prefill_gate_up", "moe_prefill_swiglu_q8_1",
            "moe_prefill_down", "moe_prefill_scatter",
+           "moe_add_rmsnorm", "moe_route_scores", "moe_swiglu_i8", "moe_matmul_i8",
            "moe_stream_read", "moe_status_string", "moe_last_error")
 
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_int64
+_F = ctypes.c_float
 
 
 class MoeLayer(ctypes.Structure):
@@ -87,6 +90,10 @@ def lib():
         L.moe_status_string.argtypes = [_I]
         L.moe_last_error.restype = ctypes.c_char_p
         L.moe_stream_read.argtypes = [_P, _P, ctypes.c_uint64, _P, _I]
+        L.moe_add_rmsnorm.argtypes = [_P, _I, _P, _L, _P, _L, _I, _P, _F, _I, _I, _P, _L, _I, _P, _L, _P, _L, _P, _P]
+        L.moe_route_scores.argtypes = [_P, _I, _P, _L, _I, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P]
+        L.moe_swiglu_i8.argtypes = [_P, _I, _P, _L, _P, _L, _I, _I, _P, _L, _P]
+        L.moe_matmul_i8.argtypes = [_P, _P, _L, _P, _P, _L, _P, _I, _I, _I, _I, _P, _L, _I]
         _lib = L
     return _lib
 
@@ -379,6 +386,148 @@ def moe_layer_down(layer: Layer, plan: Plan, ws, n_tokens, Y, grid_limit=0, stre
                                 _ptr(ws), ws.numel(), n_tokens, _ptr(Y), Y.shape[0], Y.stride(0),
                                 grid_limit), "moe_layer_down")
 
+
+# ------------------------------------------------------------------ around the layer ----------
+
+F32, BF16, F16 = 1, 2, 3                 # element types of rows (moe_dtype)
+SCORE_SOFTMAX, SCORE_SIGMOID = 1, 2      # moe_score
+_DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
+
+
+class _On:
+    """Makes `device` current for a call whose tensors live on another one."""
+    __slots__ = ("guard",)
+
+    def __init__(self, device):
+        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _rows(what, name, t, shape, dtypes, device):
+    """Checks a 2-D tensor of rows (contiguous elements, any row stride) and returns its row stride."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}" + (f", not {shape}" if shape else ", not 2-D"))
+    if t.dtype not in dtypes:
+        raise ValueError(f"{what}: {name} is {t.dtype}")
+    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{what}: {name} is on {t.device}, not on the call's GPU")
+    rows, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what}: {name}'s row elements are not next to each other")
+    return max(t.stride(0), n) if rows <= 1 else t.stride(0)
+
+
+def _vec(what, name, t, n, dtypes, device):
+    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} has to be a contiguous vector of {n} on {device}, one of {dtypes}")
+
+
+_FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.float32,), (torch.uint8,), (torch.int32,)
+
+
+def i8_rows(rows, n, device="cuda"):
+    """New int8 rows and their scales: q [rows, n] (rows 16-byte aligned), scale [rows] float32."""
+    return (torch.empty((rows, -(-n // 16) * 16), dtype=torch.int8, device=device)[:, :n],
+            torch.empty(rows, dtype=torch.float32, device=device))
+
+
+def moe_add_rmsnorm(x, weight, eps, res=None, res_out=None, y=None, q=None, scale=None, q8_1=None, stream=None):
+    """RMS norm of x (+ res) rows [rows, n] into the outputs given: res_out (the sum, may be x or
+    res), y (float rows), q and scale (int8 rows), q8_1 (uint8 [rows, n / 32 * 36])."""
+    what, dev = "moe_add_rmsnorm", x.device
+    same = (x.dtype,)
+    ldx = _rows(what, "x", x, None, _FLOATS, dev)
+    shape = (rows, n) = tuple(x.shape)
+    _vec(what, "weight", weight, n, _FLOATS, dev)
+    ldres = _rows(what, "res", res, shape, same, dev) if res is not None else 0
+    ldro = _rows(what, "res_out", res_out, shape, same, dev) if res_out is not None else 0
+    ldy = _rows(what, "y", y, shape, _FLOATS, dev) if y is not None else 0
+    ldq = _rows(what, "q", q, shape, _INT8, dev) if q is not None else 0
+    if scale is not None:
+        _vec(what, "scale", scale, rows, _F32ONLY, dev)
+    if q8_1 is not None:
+        if n % 32:
+            raise ValueError(f"{what}: q8_1 rows need a multiple of 32 values, not {n}")
+        _rows(what, "q8_1", q8_1, (rows, n // 32 * 36), _BYTES, dev)
+        if not q8_1.is_contiguous():
+            raise ValueError(f"{what}: q8_1 is not contiguous")
+    with _On(dev):
+        _check(lib().moe_add_rmsnorm(_stream(stream), _DTYPE[x.dtype], _ptr(x), ldx, _ptr(res), ldres,
+                                     _DTYPE[weight.dtype], _ptr(weight), eps, rows, n, _ptr(res_out), ldro,
+                                     _DTYPE[y.dtype] if y is not None else 0, _ptr(y), ldy, _ptr(q), ldq, _ptr(scale),
+                                     _ptr(q8_1)), what)
+
+
+def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep_groups=1, group_top=1, renorm=True,
+                     factor=1.0, ids=None, w=None, stream=None):
+    """The k experts of each token (int32 [T, k]) and their weights (float32 [T, k]) from logits [T, E]."""
+    what, dev = "moe_route_scores", logits.device
+    ld = _rows(what, "logits", logits, None, _FLOATS, dev)
+    T, E = logits.shape
+    if bias is not None:
+        _vec(what, "bias", bias, E, _F32ONLY, dev)
+    ids = ids if ids is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
+    w = w if w is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
+    for name, t, kinds in (("ids", ids, _INT32), ("w", w, _F32ONLY)):
+        _rows(what, name, t, (T, k), kinds, dev)
+        if not t.is_contiguous():
+            raise ValueError(f"{what}: {name} is not contiguous")
+    with _On(dev):
+        _check(lib().moe_route_scores(_stream(stream), _DTYPE[logits.dtype], _ptr(logits), ld, T, E, k, score, _ptr(bias),
+                                      n_groups, keep_groups, group_top, 1 if renorm else 0, factor, _ptr(ids), _ptr(w)),
+               what)
+    return ids, w
+
+
+def moe_swiglu_i8(g, u, q=None, scale=None, stream=None):
+    """int8 rows (q, scale) of silu(g) * u for rows g, u [rows, n], each of its own row stride."""
+    what, dev = "moe_swiglu_i8", g.device
+    ldg = _rows(what, "g", g, None, _FLOATS, dev)
+    shape = (rows, n) = tuple(g.shape)
+    ldu = _rows(what, "u", u, shape, (g.dtype,), dev)
+    if (q is None) != (scale is None):
+        raise ValueError(f"{what}: q and scale come together")
+    if q is None:
+        q, scale = i8_rows(rows, n, dev)
+    ldq = _rows(what, "q", q, shape, _INT8, dev)
+    _vec(what, "scale", scale, rows, _F32ONLY, dev)
+    with _On(dev):
+        _check(lib().moe_swiglu_i8(_stream(stream), _DTYPE[g.dtype], _ptr(g), ldg, _ptr(u), ldu, rows, n, _ptr(q), ldq,
+                                   _ptr(scale)), what)
+    return q, scale
+
+
+def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, stream=None):
+    """C [M, N] (+)= (a [M, K] . b [N, K]^T) * sa [M] * sb [N] for int8 rows a, b; c, or a new tensor
+    of `dtype`."""
+    what, dev = "moe_matmul_i8", a.device
+    lda = _rows(what, "a", a, None, _INT8, dev)
+    M, K = a.shape
+    N = b.shape[0]
+    ldb = _rows(what, "b", b, (N, K), _INT8, dev)
+    _vec(what, "sa", sa, M, _F32ONLY, dev)
+    _vec(what, "sb", sb, N, _F32ONLY, dev)
+    if c is None:
+        if accumulate:
+            raise ValueError(f"{what}: accumulate needs c")
+        if dtype not in _DTYPE:
+            raise ValueError(f"{what}: dtype {dtype}")
+        c = torch.empty((M, N), dtype=dtype, device=dev)
+    ldc = _rows(what, "c", c, (M, N), _FLOATS, dev)
+    with _On(dev):
+        _check(lib().moe_matmul_i8(_stream(stream), _ptr(a), lda, _ptr(sa), _ptr(b), ldb, _ptr(sb), M, N, K,
+                                   _DTYPE[c.dtype], _ptr(c), ldc, 1 if accumulate else 0), what)
+    return c
+
+
+# ------------------------------------------------------------------ bandwidth reference -------
 
 def moe_stream_read(buf, out, grid, stream=None):
     """The achievable-bandwidth reference: one streaming read of `buf` (a contiguous device tensor

@@ -1,15 +1,16 @@
-"""Build step: compile csrc/moe_route.hip for gfx950 into libmoe_route.so next to this file."""
+"""Build step: compile the sources in csrc/ for gfx950 into libmoe_route.so next to this file."""
 from __future__ import annotations
 
 import os
 import subprocess
+from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SRC = os.path.join(HERE, "csrc", "moe_route.hip")
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route.hip", "moe_ops.hip")]
 LIB = os.path.join(HERE, "libmoe_route.so")
 
 HIPCC_FLAGS = [
-    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-shared",
+    "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
     # no packed-FP32 instructions anywhere in the device code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
     # IEEE float32 exactly as written: no FMA contraction, correctly rounded division, denormals
@@ -20,17 +21,26 @@ HIPCC_FLAGS = [
 ]
 
 
-def build(verbose: bool = False) -> str:
-    """Always recompiles (seconds); writes the library atomically."""
-    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    tmp = LIB + ".tmp"
-    cmd = [hipcc, *HIPCC_FLAGS, "-o", tmp, SRC]
+def _run(cmd) -> str:
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError("hipcc failed:\n" + res.stderr[-4000:])
-    if verbose and res.stderr:
-        print(res.stderr)
+    return res.stderr
+
+
+def build(verbose: bool = False) -> str:
+    """Always recompiles (the sources side by side); writes the library atomically."""
+    hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+    objs = [os.path.splitext(s)[0] + ".o" for s in SRCS]
+    with ThreadPoolExecutor(len(SRCS)) as pool:
+        logs = list(pool.map(lambda so: _run([hipcc, *HIPCC_FLAGS, "-c", "-o", so[1], so[0]]), zip(SRCS, objs)))
+    tmp = LIB + ".tmp"
+    logs.append(_run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objs]))
+    if verbose:
+        print("".join(logs))
     os.replace(tmp, LIB)
+    for o in objs:
+        os.remove(o)
     return LIB
 
 

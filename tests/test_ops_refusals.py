@@ -1,0 +1,101 @@
+"""Argument checks of the calls around the layer (moe_add_rmsnorm, moe_route_scores, moe_swiglu_i8,
+moe_matmul_i8): made on the host before anything is enqueued, so no GPU is needed. Pointers are
+fakes that no call below gets to use."""
+import ctypes
+import os
+
+import pytest
+import torch
+
+from moe_routed_expert_route_amd import binding as B
+
+ARG, SHAPE, OK = -1, -3, 0
+P, P2, P3, P4, P5 = (i << 32 for i in range(1, 6))   # far from each other
+NAN, INF = float("nan"), float("inf")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="library not built")
+
+NORM = dict(dtype=1, x=P, ldx=64, res=P2, ldres=64, w_dtype=1, weight=P3, eps=1e-6, rows=4, n=64, res_out=P2, ldro=64,
+            y_dtype=1, y=P4, ldy=64, q=P5, ldq=64, scale=P5 + 4096, q8_1=None)
+ROUTE = dict(dtype=1, logits=P, ld=64, T=4, E=64, k=8, score=1, bias=P2, n_groups=8, keep=4, top=2, renorm=1, factor=1.0,
+             ids=P3, w=P4)
+SWIGLU = dict(dtype=2, g=P, ldg=128, u=P + 128, ldu=128, rows=4, n=64, q=P3, ldq=64, scale=P4)
+MATMUL = dict(a=P, lda=64, sa=P2, b=P3, ldb=64, sb=P4, M=4, N=32, K=64, c_dtype=2, c=P5, ldc=32, accumulate=0)
+CALLS = {"moe_add_rmsnorm": NORM, "moe_route_scores": ROUTE, "moe_swiglu_i8": SWIGLU, "moe_matmul_i8": MATMUL}
+
+BAD = [
+    ("moe_add_rmsnorm", dict(dtype=0), ARG), ("moe_add_rmsnorm", dict(dtype=4), ARG), ("moe_add_rmsnorm", dict(w_dtype=9), ARG),
+    ("moe_add_rmsnorm", dict(y_dtype=0), ARG), ("moe_add_rmsnorm", dict(rows=-1), ARG), ("moe_add_rmsnorm", dict(n=0), SHAPE),
+    ("moe_add_rmsnorm", dict(n=16385, ldx=20000, ldres=20000, ldro=20000, ldy=20000, ldq=20000), SHAPE),
+    ("moe_add_rmsnorm", dict(eps=0.0), ARG), ("moe_add_rmsnorm", dict(eps=-1.0), ARG), ("moe_add_rmsnorm", dict(eps=NAN), ARG),
+    ("moe_add_rmsnorm", dict(eps=INF), ARG), ("moe_add_rmsnorm", dict(x=None), ARG), ("moe_add_rmsnorm", dict(weight=None), ARG),
+    ("moe_add_rmsnorm", dict(q=None), ARG), ("moe_add_rmsnorm", dict(scale=None), ARG),
+    ("moe_add_rmsnorm", dict(res_out=None, y=None, q=None, scale=None), ARG),
+    ("moe_add_rmsnorm", dict(ldx=63), ARG), ("moe_add_rmsnorm", dict(ldres=63), ARG), ("moe_add_rmsnorm", dict(ldro=63), ARG),
+    ("moe_add_rmsnorm", dict(ldy=63), ARG), ("moe_add_rmsnorm", dict(ldq=63), ARG), ("moe_add_rmsnorm", dict(x=P + 2), ARG),
+    ("moe_add_rmsnorm", dict(y=P4 + 1), ARG), ("moe_add_rmsnorm", dict(scale=P5 + 4098), ARG),
+    ("moe_add_rmsnorm", dict(n=63, q8_1=P4 + (1 << 20)), SHAPE), ("moe_add_rmsnorm", dict(q8_1=P4 + 2 + (1 << 20)), ARG),
+    ("moe_add_rmsnorm", dict(res_out=P2 + 4), ARG), ("moe_add_rmsnorm", dict(res_out=P2, ldro=65), ARG),
+    ("moe_add_rmsnorm", dict(y=P), ARG), ("moe_add_rmsnorm", dict(q=P + 100), ARG), ("moe_add_rmsnorm", dict(q8_1=P2 + 64), ARG),
+    ("moe_route_scores", dict(dtype=0), ARG), ("moe_route_scores", dict(T=-1), ARG), ("moe_route_scores", dict(E=0, ld=64), ARG),
+    ("moe_route_scores", dict(E=1025, ld=2048, n_groups=1, keep=1), ARG), ("moe_route_scores", dict(k=0), ARG),
+    ("moe_route_scores", dict(k=33), ARG), ("moe_route_scores", dict(k=9, keep=1), ARG), ("moe_route_scores", dict(score=0), ARG),
+    ("moe_route_scores", dict(score=3), ARG), ("moe_route_scores", dict(n_groups=0), ARG), ("moe_route_scores", dict(n_groups=7), ARG),
+    ("moe_route_scores", dict(E=650, ld=650, n_groups=65, keep=65), ARG), ("moe_route_scores", dict(keep=0), ARG),
+    ("moe_route_scores", dict(keep=9), ARG), ("moe_route_scores", dict(top=0), ARG), ("moe_route_scores", dict(top=3), ARG),
+    ("moe_route_scores", dict(E=8, ld=8, n_groups=8, keep=8, k=2, top=2), ARG), ("moe_route_scores", dict(renorm=2), ARG),
+    ("moe_route_scores", dict(factor=NAN), ARG), ("moe_route_scores", dict(ld=63), ARG), ("moe_route_scores", dict(logits=None), ARG),
+    ("moe_route_scores", dict(ids=None), ARG), ("moe_route_scores", dict(w=None), ARG), ("moe_route_scores", dict(logits=P + 2), ARG),
+    ("moe_route_scores", dict(ids=P3 + 2), ARG), ("moe_route_scores", dict(bias=P2 + 1), ARG),
+    ("moe_swiglu_i8", dict(dtype=7), ARG), ("moe_swiglu_i8", dict(rows=-1), ARG), ("moe_swiglu_i8", dict(n=0), SHAPE),
+    ("moe_swiglu_i8", dict(n=16385, ldg=40000, ldu=40000, ldq=20000), SHAPE), ("moe_swiglu_i8", dict(g=None), ARG),
+    ("moe_swiglu_i8", dict(u=None), ARG), ("moe_swiglu_i8", dict(q=None), ARG), ("moe_swiglu_i8", dict(scale=None), ARG),
+    ("moe_swiglu_i8", dict(ldg=63), ARG), ("moe_swiglu_i8", dict(ldu=63), ARG), ("moe_swiglu_i8", dict(ldq=63), ARG),
+    ("moe_swiglu_i8", dict(g=P + 1), ARG), ("moe_swiglu_i8", dict(u=P + 129), ARG), ("moe_swiglu_i8", dict(q=P + 64), ARG),
+    ("moe_matmul_i8", dict(c_dtype=0), ARG), ("moe_matmul_i8", dict(M=-1), ARG), ("moe_matmul_i8", dict(N=-1), ARG),
+    ("moe_matmul_i8", dict(K=0), SHAPE), ("moe_matmul_i8", dict(K=131072, lda=1 << 20, ldb=1 << 20), SHAPE),
+    ("moe_matmul_i8", dict(a=None), ARG), ("moe_matmul_i8", dict(b=None), ARG), ("moe_matmul_i8", dict(sa=None), ARG),
+    ("moe_matmul_i8", dict(sb=None), ARG), ("moe_matmul_i8", dict(c=None), ARG), ("moe_matmul_i8", dict(lda=63), ARG),
+    ("moe_matmul_i8", dict(ldb=63), ARG), ("moe_matmul_i8", dict(ldc=31), ARG), ("moe_matmul_i8", dict(sa=P2 + 2), ARG),
+    ("moe_matmul_i8", dict(c=P5 + 1), ARG), ("moe_matmul_i8", dict(accumulate=2), ARG),
+    # calls of no rows succeed without their row pointers, once their scalars are sound
+    ("moe_add_rmsnorm", dict(rows=0, x=None, res=None, y=None, q=None, scale=None), OK),
+    ("moe_route_scores", dict(T=0, logits=None, ids=None, w=None), OK),
+    ("moe_swiglu_i8", dict(rows=0, g=None, u=None, q=None, scale=None), OK),
+    ("moe_matmul_i8", dict(M=0, a=None, sa=None, c=None), OK), ("moe_matmul_i8", dict(N=0, b=None, sb=None, c=None), OK),
+]
+
+
+@pytest.mark.parametrize("name,change,want", BAD, ids=[f"{n}-{','.join(f'{k}={v}' for k, v in c.items())}" for n, c, _ in BAD])
+def test_refused_on_the_host(name, change, want):
+    args = dict(CALLS[name])
+    assert set(change) <= set(args)
+    args.update(change)
+    assert getattr(B.lib(), name)(None, *args.values()) == want
+
+
+def test_binding_refuses_tensors_of_the_cpu():
+    x, q = torch.zeros(2, 64), torch.zeros(2, 64, dtype=torch.int8)
+    s = torch.zeros(2)
+    for call in (lambda: B.moe_add_rmsnorm(x, torch.ones(64), 1e-6, y=x), lambda: B.moe_route_scores(x, 2),
+                 lambda: B.moe_swiglu_i8(x, x, q, s), lambda: B.moe_matmul_i8(q, s, q, s)):
+        with pytest.raises(ValueError, match="not on the call's GPU"):
+            call()
+
+
+def test_binding_refuses_shapes_types_and_strides():
+    x = torch.zeros(2, 64)
+    cuda = torch.device("cuda:0")
+    with pytest.raises(ValueError, match="shape"):
+        B._rows("call", "t", x, (2, 63), (torch.float32,), x.device)
+    with pytest.raises(ValueError, match="2-D"):
+        B._rows("call", "t", x[0], None, (torch.float32,), x.device)
+    with pytest.raises(ValueError, match="float32"):
+        B._rows("call", "t", x, None, (torch.int8,), x.device)
+    with pytest.raises(ValueError, match="on the call's GPU"):
+        B._rows("call", "t", x, None, (torch.float32,), cuda)
+    m = torch.zeros(64, 2, device="meta").t()
+    with pytest.raises(ValueError):
+        B._rows("call", "t", m, None, (torch.float32,), m.device)
+    with pytest.raises(ValueError, match="vector"):
+        B._vec("call", "t", torch.zeros(8)[::2], 4, (torch.float32,), torch.device("cpu"))
