@@ -14,6 +14,14 @@ namespace moe {
 int hip_fail(hipError_t e, const char* what);   // moe_route.hip: keeps the text for moe_last_error
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+
+// s_waitcnt vmcnt(n), the other counters left alone (n < 64; vmcnt in bits 3:0 and 15:14)
+#define MOE_OPS_VM(n) (((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+// Every LDS access of the wave has finished, then the workgroup meets.
+__device__ __forceinline__ void ops_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
 
 // ------------------------------------------------------------------ element types -----------
 
@@ -297,40 +305,201 @@ struct MatmulArgs {
   void* c;
   int64_t lda, ldb, ldc;
   int M, N, K, accumulate;
+  int tiles_n, tiles;   // tile grid: channels, all
+  int vec;              // rows of C and sb take four-value accesses
+  int c_dtype;
 };
 
-// 16 bytes of a row from column k, zero from column K on (rows at any alignment).
+// 16 bytes of a row from column k, zero from column K on (rows at any alignment): the last 16 bytes of
+// the row shifted down where the piece passes K. Rows shorter than that are read byte by byte.
 __device__ __forceinline__ i32x4 row16(const int8_t* p, int k, int K) {
-  i32x4 v = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&v, p + k, 16);
+  uint64_t lo = 0, hi = 0;
+  if (K < 16) {
+#pragma unroll 1
+    for (int i = K - 1; i >= k; --i) {
+      hi = hi << 8 | lo >> 56;
+      lo = lo << 8 | (uint64_t)(uint8_t)p[i];
+    }
   } else {
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-      if (k + i < K) v[i / 4] |= (int)((uint32_t)(uint8_t)p[k + i] << (8 * (i % 4)));
+    const int at = min(k, K - 16), cut = min(k - at, 16), sh = 8 * (cut & 7);
+    __builtin_memcpy(&lo, p + at, 8);
+    __builtin_memcpy(&hi, p + at + 8, 8);
+    if (cut >= 8) lo = hi, hi = 0;
+    if (sh) lo = lo >> sh | hi << (64 - sh), hi >>= sh;
+    if (cut == 16) lo = 0;
   }
+  return __builtin_bit_cast(i32x4, u64x2{lo, hi});
+}
+__device__ __forceinline__ i32x4 any16(const int8_t* p) {   // 16 bytes at any alignment
+  i32x4 v;
+  __builtin_memcpy(&v, p, 16);
   return v;
 }
 
-// One wave a 16 x 16 tile: v_mfma_i32_16x16x64_i8 with the channels as rows and the tokens as
-// columns, so that a lane ends with four neighbouring channels of one token.
+// One value of C: scales, the previous value, the type's rounding.
 template <typename T>
-__global__ __launch_bounds__(64) void k_matmul_i8(MatmulArgs p) {
-  const int lane = threadIdx.x, n0 = blockIdx.x * 16, m0 = blockIdx.y * 16;
-  const int n = min(n0 + (lane & 15), p.N - 1), m = min(m0 + (lane & 15), p.M - 1);
-  const int8_t* a = p.a + m * p.lda;
-  const int8_t* b = p.b + n * p.ldb;
-  i32x4 acc = {0, 0, 0, 0};
-  for (int k = (lane >> 4) * 16; k - (lane >> 4) * 16 < p.K; k += 64)
-    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(row16(b, k, p.K), row16(a, k, p.K), acc, 0, 0, 0);
-  const int mo = m0 + (lane & 15), no = n0 + 4 * (lane >> 4);
-  if (mo >= p.M) return;
-  T* c = (T*)p.c + mo * p.ldc;
-  for (int i = 0; i < 4 && no + i < p.N; ++i) {
-    float v = (float)acc[i] * p.sa[mo] * p.sb[no + i];
-    if (p.accumulate) v += to_f(c[no + i]);
-    c[no + i] = from_f<T>(v);
+__device__ __forceinline__ void store_one(const MatmulArgs& p, int m, int n, int sum) {
+  T* c = (T*)p.c + m * p.ldc + n;
+  float v = (float)sum * p.sa[m] * p.sb[n];
+  if (p.accumulate) v += to_f(*c);
+  *c = from_f<T>(v);
+}
+// Four neighbouring channels of one token.
+template <typename T>
+__device__ __forceinline__ void store_four(const MatmulArgs& p, int m, int n, float sa, const f32x4& sb, i32x4 s) {
+  struct alignas(4 * sizeof(T)) T4 {
+    T v[4];
+  };
+  T4* c = (T4*)((T*)p.c + m * p.ldc + n);
+  T4 o;
+  if (p.accumulate) {
+    const T4 old = *c;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = from_f<T>((float)s[i] * sa * sb[i] + to_f(old.v[i]));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o.v[i] = from_f<T>((float)s[i] * sa * sb[i]);
   }
+  *c = o;
+}
+
+constexpr int kMmK = 128;   // bytes of K per step
+
+// One workgroup a tile of BT tokens x BC channels, WT x WC waves. v_mfma_i32_16x16x64_i8 with the
+// channels as rows and the tokens as columns, so that a lane ends with four neighbouring channels of
+// one token. A ring of S stages in LDS holds BT + BC rows of 128 bytes, a row's 16-byte chunk c at
+// place c ^ (row & 7): the eight rows that eight lanes read at one chunk then sit in different banks.
+// DIRECT: rows and their stride are 16-byte aligned and go straight to LDS; else through registers. A
+// last piece of K below 128 bytes is taken first, through registers, zero past K.
+template <int BT, int BC, int WT, int WC, bool DIRECT>
+__global__ __launch_bounds__(64 * WT * WC) void k_matmul_tile(MatmulArgs p) {
+  extern __shared__ __align__(16) uint8_t s_ring[];
+  constexpr int W = WT * WC, R = BT + BC, L = R / 8 / W;   // L: 8-row pieces a wave loads per step
+  constexpr int NT = BT / WT / 16, NC = BC / WC / 16, STAGE = R * kMmK;
+  static_assert(R % (8 * W) == 0 && BT % (16 * WT) == 0 && BC % (16 * WC) == 0 && NC >= 2, "tile split");
+  static_assert(2 * STAGE >= W * NC * 1024, "the epilogue's piece of each wave fits");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  // Workgroups go to the eight dies in turn: each die takes one run of tiles, in 4-token-tile strips, so
+  // that what its workgroups read together is a near-square patch that its L2 holds.
+  int id = blockIdx.x;
+  {
+    const int per = p.tiles / 8, extra = p.tiles % 8, die = id & 7, i = id >> 3;
+    id = die * per + min(die, extra) + i;
+  }
+  const int tiles_m = p.tiles / p.tiles_n, strip = id / (4 * p.tiles_n), in = id - strip * 4 * p.tiles_n;
+  const int hs = min(4, tiles_m - 4 * strip);
+  const int m0 = (4 * strip + in % hs) * BT, n0 = (in / hs) * BC;
+
+  // this lane's rows: piece i of the wave is rows 8 (wave + W i) .. + 7 of the stage, tokens first
+  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
+  const int8_t* src[L];
+#pragma unroll
+  for (int i = 0; i < L; ++i) {
+    const int r = 8 * (wave + W * i) + (lane >> 3);
+    src[i] = (r < BT ? p.a + min(m0 + r, p.M - 1) * p.lda : p.b + min(n0 + r - BT, p.N - 1) * p.ldb) + chunk;
+  }
+  const int rem = p.K % kMmK, steps = (p.K + kMmK - 1) / kMmK;
+  i32x4 hold[L];
+  auto fetch = [&](int t) {   // step t on its way to LDS, or to registers
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      if constexpr (DIRECT)
+        __builtin_amdgcn_global_load_lds((const void*)src[i],
+                                         (MOE_LDS void*)(s_ring + (t & 1) * STAGE + 1024 * (wave + W * i)), 16, 0, 0);
+      else
+        hold[i] = any16(src[i]);
+      src[i] += kMmK;
+    }
+  };
+  auto put = [&](int t) {     // registers to LDS
+#pragma unroll
+    for (int i = 0; i < L; ++i) *(i32x4*)(s_ring + (t & 1) * STAGE + 1024 * (wave + W * i) + 16 * lane) = hold[i];
+  };
+  const int wt = wave % WT, wc = wave / WT, row = lane & 15, quad = lane >> 4;
+  i32x4 acc[NC][NT];
+#pragma unroll
+  for (int i = 0; i < NC; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+  auto compute = [&](int t) {
+    const uint8_t* st = s_ring + (t & 1) * STAGE;
+    i32x4 av[2][NC], bv[2][NT];
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {
+      const int at = ((4 * kk + quad) ^ (row & 7)) * 16 + row * kMmK;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) bv[kk][j] = *(const i32x4*)(st + (wt * NT + j) * 16 * kMmK + at);
+#pragma unroll
+      for (int i = 0; i < NC; ++i) av[kk][i] = *(const i32x4*)(st + (BT + (wc * NC + i) * 16) * kMmK + at);
+    }
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[kk][i], bv[kk][j], acc[i][j], 0, 0, 0);
+    // reads two channel tiles ahead of the products that use them
+    __builtin_amdgcn_sched_group_barrier(0x100, NT + 2, 0);
+#pragma unroll
+    for (int s = 0; s < 2 * NC; ++s) {
+      __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
+      if (s < NC - 2 || (s >= NC && s < 2 * NC - 2)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (s == NC - 2) __builtin_amdgcn_sched_group_barrier(0x100, NT / 2 + 1, 0);
+      if (s == NC - 1) __builtin_amdgcn_sched_group_barrier(0x100, NT - NT / 2 + 1, 0);
+    }
+  };
+  if (rem) {
+#pragma unroll
+    for (int i = 0; i < L; ++i) hold[i] = row16(src[i] - chunk, p.K - rem + chunk, p.K);
+    put(0);
+  } else {
+    fetch(0);
+    if (!DIRECT) put(0);
+  }
+  for (int t = 0; t < steps; ++t) {
+    __builtin_amdgcn_s_waitcnt(MOE_OPS_VM(0));
+    ops_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (t + 1 < steps) fetch(t + 1);
+    compute(t);
+    __builtin_amdgcn_sched_barrier(0);
+    if (!DIRECT && t + 1 < steps) put(t + 1);
+  }
+  auto finish = [&](auto type) {
+    using T = decltype(type);
+    if (p.vec && m0 + BT <= p.M && n0 + BC <= p.N) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int m = m0 + (wt * NT + j) * 16 + row;
+        const float sa = p.sa[m];
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          const int n = n0 + (wc * NC + i) * 16 + 4 * quad;
+          store_four<T>(p, m, n, sa, *(const f32x4*)(p.sb + n), acc[i][j]);
+        }
+      }
+    } else {   // ragged or unaligned: through the wave's piece of LDS, so that lanes write along a row
+      ops_barrier();
+      int* mine = (int*)(s_ring + wave * NC * 1024);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) *(i32x4*)(mine + row * 16 * NC + 16 * i + 4 * quad) = acc[i][j];
+        __builtin_amdgcn_wave_barrier();
+        const int m1 = m0 + (wt * NT + j) * 16, n1 = n0 + wc * NC * 16;
+#pragma unroll 1
+        for (int e = lane; e < 256 * NC; e += 64) {
+          const int m = m1 + e / (16 * NC), n = n1 + e % (16 * NC);
+          if (m < p.M && n < p.N) store_one<T>(p, m, n, mine[e]);
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  };
+  if (p.c_dtype == MOE_F32) finish(float{});
+  else if (p.c_dtype == MOE_BF16) finish(bf16_t{});
+  else finish(f16_t{});
 }
 
 // ------------------------------------------------------------------ host checks -------------
@@ -348,6 +517,34 @@ bool overlap(const void* p, int64_t ldp, int sp, const void* q, int64_t ldq, int
 int launched(const char* what) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? MOE_OK : hip_fail(e, what);
+}
+
+template <int BT, int BC, int WT, int WC>
+int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
+  const int64_t tn = (p.N + BC - 1) / BC, tiles = tn * ((p.M + BT - 1) / BT);
+  if (tiles > 0x7FFFFFFF) return MOE_E_SHAPE;
+  p.tiles_n = (int)tn;
+  p.tiles = (int)tiles;
+  constexpr int lds = 2 * (BT + BC) * kMmK;
+  auto go = [&](auto kern) {
+    if (lds > 64 * 1024) {
+      const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      if (e != hipSuccess) return hip_fail(e, "moe_matmul_i8");
+    }
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * WT * WC), lds, st, p);
+    return launched("moe_matmul_i8");
+  };
+  return direct ? go(k_matmul_tile<BT, BC, WT, WC, true>) : go(k_matmul_tile<BT, BC, WT, WC, false>);
+}
+
+int run_matmul(hipStream_t st, MatmulArgs p) {
+  const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0;
+  p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
+  const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
+  const int64_t mid = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
+  if (big >= 200) return launch_tile<256, 256, 4, 2>(st, p, direct);
+  if (mid >= 200) return launch_tile<128, 128, 2, 2>(st, p, direct);
+  return launch_tile<64, 64, 2, 2>(st, p, direct);
 }
 
 }  // namespace moe
@@ -427,11 +624,7 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
   if (M == 0 || N == 0) return MOE_OK;
   if (!a || !sa || !b || !sb || !C || lda < K || ldb < K || ldc < N) return MOE_E_ARG;
   if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(C, type_size(c_dtype))) return MOE_E_ARG;
-  const MatmulArgs p{a, b, sa, sb, C, lda, ldb, ldc, M, N, K, accumulate};
-  with_type(c_dtype, [&](auto t) {
-    hipLaunchKernelGGL(k_matmul_i8<decltype(t)>, dim3((N + 15) / 16, (M + 15) / 16), dim3(64), 0, (hipStream_t)stream, p);
-  });
-  return launched("moe_matmul_i8");
+  return run_matmul((hipStream_t)stream, MatmulArgs{a, b, sa, sb, C, lda, ldb, ldc, M, N, K, accumulate, 0, 0, 0, c_dtype});
 }
 
 }  // extern "C"

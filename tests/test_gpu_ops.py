@@ -389,7 +389,7 @@ SIZES = [(1, 1, 1), (1, 16, 64), (1, 17, 63), (2, 1536, 2560), (3, 100, 1000), (
          (7, 64, 8192), (8, 129, 512), (9, 640, 2560), (15, 128, 128), (16, 16, 16), (17, 257, 129), (31, 512, 640), (33, 31, 33),
          (48, 1000, 1001), (64, 1536, 2560), (65, 65, 65), (100, 2560, 768), (127, 129, 255), (128, 128, 128), (129, 300, 2048),
          (200, 640, 1111), (256, 256, 256), (257, 511, 384), (300, 1024, 1024), (509, 517, 523), (520, 2560, 768),
-         (700, 777, 130), (1030, 1536, 640), (2050, 513, 192), (1, 8200, 4096), (40, 4096, 97)]
+         (4100, 3301, 200), (3330, 4096, 384), (2048, 6400, 129), (4096, 4096, 144), (700, 777, 130), (1030, 1536, 640), (2050, 513, 192), (1, 8200, 4096), (40, 4096, 97)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)
@@ -398,14 +398,14 @@ def test_matmul(M, N, K):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
-@pytest.mark.parametrize("M,N,K", [(1, 130, 320), (6, 257, 511), (37, 300, 640), (130, 192, 256), (300, 515, 1000), (600, 1024, 512)])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 320), (6, 257, 511), (37, 300, 640), (130, 192, 256), (300, 515, 1000), (600, 1024, 512), (3400, 4100, 272)])
 def test_matmul_types_and_accumulation(M, N, K, dtype):
     a, b = i8((M, K), M, 50), i8((N, K), N, 51)
     check_matmul(a, b, dtype)
     check_matmul(a, b, c=randn((M, N), dtype, M, N, 52), accumulate=True)
 
 
-@pytest.mark.parametrize("M", [1, 5, 40, 300, 1100])
+@pytest.mark.parametrize("M", [1, 5, 40, 300, 1100, 33000])
 @pytest.mark.parametrize("lda,ldb,ldc,off", [(261, 259, 201, 1), (272, 288, 208, 16), (264, 268, 204, 4), (512, 257, 1000, 3)])
 def test_matmul_strides_and_untouched_bytes(M, lda, ldb, ldc, off):
     N, K = 200, 257
