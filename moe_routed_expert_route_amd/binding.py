@@ -394,136 +394,161 @@ SCORE_SOFTMAX, SCORE_SIGMOID = 1, 2      # moe_score
 _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
-class _On:
-    """Makes `device` current for a call whose tensors live on another one."""
-    __slots__ = ("guard",)
+_FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.float32,), (torch.uint8,), (torch.int32,)
 
-    def __init__(self, device):
-        self.guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
+# These calls can be a few microseconds long: the checks below ask each tensor for as little as they can,
+# pointers go to ctypes as plain numbers, and the stream comes without a Stream object.
+def _call(what, device, stream, *args):
+    """Enqueues on `stream` (default: the current one of the tensors' GPU `device`, an index), with that
+    GPU current."""
+    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+    fn = getattr(lib(), what)
+    if torch.cuda.current_device() == device:
+        rc = fn(st, *args)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(st, *args)
+    if rc:
+        _check(rc, what)
 
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
+
+def _gpu(what, name, t):
+    """The index of the GPU that t, the call's first tensor, is on."""
+    device = t.get_device()
+    if device < 0:
+        raise ValueError(f"{what}: {name} is on {t.device}, not on a GPU")
+    return device
 
 
 def _rows(what, name, t, shape, dtypes, device):
-    """Checks a 2-D tensor of rows (contiguous elements, any row stride) and returns its row stride."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise ValueError(f"{what}: {name} has shape {tuple(t.shape)}" + (f", not {shape}" if shape else ", not 2-D"))
+    """The row stride of t, checked to be rows (any stride, elements next to each other) of `shape` (None:
+    any) and one of `dtypes` on GPU `device`."""
+    strides, size = t.stride(), t.shape
+    if len(size) != 2 or (shape is not None and size != shape):
+        raise ValueError(f"{what}: {name} has shape {tuple(size)}, not " + ("rows" if shape is None else str(tuple(shape))))
     if t.dtype not in dtypes:
-        raise ValueError(f"{what}: {name} is {t.dtype}")
-    if t.device != device or device.type != "cuda":
+        raise ValueError(f"{what}: {name} is {t.dtype}, not one of {dtypes}")
+    if t.get_device() != device:
         raise ValueError(f"{what}: {name} is on {t.device}, not on the call's GPU")
-    rows, n = t.shape
-    if n > 1 and t.stride(1) != 1:
+    rows, n = size
+    ld, step = strides
+    if step != 1 and n > 1:
         raise ValueError(f"{what}: {name}'s row elements are not next to each other")
-    return max(t.stride(0), n) if rows <= 1 else t.stride(0)
+    return ld if rows > 1 or ld > n else n
 
 
-def _vec(what, name, t, n, dtypes, device):
-    if t.dim() != 1 or t.shape[0] != n or t.dtype not in dtypes or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{what}: {name} has to be a contiguous vector of {n} on {device}, one of {dtypes}")
+def _packed(what, name, t, shape, dtype, device):
+    """t checked to be contiguous, of `shape` and `dtype` on GPU `device`."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{what}: {name} is {t.dtype} {tuple(t.shape)} on {t.device}, not contiguous {dtype} {shape} on the "
+                         "call's GPU")
 
 
-_FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.float32,), (torch.uint8,), (torch.int32,)
+def _new_i8(like, rows, n):
+    q = like.new_empty((rows, (n + 15) // 16 * 16), dtype=torch.int8)
+    return (q if n % 16 == 0 else q[:, :n]), like.new_empty(rows, dtype=torch.float32)
 
 
 def i8_rows(rows, n, device="cuda"):
     """New int8 rows and their scales: q [rows, n] (rows 16-byte aligned), scale [rows] float32."""
-    return (torch.empty((rows, -(-n // 16) * 16), dtype=torch.int8, device=device)[:, :n],
-            torch.empty(rows, dtype=torch.float32, device=device))
+    return _new_i8(torch.empty(0, device=device), rows, n)
 
 
 def moe_add_rmsnorm(x, weight, eps, res=None, res_out=None, y=None, q=None, scale=None, q8_1=None, stream=None):
     """RMS norm of x (+ res) rows [rows, n] into the outputs given: res_out (the sum, may be x or
     res), y (float rows), q and scale (int8 rows), q8_1 (uint8 [rows, n / 32 * 36])."""
-    what, dev = "moe_add_rmsnorm", x.device
-    same = (x.dtype,)
+    what = "moe_add_rmsnorm"
+    dev, size, same = _gpu(what, "x", x), x.shape, (x.dtype,)
     ldx = _rows(what, "x", x, None, _FLOATS, dev)
-    shape = (rows, n) = tuple(x.shape)
-    _vec(what, "weight", weight, n, _FLOATS, dev)
-    ldres = _rows(what, "res", res, shape, same, dev) if res is not None else 0
-    ldro = _rows(what, "res_out", res_out, shape, same, dev) if res_out is not None else 0
-    ldy = _rows(what, "y", y, shape, _FLOATS, dev) if y is not None else 0
-    ldq = _rows(what, "q", q, shape, _INT8, dev) if q is not None else 0
+    rows, n = size
+    if weight.dtype not in _DTYPE:
+        raise ValueError(f"{what}: weight is {weight.dtype}")
+    _packed(what, "weight", weight, (n,), weight.dtype, dev)
+    ldres = ldro = ldy = ldq = y_type = 0
+    if res is not None:
+        ldres = _rows(what, "res", res, size, same, dev)
+    if res_out is not None:
+        ldro = _rows(what, "res_out", res_out, size, same, dev)
+    if y is not None:
+        ldy, y_type = _rows(what, "y", y, size, _FLOATS, dev), _DTYPE[y.dtype]
+    if q is not None:
+        ldq = _rows(what, "q", q, size, _INT8, dev)
     if scale is not None:
-        _vec(what, "scale", scale, rows, _F32ONLY, dev)
+        _packed(what, "scale", scale, (rows,), torch.float32, dev)
     if q8_1 is not None:
         if n % 32:
             raise ValueError(f"{what}: q8_1 rows need a multiple of 32 values, not {n}")
-        _rows(what, "q8_1", q8_1, (rows, n // 32 * 36), _BYTES, dev)
-        if not q8_1.is_contiguous():
-            raise ValueError(f"{what}: q8_1 is not contiguous")
-    with _On(dev):
-        _check(lib().moe_add_rmsnorm(_stream(stream), _DTYPE[x.dtype], _ptr(x), ldx, _ptr(res), ldres,
-                                     _DTYPE[weight.dtype], _ptr(weight), eps, rows, n, _ptr(res_out), ldro,
-                                     _DTYPE[y.dtype] if y is not None else 0, _ptr(y), ldy, _ptr(q), ldq, _ptr(scale),
-                                     _ptr(q8_1)), what)
+        _packed(what, "q8_1", q8_1, (rows, n // 32 * 36), torch.uint8, dev)
+    _call(what, dev, stream, _DTYPE[x.dtype], x.data_ptr(), ldx, res.data_ptr() if res is not None else 0, ldres,
+          _DTYPE[weight.dtype], weight.data_ptr(), eps, rows, n, res_out.data_ptr() if res_out is not None else 0, ldro,
+          y_type, y.data_ptr() if y is not None else 0, ldy, q.data_ptr() if q is not None else 0, ldq,
+          scale.data_ptr() if scale is not None else 0, q8_1.data_ptr() if q8_1 is not None else 0)
 
 
 def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep_groups=1, group_top=1, renorm=True,
                      factor=1.0, ids=None, w=None, stream=None):
     """The k experts of each token (int32 [T, k]) and their weights (float32 [T, k]) from logits [T, E]."""
-    what, dev = "moe_route_scores", logits.device
+    what = "moe_route_scores"
+    dev = _gpu(what, "logits", logits)
     ld = _rows(what, "logits", logits, None, _FLOATS, dev)
     T, E = logits.shape
     if bias is not None:
-        _vec(what, "bias", bias, E, _F32ONLY, dev)
-    ids = ids if ids is not None else torch.empty((T, k), dtype=torch.int32, device=dev)
-    w = w if w is not None else torch.empty((T, k), dtype=torch.float32, device=dev)
-    for name, t, kinds in (("ids", ids, _INT32), ("w", w, _F32ONLY)):
-        _rows(what, name, t, (T, k), kinds, dev)
-        if not t.is_contiguous():
-            raise ValueError(f"{what}: {name} is not contiguous")
-    with _On(dev):
-        _check(lib().moe_route_scores(_stream(stream), _DTYPE[logits.dtype], _ptr(logits), ld, T, E, k, score, _ptr(bias),
-                                      n_groups, keep_groups, group_top, 1 if renorm else 0, factor, _ptr(ids), _ptr(w)),
-               what)
+        _packed(what, "bias", bias, (E,), torch.float32, dev)
+    if ids is None:
+        ids = logits.new_empty((T, k), dtype=torch.int32)
+    else:
+        _packed(what, "ids", ids, (T, k), torch.int32, dev)
+    if w is None:
+        w = logits.new_empty((T, k), dtype=torch.float32)
+    else:
+        _packed(what, "w", w, (T, k), torch.float32, dev)
+    _call(what, dev, stream, _DTYPE[logits.dtype], logits.data_ptr(), ld, T, E, k, score,
+          bias.data_ptr() if bias is not None else 0, n_groups, keep_groups, group_top, 1 if renorm else 0, factor,
+          ids.data_ptr(), w.data_ptr())
     return ids, w
 
 
 def moe_swiglu_i8(g, u, q=None, scale=None, stream=None):
     """int8 rows (q, scale) of silu(g) * u for rows g, u [rows, n], each of its own row stride."""
-    what, dev = "moe_swiglu_i8", g.device
+    what = "moe_swiglu_i8"
+    dev, size = _gpu(what, "g", g), g.shape
     ldg = _rows(what, "g", g, None, _FLOATS, dev)
-    shape = (rows, n) = tuple(g.shape)
-    ldu = _rows(what, "u", u, shape, (g.dtype,), dev)
+    ldu = _rows(what, "u", u, size, (g.dtype,), dev)
+    rows, n = size
     if (q is None) != (scale is None):
         raise ValueError(f"{what}: q and scale come together")
     if q is None:
-        q, scale = i8_rows(rows, n, dev)
-    ldq = _rows(what, "q", q, shape, _INT8, dev)
-    _vec(what, "scale", scale, rows, _F32ONLY, dev)
-    with _On(dev):
-        _check(lib().moe_swiglu_i8(_stream(stream), _DTYPE[g.dtype], _ptr(g), ldg, _ptr(u), ldu, rows, n, _ptr(q), ldq,
-                                   _ptr(scale)), what)
+        q, scale = _new_i8(g, rows, n)
+        ldq = q.stride(0)
+    else:
+        ldq = _rows(what, "q", q, size, _INT8, dev)
+        _packed(what, "scale", scale, (rows,), torch.float32, dev)
+    _call(what, dev, stream, _DTYPE[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu, rows, n, q.data_ptr(), ldq,
+          scale.data_ptr())
     return q, scale
 
 
 def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, stream=None):
     """C [M, N] (+)= (a [M, K] . b [N, K]^T) * sa [M] * sb [N] for int8 rows a, b; c, or a new tensor
     of `dtype`."""
-    what, dev = "moe_matmul_i8", a.device
-    lda = _rows(what, "a", a, None, _INT8, dev)
+    what = "moe_matmul_i8"
+    dev = _gpu(what, "a", a)
+    lda, ldb = _rows(what, "a", a, None, _INT8, dev), _rows(what, "b", b, None, _INT8, dev)
     M, K = a.shape
-    N = b.shape[0]
-    ldb = _rows(what, "b", b, (N, K), _INT8, dev)
-    _vec(what, "sa", sa, M, _F32ONLY, dev)
-    _vec(what, "sb", sb, N, _F32ONLY, dev)
+    N, kb = b.shape
+    if kb != K:
+        raise ValueError(f"{what}: rows of {K} and of {kb} values")
+    _packed(what, "sa", sa, (M,), torch.float32, dev)
+    _packed(what, "sb", sb, (N,), torch.float32, dev)
     if c is None:
-        if accumulate:
-            raise ValueError(f"{what}: accumulate needs c")
-        if dtype not in _DTYPE:
-            raise ValueError(f"{what}: dtype {dtype}")
-        c = torch.empty((M, N), dtype=dtype, device=dev)
-    ldc = _rows(what, "c", c, (M, N), _FLOATS, dev)
-    with _On(dev):
-        _check(lib().moe_matmul_i8(_stream(stream), _ptr(a), lda, _ptr(sa), _ptr(b), ldb, _ptr(sb), M, N, K,
-                                   _DTYPE[c.dtype], _ptr(c), ldc, 1 if accumulate else 0), what)
+        if accumulate or dtype not in _DTYPE:
+            raise ValueError(f"{what}: accumulate needs c" if accumulate else f"{what}: dtype {dtype}")
+        c, ldc = a.new_empty((M, N), dtype=dtype), N
+    else:
+        dtype, ldc = c.dtype, _rows(what, "c", c, (M, N), _FLOATS, dev)
+    _call(what, dev, stream, a.data_ptr(), lda, sa.data_ptr(), b.data_ptr(), ldb, sb.data_ptr(), M, N, K, _DTYPE[dtype],
+          c.data_ptr(), ldc, 1 if accumulate else 0)
     return c
 
 

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "../../include/moe_route.h"
 #include "moe_device.hpp"
@@ -69,40 +70,141 @@ __device__ __forceinline__ void store_f(void* p, int dtype, int64_t i, float v) 
   else ((f16_t*)p)[i] = from_f<f16_t>(v);
 }
 
-// ------------------------------------------------------------------ workgroup sums ----------
+// ------------------------------------------------------------------ rows --------------------
+//
+// moe_add_rmsnorm and moe_swiglu_i8 give a row to one workgroup, which reads it once and keeps it in
+// registers, eight neighbouring values a thread (16-byte accesses for 16-bit types) and C such pieces.
 
-constexpr int kRowThreads = 256;
+constexpr int kPiece = 8;
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
-  for (int o = 32; o; o >>= 1) v += __shfl_xor(v, o);
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0.0;
-  for (int w = 0; w < kRowThreads / 64; ++w) v += red[w];
-  __syncthreads();
+template <typename T>
+__device__ __forceinline__ void load_piece(const T* p, int i, int n, float (&f)[kPiece]) {
+  if (i + kPiece <= n) {
+    T v[kPiece];
+    __builtin_memcpy(v, p + i, sizeof v);   // any alignment T allows
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) f[e] = to_f(v[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) f[e] = i + e < n ? to_f(p[i + e]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void load_piece(const void* p, int dtype, int i, int n, float (&f)[kPiece]) {
+  if (dtype == MOE_F32) load_piece((const float*)p, i, n, f);
+  else if (dtype == MOE_BF16) load_piece((const bf16_t*)p, i, n, f);
+  else load_piece((const f16_t*)p, i, n, f);
+}
+template <typename T>
+__device__ __forceinline__ void store_piece(T* p, int i, int n, const float (&f)[kPiece]) {
+  if (i + kPiece <= n) {
+    T v[kPiece];
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) v[e] = from_f<T>(f[e]);
+    __builtin_memcpy(p + i, v, sizeof v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e)
+      if (i + e < n) p[i + e] = from_f<T>(f[e]);
+  }
+}
+__device__ __forceinline__ void store_piece(void* p, int dtype, int64_t at, int i, int n, const float (&f)[kPiece]) {
+  if (dtype == MOE_F32) store_piece((float*)p + at, i, n, f);
+  else if (dtype == MOE_BF16) store_piece((bf16_t*)p + at, i, n, f);
+  else store_piece((f16_t*)p + at, i, n, f);
+}
+
+// Sum and maximum over the wave, the same in every lane: four steps inside rows of 16 lanes, then
+// lane 15 of a row into the next row and lane 31 into the upper half, and lane 63 has all.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t dpp0(uint32_t v) {   // 0 where no lane is read
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, 0xF, true);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp0(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp0<CTRL, ROWS>((uint32_t)b) |
+                                        (uint64_t)dpp0<CTRL, ROWS>((uint32_t)(b >> 32)) << 32);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+  v += dpp0<0x111, 0xF>(v);   // row_shr 1, 2, 4, 8
+  v += dpp0<0x112, 0xF>(v);
+  v += dpp0<0x114, 0xF>(v);
+  v += dpp0<0x118, 0xF>(v);
+  v += dpp0<0x142, 0xA>(v);   // row_bcast 15 into rows 1 and 3
+  v += dpp0<0x143, 0xC>(v);   // row_bcast 31 into rows 2 and 3
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)b, 63) |
+                                        (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), 63) << 32);
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  v = max(v, dpp0<0x111, 0xF>(v));
+  v = max(v, dpp0<0x112, 0xF>(v));
+  v = max(v, dpp0<0x114, 0xF>(v));
+  v = max(v, dpp0<0x118, 0xF>(v));
+  v = max(v, dpp0<0x142, 0xA>(v));
+  v = max(v, dpp0<0x143, 0xC>(v));
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+// Over the workgroup; `red` is used for one call only.
+template <int THREADS>
+__device__ __forceinline__ double row_sum(double v, double* red) {
+  v = wave_sum(v);
+  if constexpr (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) v += red[w];
+  }
   return v;
 }
-// The largest |y| of the row as its bits: they order like the values, infinities and NaNs above all.
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
-  for (int o = 32; o; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0;
-  for (int w = 0; w < kRowThreads / 64; ++w) v = max(v, red[w]);
-  __syncthreads();
+template <int THREADS>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+  v = wave_max(v);
+  if constexpr (THREADS > 64) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int w = 1; w < THREADS / 64; ++w) v = max(v, red[w]);
+  }
   return v;
 }
+// |y| as its bits: they order like the values, infinities and NaNs above all.
 __device__ __forceinline__ uint32_t abs_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
 
-// int8 row of the float32 values in LDS.
-__device__ __forceinline__ void write_i8_row(const float* y, int n, int8_t* q, float* scale, uint32_t* red) {
+__device__ __forceinline__ void codes8(const float (&y)[kPiece], const QScale& s, uint32_t (&q)[2]) {
+  const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+  q[0] = quant_pack4(lo, s);
+  q[1] = quant_pack4(hi, s);
+}
+
+// The int8 row of y.
+template <int THREADS, int C>
+__device__ __forceinline__ void write_i8_row(const float (&y)[C][kPiece], int n, int8_t* q, float* scale, uint32_t* red) {
   uint32_t m = 0;
-  for (int i = threadIdx.x; i < n; i += kRowThreads) m = max(m, abs_bits(y[i]));
-  m = block_max(m, red);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) m = max(m, abs_bits(y[c][e]));
+  m = row_max<THREADS>(m, red);
   const bool finite = m < 0x7F800000u;
   const QScale s = q_scale(__builtin_bit_cast(float, m));
-  for (int i = threadIdx.x; i < n; i += kRowThreads)
-    q[i] = finite && s.d != 0.0f ? (int8_t)quant_code(y[i], s) : (int8_t)0;
+  const bool codes = finite && s.d != 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = (c * THREADS + (int)threadIdx.x) * kPiece;
+    if (i >= n) break;
+    uint32_t v[2] = {0, 0};
+    if (codes) codes8(y[c], s, v);
+    if (i + kPiece <= n) {
+      __builtin_memcpy(q + i, v, 8);
+    } else {
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e)
+        if (i + e < n) q[i + e] = (int8_t)(v[e / 4] >> (8 * (e & 3)));
+    }
+  }
   if (threadIdx.x == 0) *scale = finite ? s.d : __builtin_nanf("");
 }
 
@@ -118,49 +220,115 @@ struct NormArgs {
   float eps;
 };
 
-// One workgroup a row, the row in LDS.
-template <typename T>
-__global__ __launch_bounds__(kRowThreads) void k_add_rmsnorm(NormArgs a) {
-  extern __shared__ float s_row[];
-  __shared__ double s_red[kRowThreads / 64];
-  __shared__ uint32_t s_redu[kRowThreads / 64];
+// The sum of squares and y are in 64 bits (y's one rounding to float32 then decides every code, whatever
+// the order of the sum): on this chip a 64-bit product costs what a 32-bit one does, and the row's bytes
+// take longer.
+template <typename T, int THREADS, int C>
+__global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
+  __shared__ double s_sum[THREADS / 64];
+  __shared__ uint32_t s_max[THREADS / 64];
   const int64_t row = blockIdx.x;
   const T* x = (const T*)a.x + row * a.ldx;
-  const T* res = a.res ? (const T*)a.res + row * a.ldres : nullptr;
+  const T* res = (const T*)a.res + row * a.ldres;
+  float r[C][kPiece], w[C][kPiece];
+#pragma unroll
+  for (int c = 0; c < C; ++c) load_piece(x, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, r[c]);
+  if (a.res) {
+    float s[C][kPiece];
+#pragma unroll
+    for (int c = 0; c < C; ++c) load_piece(res, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, s[c]);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) r[c][e] = to_f(from_f<T>(r[c][e] + s[c][e]));
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c) load_piece(a.weight, a.w_dtype, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, w[c]);
   double sum = 0.0;
-  for (int i = threadIdx.x; i < a.n; i += kRowThreads) {
-    T r = x[i];
-    if (res) r = from_f<T>(to_f(r) + to_f(res[i]));
-    if (a.res_out) ((T*)a.res_out)[row * a.ldro + i] = r;
-    const double d = (double)to_f(r);
-    s_row[i] = to_f(r);
-    sum += d * d;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) sum = __builtin_fma((double)r[c][e], (double)r[c][e], sum);
+  if (a.res_out) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      store_piece((T*)a.res_out + row * a.ldro, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, r[c]);
   }
-  sum = block_sum(sum, s_red);
+  sum = row_sum<THREADS>(sum, s_sum);
   const double rinv = 1.0 / __builtin_sqrt(sum / a.n + (double)a.eps);
-  for (int i = threadIdx.x; i < a.n; i += kRowThreads) {
-    const float y = (float)((double)s_row[i] * rinv * (double)load_f(a.weight, a.w_dtype, i));
-    s_row[i] = y;
-    if (a.y) store_f(a.y, a.y_dtype, row * a.ldy + i, y);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      const int i = (c * THREADS + (int)threadIdx.x) * kPiece + e;
+      const float y = (float)((double)r[c][e] * rinv * (double)w[c][e]);
+      r[c][e] = i < a.n ? y : 0.0f;   // past the row 0 * rinv * 0, where rinv may not be finite
+    }
+  if (a.y) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      store_piece(a.y, a.y_dtype, row * a.ldy, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, r[c]);
   }
-  __syncthreads();
-  if (a.q) write_i8_row(s_row, a.n, a.q + row * a.ldq, a.scale + row, s_redu);
-  if (a.q8_1) {
+  if (a.q8_1) {   // four threads a block of 32
     const int nb = a.n / 32;
-    for (int b = threadIdx.x; b < nb; b += kRowThreads) {
-      float v[32];
 #pragma unroll
-      for (int i = 0; i < 32; ++i) v[i] = s_row[32 * b + i];
-      const QBlock qb = quant_block(v);
-      uint32_t* o = (uint32_t*)((uint8_t*)a.q8_1 + 36 * (row * nb + b));
-      o[0] = qb.d16 | (qb.s16 << 16);
+    for (int c = 0; c < C; ++c) {
+      const int i = (c * THREADS + (int)threadIdx.x) * kPiece, part = threadIdx.x & 3;
+      float amax = 0.0f;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[1 + i] = qb.q[i];
+      for (int e = 0; e < kPiece; ++e) {
+        const float v = __builtin_fabsf(r[c][e]);
+        amax = v > amax ? v : amax;
+      }
+      float o = dpp<0xB1>(amax);   // quad_perm: the neighbour, then the other pair
+      amax = o > amax ? o : amax;
+      o = dpp<0x4E>(amax);
+      amax = o > amax ? o : amax;
+      const QScale qs = q_scale(amax);
+      uint32_t v[2] = {0, 0};
+      if (amax != 0.0f) codes8(r[c], qs, v);
+      int isum = 0;
+#pragma unroll
+      for (int e = 0; e < kPiece; ++e) isum += (int)(int8_t)(v[e / 4] >> (8 * (e & 3)));
+      isum += __builtin_amdgcn_update_dpp(0, isum, 0xB1, 0xF, 0xF, false);
+      isum += __builtin_amdgcn_update_dpp(0, isum, 0x4E, 0xF, 0xF, false);
+      if (i < a.n) {
+        uint32_t* blk = (uint32_t*)((uint8_t*)a.q8_1 + 36 * (row * nb + i / 32));
+        const uint32_t d16 = f2h(qs.d);
+        if (part == 0) blk[0] = d16 | (sum_field(d16, isum) << 16);
+        blk[1 + 2 * part] = v[0];
+        blk[2 + 2 * part] = v[1];
+      }
     }
   }
+  if (a.q) write_i8_row<THREADS, C>(r, a.n, a.q + row * a.ldq, a.scale + row, s_max);
 }
 
 // ------------------------------------------------------------------ SwiGLU ------------------
+
+// 1 / (1 + exp(-g)) within some 2^-45 relative: exp(-g) = 2^n 2^f with n = rint(t), t = -g log2(e), and
+// 2^f, |f| <= 1/2, by its power series to f^11 (the next term is below 2^-47); the reciprocal's seed takes
+// one Newton step. t is held to +-1000: beyond, the result times any two float32 values rounds as it
+// does there.
+__device__ __forceinline__ double sigmoid64(double g) {
+  const double t = __builtin_fmin(__builtin_fmax(g * -1.4426950408889634, -1000.0), 1000.0);
+  const double n = __builtin_rint(t), f = t - n;
+  double e = 4.44553827187081e-10;
+  e = __builtin_fma(e, f, 7.054911620801121e-09);
+  e = __builtin_fma(e, f, 1.0178086009239696e-07);
+  e = __builtin_fma(e, f, 1.3215486790144305e-06);
+  e = __builtin_fma(e, f, 1.5252733804059838e-05);
+  e = __builtin_fma(e, f, 0.00015403530393381606);
+  e = __builtin_fma(e, f, 0.0013333558146428441);
+  e = __builtin_fma(e, f, 0.009618129107628477);
+  e = __builtin_fma(e, f, 0.055504108664821576);
+  e = __builtin_fma(e, f, 0.2402265069591007);
+  e = __builtin_fma(e, f, 0.6931471805599453);
+  e = __builtin_fma(e, f, 1.0);
+  const double den = 1.0 + __builtin_ldexp(e, (int)n);
+  const double x = __builtin_amdgcn_rcp(den);
+  return __builtin_fma(__builtin_fma(-den, x, 1.0), x, x);
+}
 
 struct SwigluArgs {
   const void *g, *u;
@@ -170,19 +338,26 @@ struct SwigluArgs {
   int n;
 };
 
-template <typename T>
-__global__ __launch_bounds__(kRowThreads) void k_swiglu_i8(SwigluArgs a) {
-  extern __shared__ float s_row[];
-  __shared__ uint32_t s_redu[kRowThreads / 64];
+template <typename T, int THREADS, int C>
+__global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
+  __shared__ uint32_t s_max[THREADS / 64];
   const int64_t row = blockIdx.x;
-  const T* g = (const T*)a.g + row * a.ldg;
-  const T* u = (const T*)a.u + row * a.ldu;
-  for (int i = threadIdx.x; i < a.n; i += kRowThreads) {
-    const double gd = (double)to_f(g[i]);
-    s_row[i] = (float)(gd / (1.0 + exp(-gd)) * (double)to_f(u[i]));
+  const T* gp = (const T*)a.g + row * a.ldg;
+  const T* up = (const T*)a.u + row * a.ldu;
+  float g[C][kPiece], u[C][kPiece];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    load_piece(gp, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, g[c]);
+    load_piece(up, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, u[c]);
   }
-  __syncthreads();
-  write_i8_row(s_row, a.n, a.q + row * a.ldq, a.scale + row, s_redu);
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      const double gd = (double)g[c][e];
+      g[c][e] = (float)(gd * sigmoid64(gd) * (double)u[c][e]);
+    }
+  write_i8_row<THREADS, C>(g, a.n, a.q + row * a.ldq, a.scale + row, s_max);
 }
 
 // ------------------------------------------------------------------ router ------------------
@@ -514,6 +689,21 @@ bool overlap(const void* p, int64_t ldp, int sp, const void* q, int64_t ldq, int
   return a < b + nb && b < a + na;
 }
 
+// A row call's type and workgroup: by the row length alone, so that a row's sums have one order.
+template <typename F>
+void with_row(int dtype, int n, F f) {
+  auto size = [&](auto t) {
+    using std::integral_constant;
+    if (n <= 64 * kPiece) f(t, integral_constant<int, 64>{}, integral_constant<int, 1>{});
+    else if (n <= 256 * kPiece) f(t, integral_constant<int, 256>{}, integral_constant<int, 1>{});
+    else if (n <= 512 * kPiece) f(t, integral_constant<int, 256>{}, integral_constant<int, 2>{});
+    else if (n <= 1024 * kPiece) f(t, integral_constant<int, 512>{}, integral_constant<int, 2>{});
+    else f(t, integral_constant<int, 1024>{}, integral_constant<int, 2>{});
+  };
+  with_type(dtype, size);
+}
+static_assert(1024 * 2 * kPiece == MOE_MAX_ROW, "the longest row fits one workgroup");
+
 int launched(const char* what) {
   const hipError_t e = hipGetLastError();
   return e == hipSuccess ? MOE_OK : hip_fail(e, what);
@@ -577,8 +767,8 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
     if (overlap(in, ldi * sz, 1, q8_1, nb8, 1, rows, std::max<int>(n * sz, (int)nb8))) return MOE_E_ARG;
   }
   const NormArgs a{x, res, weight, res_out, yout, q8_1, q, scale, ldx, ldres, ldro, ldy, ldq, w_dtype, y_dtype, n, eps};
-  with_type(dtype, [&](auto t) {
-    hipLaunchKernelGGL(k_add_rmsnorm<decltype(t)>, dim3(rows), dim3(kRowThreads), n * 4, (hipStream_t)stream, a);
+  with_row(dtype, n, [&](auto t, auto threads, auto pieces) {
+    hipLaunchKernelGGL((k_add_rmsnorm<decltype(t), threads(), pieces()>), dim3(rows), dim3(threads()), 0, (hipStream_t)stream, a);
   });
   return launched("moe_add_rmsnorm");
 }
@@ -611,8 +801,8 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
   if (!aligned(g, sz) || !aligned(u, sz) || !aligned(scale, 4)) return MOE_E_ARG;
   if (overlap(g, ldg, sz, q, ldq, 1, rows, n) || overlap(u, ldu, sz, q, ldq, 1, rows, n)) return MOE_E_ARG;
   const SwigluArgs a{g, u, q, scale, ldg, ldu, ldq, n};
-  with_type(dtype, [&](auto t) {
-    hipLaunchKernelGGL(k_swiglu_i8<decltype(t)>, dim3(rows), dim3(kRowThreads), n * 4, (hipStream_t)stream, a);
+  with_row(dtype, n, [&](auto t, auto threads, auto pieces) {
+    hipLaunchKernelGGL((k_swiglu_i8<decltype(t), threads(), pieces()>), dim3(rows), dim3(threads()), 0, (hipStream_t)stream, a);
   });
   return launched("moe_swiglu_i8");
 }

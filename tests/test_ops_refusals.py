@@ -79,23 +79,21 @@ def test_binding_refuses_tensors_of_the_cpu():
     s = torch.zeros(2)
     for call in (lambda: B.moe_add_rmsnorm(x, torch.ones(64), 1e-6, y=x), lambda: B.moe_route_scores(x, 2),
                  lambda: B.moe_swiglu_i8(x, x, q, s), lambda: B.moe_matmul_i8(q, s, q, s)):
-        with pytest.raises(ValueError, match="not on the call's GPU"):
+        with pytest.raises(ValueError, match="not on a GPU"):
             call()
 
 
 def test_binding_refuses_shapes_types_and_strides():
-    x = torch.zeros(2, 64)
-    cuda = torch.device("cuda:0")
-    with pytest.raises(ValueError, match="shape"):
-        B._rows("call", "t", x, (2, 63), (torch.float32,), x.device)
-    with pytest.raises(ValueError, match="2-D"):
-        B._rows("call", "t", x[0], None, (torch.float32,), x.device)
-    with pytest.raises(ValueError, match="float32"):
-        B._rows("call", "t", x, None, (torch.int8,), x.device)
-    with pytest.raises(ValueError, match="on the call's GPU"):
-        B._rows("call", "t", x, None, (torch.float32,), cuda)
-    m = torch.zeros(64, 2, device="meta").t()
-    with pytest.raises(ValueError):
-        B._rows("call", "t", m, None, (torch.float32,), m.device)
-    with pytest.raises(ValueError, match="vector"):
-        B._vec("call", "t", torch.zeros(8)[::2], 4, (torch.float32,), torch.device("cpu"))
+    x = torch.zeros(2, 64)   # the checks themselves, with the CPU's index (-1) as the call's device
+    for want, t, shape, dtypes, device in (("shape", x, (2, 63), (torch.float32,), -1), ("rows", x[0], None, (torch.float32,), -1),
+                                           ("int8", x, None, (torch.int8,), -1), ("call's GPU", x, None, (torch.float32,), 0),
+                                           ("next to each other", x.t(), None, (torch.float32,), -1)):
+        with pytest.raises(ValueError, match=want):
+            B._rows("call", "t", t, shape, dtypes, device)
+    assert B._rows("call", "t", torch.zeros(3, 90)[:, 5:69], (3, 64), (torch.float32,), -1) == 90
+    assert B._rows("call", "t", torch.zeros(1, 64), None, (torch.float32,), -1) == 64
+    for t in (torch.zeros(8)[::2], torch.zeros(5), torch.zeros(4, dtype=torch.int32), torch.zeros(4, 1)):
+        with pytest.raises(ValueError, match="not contiguous"):
+            B._packed("call", "t", t, (4,), torch.float32, -1)
+    with pytest.raises(ValueError, match="call's GPU"):
+        B._packed("call", "t", torch.zeros(4), (4,), torch.float32, 0)
