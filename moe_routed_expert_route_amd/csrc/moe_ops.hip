@@ -677,6 +677,108 @@ __global__ __launch_bounds__(64 * WT * WC) void k_matmul_tile(MatmulArgs p) {
   else finish(f16_t{});
 }
 
+// Few tokens (M <= 16 MT): the weights are read once, straight into the lanes of the matrix
+// instruction, and a workgroup's W waves share out K, so that each has few dependent loads. C = 16 / P
+// channels a workgroup: with P > 1 (M <= C) the instruction's 16 rows are C channels at P neighbouring
+// pieces of K and its 16 columns the tokens at the same pieces; the blocks of its result where the
+// two pieces agree are partial sums of the product. Few channels then still fill the chip.
+template <int MT, int P, int W>
+__global__ __launch_bounds__(64 * W) void k_matmul_thin(MatmulArgs p) {
+  constexpr int C = 16 / P, PIECE = 128 * P, STRIDE = PIECE * W, UN = MT == 4 ? 2 : 4;
+  __shared__ i32x4 s_sum[W][MT][64];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int row = lane & 15, quad = lane >> 4, n0 = blockIdx.x * C;
+  const int8_t* b = p.b + (int64_t)min(n0 + row % C, p.N - 1) * p.ldb;
+  const int8_t* a[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) a[j] = p.a + (int64_t)min(16 * j + row % C, p.M - 1) * p.lda;
+  // what this thread stores at the end: channels on .. on + 3 of token om
+  const int outs = MT * C * C / 4, om = (int)threadIdx.x / (C / 4), on = n0 + 4 * ((int)threadIdx.x % (C / 4));
+  const bool mine = (int)threadIdx.x < outs && om < p.M && on < p.N;
+  float sa = 0.0f;
+  f32x4 sb = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (mine) {
+    sa = p.sa[om];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) sb[i] = p.sb[min(on + i, p.N - 1)];
+  }
+  i32x4 acc[MT];
+#pragma unroll
+  for (int j = 0; j < MT; ++j) acc[j] = i32x4{0, 0, 0, 0};
+  int k = wave * PIECE + (row / C) * 64 + quad * 16;   // this lane's 16 bytes; the next are 64 P on
+  int left = p.K - wave * PIECE;                       // bytes of K from the wave's piece on
+  for (; left >= PIECE + (UN - 1) * STRIDE; left -= UN * STRIDE) {
+    i32x4 bv[UN][2], av[UN][2][MT];
+#pragma unroll
+    for (int v = 0; v < UN; ++v)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int at = k + v * STRIDE + u * 64 * P;
+        bv[v][u] = any16(b + at);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) av[v][u][j] = any16(a[j] + at);
+      }
+#pragma unroll
+    for (int v = 0; v < UN; ++v)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[v][u], av[v][u][j], acc[j], 0, 0, 0);
+    k += UN * STRIDE;
+  }
+  for (; left >= PIECE; left -= STRIDE) {
+    i32x4 bv[2], av[2][MT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      bv[u] = any16(b + k + u * 64 * P);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) av[u][j] = any16(a[j] + k + u * 64 * P);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[u], av[u][j], acc[j], 0, 0, 0);
+    k += STRIDE;
+  }
+  if (left > 0) {   // the wave that K ends in: zeros past it
+    i32x4 bv[2], av[2][MT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      bv[u] = row16(b, k + u * 64 * P, p.K);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) av[u][j] = row16(a[j], k + u * 64 * P, p.K);
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bv[u], av[u][j], acc[j], 0, 0, 0);
+  }
+#pragma unroll
+  for (int j = 0; j < MT; ++j) s_sum[wave][j][lane] = acc[j];
+  __syncthreads();
+  if (!mine) return;
+  // rows 4 q .. 4 q + 3 of the result are with quad q: channel group g of piece s is rows s C + 4 g
+  const int j = om / 16, t = om % 16, g = (on - n0) / 4;
+  i32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+  for (int w = 0; w < W; ++w)
+#pragma unroll
+    for (int s = 0; s < P; ++s) sum += s_sum[w][j][(s * C / 4 + g) * 16 + s * C + t];
+  auto finish = [&](auto type) {
+    using T = decltype(type);
+    if (p.vec && on + 4 <= p.N) {
+      store_four<T>(p, om, on, sa, sb, sum);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (on + i < p.N) store_one<T>(p, om, on + i, sum[i]);
+    }
+  };
+  if (p.c_dtype == MOE_F32) finish(float{});
+  else if (p.c_dtype == MOE_BF16) finish(bf16_t{});
+  else finish(f16_t{});
+}
+
 // ------------------------------------------------------------------ host checks -------------
 
 bool aligned(const void* p, int size) { return ((uintptr_t)p & (uintptr_t)(size - 1)) == 0; }
@@ -730,6 +832,18 @@ int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
 int run_matmul(hipStream_t st, MatmulArgs p) {
   const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
+  if (p.M <= 64) {
+    auto go = [&](auto kern, int channels, int threads) {
+      hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)p.N + channels - 1) / channels)), dim3(threads), 0, st, p);
+      return launched("moe_matmul_i8");
+    };
+    // as few pieces of K side by side as leave two workgroups a CU
+    if (p.M <= 4 && p.N < 8 * 512) return go(k_matmul_thin<1, 4, 8>, 4, 512);
+    if (p.M <= 8 && p.N < 16 * 512) return go(k_matmul_thin<1, 2, 8>, 8, 512);
+    if (p.M <= 16) return go(k_matmul_thin<1, 1, 8>, 16, 512);
+    if (p.M <= 32) return go(k_matmul_thin<2, 1, 8>, 16, 512);
+    return go(k_matmul_thin<4, 1, 8>, 16, 512);
+  }
   const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
   const int64_t mid = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
   if (big >= 200) return launch_tile<256, 256, 4, 2>(st, p, direct);
