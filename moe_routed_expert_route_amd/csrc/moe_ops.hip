@@ -538,21 +538,48 @@ __device__ __forceinline__ void store_four(const MatmulArgs& p, int m, int n, fl
   *c = o;
 }
 
-constexpr int kMmK = 128;   // bytes of K per step
+// f(0), .., f(N - 1) with the numbers as types.
+template <int N, typename F>
+__device__ __forceinline__ void each(F f) {
+  if constexpr (N > 0) {
+    each<N - 1>(f);
+    f(std::integral_constant<int, N - 1>{});
+  }
+}
+
+// s_waitcnt vmcnt(n * PER), n at most MAX, uniform.
+template <int PER, int MAX>
+__device__ __forceinline__ void wait_loads(int n) {
+  static_assert(PER * MAX < 64, "vmcnt");
+  if constexpr (MAX == 0) __builtin_amdgcn_s_waitcnt(MOE_OPS_VM(0));
+  else if (n >= MAX) __builtin_amdgcn_s_waitcnt(MOE_OPS_VM(PER * MAX));
+  else wait_loads<PER, MAX - 1>(n);
+}
 
 // One workgroup a tile of BT tokens x BC channels, WT x WC waves. v_mfma_i32_16x16x64_i8 with the
 // channels as rows and the tokens as columns, so that a lane ends with four neighbouring channels of
-// one token. A ring of S stages in LDS holds BT + BC rows of 128 bytes, a row's 16-byte chunk c at
-// place c ^ (row & 7): the eight rows that eight lanes read at one chunk then sit in different banks.
-// DIRECT: rows and their stride are 16-byte aligned and go straight to LDS; else through registers. A
-// last piece of K below 128 bytes is taken first, through registers, zero past K.
-template <int BT, int BC, int WT, int WC, bool DIRECT>
-__global__ __launch_bounds__(64 * WT * WC) void k_matmul_tile(MatmulArgs p) {
+// one token. A stage in LDS holds BT + BC rows of BK bytes in 16-byte chunks, placed so that the eight
+// rows that eight lanes read at one chunk sit in different banks. KG groups of WT x WC waves take
+// neighbouring BK bytes of K each step and their sums meet at the end (small tiles: fewer, larger
+// steps). DIRECT: rows and their stride are 16-byte aligned; a ring of S stages takes them straight to
+// LDS, S - 1 steps ahead. Else through registers, S steps ahead, and two stages. A last piece of K below
+// a step is taken first, through registers, zero past K.
+// A step runs in groups of NT matrix instructions (one channel tile); beside each group go the fragment
+// read that the group after next needs and a share of the step's loads, so that neither the LDS nor the
+// memory pipe sees them all at once; the next step's first reads follow the barrier ahead of the last
+// two groups.
+template <int BT, int BC, int WT, int WC, int KG, int BK, bool DIRECT, int S>
+__global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p) {
   extern __shared__ __align__(16) uint8_t s_ring[];
-  constexpr int W = WT * WC, R = BT + BC, L = R / 8 / W;   // L: 8-row pieces a wave loads per step
-  constexpr int NT = BT / WT / 16, NC = BC / WC / 16, STAGE = R * kMmK;
-  static_assert(R % (8 * W) == 0 && BT % (16 * WT) == 0 && BC % (16 * WC) == 0 && NC >= 2, "tile split");
-  static_assert(2 * STAGE >= W * NC * 1024, "the epilogue's piece of each wave fits");
+  constexpr int W = WT * WC * KG, R = BT + BC, RP = 1024 / BK;   // RP: rows of a 1 KB piece, one load of a wave
+  constexpr int L = KG * R / RP / W;                             // pieces a wave loads per step
+  constexpr int NT = BT / WT / 16, NC = BC / WC / 16, KK = BK / 64, G = NC * KK;
+  constexpr int LG = G >= 16 ? 4 : G - 2;   // groups beside which a step's loads go
+  constexpr int STEP = KG * BK, STAGE = R * STEP, RING = DIRECT ? S : 2;
+  static_assert((BK == 64 || BK == 128) && KG * R % (RP * W) == 0 && R % RP == 0 && BT % (16 * WT) == 0 &&
+                BC % (16 * WC) == 0 && NC >= 2 && G % 4 == 0, "tile split");
+  static_assert(RING * STAGE >= W / KG * NC * 1024 && RING * STAGE >= (KG - 1) * (W / KG) * NC * NT * 1024,
+                "the epilogue's pieces fit");
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   // Workgroups go to the eight dies in turn: each die takes one run of tiles, in 4-token-tile strips, so
   // that what its workgroups read together is a near-square patch that its L2 holds.
@@ -565,95 +592,174 @@ __global__ __launch_bounds__(64 * WT * WC) void k_matmul_tile(MatmulArgs p) {
   const int hs = min(4, tiles_m - 4 * strip);
   const int m0 = (4 * strip + in % hs) * BT, n0 = (in / hs) * BC;
 
-  // this lane's rows: piece i of the wave is rows 8 (wave + W i) .. + 7 of the stage, tokens first
-  const int chunk = ((lane & 7) ^ (lane >> 3)) * 16;
-  const int8_t* src[L];
+  // place of a row's chunk: 128-byte rows c ^ (row & 7); 64-byte rows, two to 128 bytes, c ^ (row / 2 & 3)
+  auto place = [](int r, int c) { return BK == 128 ? c ^ (r & 7) : c ^ (r >> 1 & 3); };
+  // this lane's rows: piece q = wave + W i is rows RP (q % (R / RP)) .., tokens first, of K group q / (R / RP)
+  const int chunk = place(lane / (BK / 16), lane % (BK / 16)) * 16;
+  auto of_tokens = [&](int i) { return (wave + W * i) % (R / RP) < BT / RP; };   // else channels; the same in all lanes
+  auto column = [&](int i) { return (wave + W * i) / (R / RP) * BK + chunk; };
+  const int8_t *a0 = p.a + m0 * p.lda, *b0 = p.b + n0 * p.ldb;
+  using Offset = std::conditional_t<DIRECT, int, int64_t>;   // DIRECT: the tile's rows lie within 2^31 bytes
+  Offset off[L];
 #pragma unroll
   for (int i = 0; i < L; ++i) {
-    const int r = 8 * (wave + W * i) + (lane >> 3);
-    src[i] = (r < BT ? p.a + min(m0 + r, p.M - 1) * p.lda : p.b + min(n0 + r - BT, p.N - 1) * p.ldb) + chunk;
+    const int r = RP * ((wave + W * i) % (R / RP)) + lane / (BK / 16);
+    off[i] = (r < BT ? min(r, p.M - 1 - m0) * (Offset)p.lda : min(r - BT, p.N - 1 - n0) * (Offset)p.ldb) + column(i);
   }
-  const int rem = p.K % kMmK, steps = (p.K + kMmK - 1) / kMmK;
-  i32x4 hold[L];
-  auto fetch = [&](int t) {   // step t on its way to LDS, or to registers
+  const int8_t* src[DIRECT ? 1 : L];
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-      if constexpr (DIRECT)
-        __builtin_amdgcn_global_load_lds((const void*)src[i],
-                                         (MOE_LDS void*)(s_ring + (t & 1) * STAGE + 1024 * (wave + W * i)), 16, 0, 0);
-      else
-        hold[i] = any16(src[i]);
-      src[i] += kMmK;
-    }
-  };
-  auto put = [&](int t) {     // registers to LDS
-#pragma unroll
-    for (int i = 0; i < L; ++i) *(i32x4*)(s_ring + (t & 1) * STAGE + 1024 * (wave + W * i) + 16 * lane) = hold[i];
-  };
-  const int wt = wave % WT, wc = wave / WT, row = lane & 15, quad = lane >> 4;
-  i32x4 acc[NC][NT];
+  for (int i = 0; i < L && !DIRECT; ++i) src[i] = (of_tokens(i) ? a0 : b0) + off[i];
+  const int rem = p.K % STEP, steps = (p.K + STEP - 1) / STEP;
+  const int wt = wave % WT, wc = wave / WT % WC, kg = wave / (WT * WC), row = lane & 15, quad = lane >> 4;
+  i32x4 acc[NC][NT], av[4], bv[2][NT], hold[DIRECT ? 1 : S][L];
 #pragma unroll
   for (int i = 0; i < NC; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  auto compute = [&](int t) {
-    const uint8_t* st = s_ring + (t & 1) * STAGE;
-    i32x4 av[2][NC], bv[2][NT];
+  auto put = [&](int slot, int i, const i32x4& v) {   // a piece from registers to LDS
+    *(i32x4*)(s_ring + slot * STAGE + 1024 * (wave + W * i) + 16 * lane) = v;
+  };
+  // A piece of column k's step on its way to LDS. A buffer load, since the compiler takes a global load to
+  // LDS for one that the LDS counter counts too, and would then wait for every read in flight at each use.
+  const auto a_rows = __builtin_amdgcn_make_buffer_rsrc((void*)a0, 0, 0x7FFFFFFF, 0x00027000);
+  const auto b_rows = __builtin_amdgcn_make_buffer_rsrc((void*)b0, 0, 0x7FFFFFFF, 0x00027000);
+  auto send = [&](int slot, int i, int k) {
+    MOE_LDS void* to = (MOE_LDS void*)(s_ring + slot * STAGE + 1024 * (wave + W * i));
+    if (of_tokens(i)) __builtin_amdgcn_raw_ptr_buffer_load_lds(a_rows, to, 16, (int)off[i], k, 0, 0);
+    else __builtin_amdgcn_raw_ptr_buffer_load_lds(b_rows, to, 16, (int)off[i], k, 0, 0);
+  };
+  auto take = [&](int i, i32x4& v) {                  // the same to registers
+    v = any16(src[i]);
+    src[i] += STEP;
+  };
+  auto first = [&](int i) {                           // a piece of step 0 where K leaves one
+    return row16((of_tokens(i) ? a0 : b0) + (off[i] - column(i)), p.K - rem + column(i), p.K);
+  };
+  // the fragments that group g of the step in `slot` starts with; par: which of bv the step's first is
+  auto read = [&](int slot, auto par, int g) {
+    const int kk = g / NC, i = g % NC;
+    const uint8_t* st = s_ring + slot * STAGE + kg * R * BK + row * BK + place(row, 4 * kk + quad) * 16;
+    if (i == 0) {
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {
-      const int at = ((4 * kk + quad) ^ (row & 7)) * 16 + row * kMmK;
+      for (int j = 0; j < NT; ++j) bv[(par() + kk) & 1][j] = *(const i32x4*)(st + (wt * NT + j) * 16 * BK);
+    }
+    av[g & 3] = *(const i32x4*)(st + (BT + (wc * NC + i) * 16) * BK);
+  };
+  // One step. Its first two groups' fragments are read; `next` is the slot of step t + 1, `back` where the
+  // loads of step t + S - 1 go, h the registers that hold step t + 1's pieces. steady: the steps that the
+  // loads are for exist, so nothing is asked.
+  auto step = [&](int t, auto steady, int slot, int next, int back, auto par, i32x4 (&h)[L]) __attribute__((always_inline)) {
+    const bool more = steady() || t + 1 < steps, ahead = steady() || t + (DIRECT ? S - 1 : 1) < steps;
+    const bool later = steady() || t + 1 + S < steps;
+    const int k_ahead = (t + S - 1) * STEP - (rem ? STEP : 0);
 #pragma unroll
-      for (int j = 0; j < NT; ++j) bv[kk][j] = *(const i32x4*)(st + (wt * NT + j) * 16 * kMmK + at);
+    for (int g = 0; g < G; ++g) {
+      if (g < G - 2) read(slot, par, g + 2);
+      if (g == G - 2) {
+        if constexpr (DIRECT) wait_loads<L, S - 2>(steady() ? S - 2 : more ? steps - 2 - t : 0);   // step t + 1 has landed
+        ops_barrier();
+      }
+      if (g >= G - 2 && more) read(next, std::integral_constant<int, (par() + KK) & 1>{}, g + 2 - G);
+      if (g < LG && ahead) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) av[kk][i] = *(const i32x4*)(st + (BT + (wc * NC + i) * 16) * kMmK + at);
+        for (int i = g * L / LG; i < (g + 1) * L / LG; ++i) {
+          if constexpr (DIRECT) {
+            send(back, i, k_ahead);
+          } else {
+            put(next, i, h[i]);
+            if (later) take(i, h[i]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        acc[g % NC][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[g & 3], bv[(par() + g / NC) & 1][j], acc[g % NC][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // U steps hold whole rounds of stages, registers and parities
+  constexpr int U = S % 2 && (KK == 1 || !DIRECT) ? 2 * S : S;
+  auto round = [&](int t, auto steady, auto d) __attribute__((always_inline)) {
+    constexpr int D = d();
+    using Par = std::integral_constant<int, (D * KK) & 1>;
+    if constexpr (DIRECT) step(t, steady, D % S, (D + 1) % S, (D + S - 1) % S, Par{}, hold[0]);
+    else step(t, steady, D & 1, (D & 1) ^ 1, 0, Par{}, hold[(D + 1) % S]);
+  };
+  if constexpr (DIRECT) {
+    i32x4 v[L];
+    if (rem) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) v[i] = first(i);
     }
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk)
+    for (int t = 0; t < S - 1; ++t)
+      if (t < steps && !(t == 0 && rem)) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) send(t, i, t * STEP - (rem ? STEP : 0));
+      }
+    if (rem) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) put(0, i, v[i]);
+    }
+    wait_loads<L, S - 2>(steps - 1);
+  } else {   // hold[t % S] takes step t's pieces, from step 1 on; step 0 goes to LDS at once
+#pragma unroll
+    for (int i = 0; i < L; ++i) {
+      if (rem) hold[0][i] = first(i);
+      else take(i, hold[0][i]);
+    }
+#pragma unroll
+    for (int i = 0; i < L; ++i) put(0, i, hold[0][i]);
+#pragma unroll
+    for (int t = 1; t <= S; ++t)
+      if (t < steps) {
+#pragma unroll
+        for (int i = 0; i < L; ++i) take(i, hold[t % S][i]);
+      }
+  }
+  ops_barrier();
+  read(0, std::integral_constant<int, 0>{}, 0);
+  read(0, std::integral_constant<int, 0>{}, 1);
+  int t = 0;
+  for (; t + U + S < steps; t += U)
+    each<U>([&](auto d) __attribute__((always_inline)) { round(t + d(), std::true_type{}, d); });
+  for (; t < steps; t += U)
+    each<U>([&](auto d) __attribute__((always_inline)) {
+      if (t + d() < steps) round(t + d(), std::false_type{}, d);
+    });
+  if constexpr (KG > 1) {
+    i32x4* sums = (i32x4*)s_ring + (wave % (WT * WC)) * NC * NT * 64 + lane;
+    constexpr int GROUP = WT * WC * NC * NT * 64;
+    ops_barrier();
+    if (kg > 0) {
 #pragma unroll
       for (int i = 0; i < NC; ++i)
 #pragma unroll
-        for (int j = 0; j < NT; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(av[kk][i], bv[kk][j], acc[i][j], 0, 0, 0);
-    // reads two channel tiles ahead of the products that use them
-    __builtin_amdgcn_sched_group_barrier(0x100, NT + 2, 0);
-#pragma unroll
-    for (int s = 0; s < 2 * NC; ++s) {
-      __builtin_amdgcn_sched_group_barrier(0x008, NT, 0);
-      if (s < NC - 2 || (s >= NC && s < 2 * NC - 2)) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      if (s == NC - 2) __builtin_amdgcn_sched_group_barrier(0x100, NT / 2 + 1, 0);
-      if (s == NC - 1) __builtin_amdgcn_sched_group_barrier(0x100, NT - NT / 2 + 1, 0);
+        for (int j = 0; j < NT; ++j) sums[(kg - 1) * GROUP + (i * NT + j) * 64] = acc[i][j];
     }
-  };
-  if (rem) {
-#pragma unroll
-    for (int i = 0; i < L; ++i) hold[i] = row16(src[i] - chunk, p.K - rem + chunk, p.K);
-    put(0);
-  } else {
-    fetch(0);
-    if (!DIRECT) put(0);
-  }
-  for (int t = 0; t < steps; ++t) {
-    __builtin_amdgcn_s_waitcnt(MOE_OPS_VM(0));
     ops_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    if (t + 1 < steps) fetch(t + 1);
-    compute(t);
-    __builtin_amdgcn_sched_barrier(0);
-    if (!DIRECT && t + 1 < steps) put(t + 1);
+    if (kg > 0) return;
+#pragma unroll
+    for (int g = 0; g < KG - 1; ++g)
+#pragma unroll
+      for (int i = 0; i < NC; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] += sums[g * GROUP + (i * NT + j) * 64];
   }
   auto finish = [&](auto type) {
     using T = decltype(type);
     if (p.vec && m0 + BT <= p.M && n0 + BC <= p.N) {
+      const int m1 = m0 + wt * NT * 16 + row, n1 = n0 + wc * NC * 16 + 4 * quad;
+      float sa[NT];   // all scales before the first store: the compiler cannot move a load across one
+      f32x4 sb[NC];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const int m = m0 + (wt * NT + j) * 16 + row;
-        const float sa = p.sa[m];
+      for (int j = 0; j < NT; ++j) sa[j] = p.sa[m1 + 16 * j];
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          const int n = n0 + (wc * NC + i) * 16 + 4 * quad;
-          store_four<T>(p, m, n, sa, *(const f32x4*)(p.sb + n), acc[i][j]);
-        }
-      }
+      for (int i = 0; i < NC; ++i) sb[i] = *(const f32x4*)(p.sb + n1 + 16 * i);
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) store_four<T>(p, m1 + 16 * j, n1 + 16 * i, sa[j], sb[i], acc[i][j]);
     } else {   // ragged or unaligned: through the wave's piece of LDS, so that lanes write along a row
       ops_barrier();
       int* mine = (int*)(s_ring + wave * NC * 1024);
@@ -677,14 +783,14 @@ __global__ __launch_bounds__(64 * WT * WC) void k_matmul_tile(MatmulArgs p) {
   else finish(f16_t{});
 }
 
-// Few tokens (M <= 16 MT): the weights are read once, straight into the lanes of the matrix
+// Few tokens (M <= 16 MT, MT 1 or 2): the weights are read once, straight into the lanes of the matrix
 // instruction, and a workgroup's W waves share out K, so that each has few dependent loads. C = 16 / P
 // channels a workgroup: with P > 1 (M <= C) the instruction's 16 rows are C channels at P neighbouring
 // pieces of K and its 16 columns the tokens at the same pieces; the blocks of its result where the
 // two pieces agree are partial sums of the product. Few channels then still fill the chip.
 template <int MT, int P, int W>
 __global__ __launch_bounds__(64 * W) void k_matmul_thin(MatmulArgs p) {
-  constexpr int C = 16 / P, PIECE = 128 * P, STRIDE = PIECE * W, UN = MT == 4 ? 2 : 4;
+  constexpr int C = 16 / P, PIECE = 128 * P, STRIDE = PIECE * W, UN = 4;
   __shared__ i32x4 s_sum[W][MT][64];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int row = lane & 15, quad = lane >> 4, n0 = blockIdx.x * C;
@@ -811,28 +917,30 @@ int launched(const char* what) {
   return e == hipSuccess ? MOE_OK : hip_fail(e, what);
 }
 
-template <int BT, int BC, int WT, int WC>
+template <int BT, int BC, int WT, int WC, int KG, int BK, int S, int BK_HELD, int S_HELD>
 int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
   const int64_t tn = (p.N + BC - 1) / BC, tiles = tn * ((p.M + BT - 1) / BT);
   if (tiles > 0x7FFFFFFF) return MOE_E_SHAPE;
   p.tiles_n = (int)tn;
   p.tiles = (int)tiles;
-  constexpr int lds = 2 * (BT + BC) * kMmK;
-  auto go = [&](auto kern) {
+  auto go = [&](auto kern, int lds) {
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
       if (e != hipSuccess) return hip_fail(e, "moe_matmul_i8");
     }
-    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * WT * WC), lds, st, p);
+    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * WT * WC * KG), lds, st, p);
     return launched("moe_matmul_i8");
   };
-  return direct ? go(k_matmul_tile<BT, BC, WT, WC, true>) : go(k_matmul_tile<BT, BC, WT, WC, false>);
+  return direct ? go(k_matmul_tile<BT, BC, WT, WC, KG, BK, true, S>, S * (BT + BC) * KG * BK)
+                : go(k_matmul_tile<BT, BC, WT, WC, KG, BK_HELD, false, S_HELD>, 2 * (BT + BC) * KG * BK_HELD);
 }
 
 int run_matmul(hipStream_t st, MatmulArgs p) {
-  const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0;
+  const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
+                      std::max(p.lda, p.ldb) < (1 << 22);   // 256 rows and K within 2^31 bytes
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
-  if (p.M <= 64) {
+  // up to 32 tokens where K is short: 32 x 2560, K = 768 3.7 us, and 4.4 in tiles; K = 2560 10.8 and 7.3
+  if (p.M <= 16 || (p.M <= 32 && p.K <= 1024)) {
     auto go = [&](auto kern, int channels, int threads) {
       hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)p.N + channels - 1) / channels)), dim3(threads), 0, st, p);
       return launched("moe_matmul_i8");
@@ -841,14 +949,33 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
     if (p.M <= 4 && p.N < 8 * 512) return go(k_matmul_thin<1, 4, 8>, 4, 512);
     if (p.M <= 8 && p.N < 16 * 512) return go(k_matmul_thin<1, 2, 8>, 8, 512);
     if (p.M <= 16) return go(k_matmul_thin<1, 1, 8>, 16, 512);
-    if (p.M <= 32) return go(k_matmul_thin<2, 1, 8>, 16, 512);
-    return go(k_matmul_thin<4, 1, 8>, 16, 512);
+    return go(k_matmul_thin<2, 1, 8>, 16, 512);
   }
-  const int64_t big = (int64_t)((p.M + 255) / 256) * ((p.N + 255) / 256);
-  const int64_t mid = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
-  if (big >= 200) return launch_tile<256, 256, 4, 2>(st, p, direct);
-  if (mid >= 200) return launch_tile<128, 128, 2, 2>(st, p, direct);
-  return launch_tile<64, 64, 2, 2>(st, p, direct);
+  // A tile's cost is its time over K (the one measured: K = 2560, one round of up to 256 tiles, us) times
+  // the rounds that 256 CUs need. Small tiles bring the chip's CUs to a small product (512 x 1536: 64 x 64
+  // 8.2 us, 128 x 128 14.2, 256 x 256 34), large ones read less for each product of a large one (8192 x
+  // 1536: 256 x 256 51 us, 64 x 64 72).
+  struct Tile {
+    int bt, bc;
+    double us;
+  };
+  static constexpr Tile tiles[] = {{32, 32, 5.6}, {64, 32, 6.9}, {64, 64, 8.2}, {128, 64, 14}, {128, 128, 19.5}, {256, 128, 27.5}, {256, 256, 43}};
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < 7; ++i) {
+    const int64_t n = (int64_t)((p.M + tiles[i].bt - 1) / tiles[i].bt) * ((p.N + tiles[i].bc - 1) / tiles[i].bc);
+    const double cost = tiles[i].us * (double)((n + 255) / 256);
+    if (i == 0 || cost < least) best = i, least = cost;
+  }
+  switch (best) {
+    case 0: return launch_tile<32, 32, 2, 1, 2, 128, 4, 128, 2>(st, p, direct);
+    case 1: return launch_tile<64, 32, 4, 1, 2, 128, 3, 128, 2>(st, p, direct);
+    case 2: return launch_tile<64, 64, 2, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 3: return launch_tile<128, 64, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 4: return launch_tile<128, 128, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 5: return launch_tile<256, 128, 4, 2, 1, 128, 3, 128, 2>(st, p, direct);
+    default: return launch_tile<256, 256, 4, 2, 1, 128, 2, 64, 1>(st, p, direct);
+  }
 }
 
 }  // namespace moe
