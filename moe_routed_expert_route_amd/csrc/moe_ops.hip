@@ -746,33 +746,88 @@ __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p)
 #pragma unroll
         for (int j = 0; j < NT; ++j) acc[i][j] += sums[g * GROUP + (i * NT + j) * 64];
   }
-  auto finish = [&](auto type) {
+  // Scales first, all of them (the compiler cannot move a load across a store), then the tile in its type.
+  const int m1 = m0 + wt * NT * 16, n1 = n0 + wc * NC * 16;
+  const bool whole = p.vec && (n0 + BC <= p.N || p.N % 4 == 0);   // four channels are stored or none
+  float sa[NT];
+  f32x4 sb[NC];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) sa[j] = p.sa[min(m1 + 16 * j + row, p.M - 1)];
+#pragma unroll
+  for (int i = 0; i < NC; ++i) {
+    const int n = n1 + 16 * i + 4 * quad;
+    if (whole) {
+      sb[i] = *(const f32x4*)(p.sb + min(n, p.N - 4));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sb[i][e] = p.sb[min(n + e, p.N - 1)];
+    }
+  }
+  auto finish = [&](auto type) __attribute__((always_inline)) {
     using T = decltype(type);
-    if (p.vec && m0 + BT <= p.M && n0 + BC <= p.N) {
-      const int m1 = m0 + wt * NT * 16 + row, n1 = n0 + wc * NC * 16 + 4 * quad;
-      float sa[NT];   // all scales before the first store: the compiler cannot move a load across one
-      f32x4 sb[NC];
+    struct alignas(4 * sizeof(T)) T4 {
+      T v[4];
+    };
+    if (whole) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) sa[j] = p.sa[m1 + 16 * j];
+      for (int j = 0; j < NT; ++j) {
+        const int m = m1 + 16 * j + row;
+        if (m >= p.M) break;
+        T* c = (T*)p.c + m * p.ldc + n1 + 4 * quad;
+        T4 old[NC];
+        if (p.accumulate) {
 #pragma unroll
-      for (int i = 0; i < NC; ++i) sb[i] = *(const f32x4*)(p.sb + n1 + 16 * i);
+          for (int i = 0; i < NC; ++i)
+            if (n1 + 16 * i + 4 * quad < p.N) old[i] = *(const T4*)(c + 16 * i);
+        }
 #pragma unroll
-      for (int j = 0; j < NT; ++j)
+        for (int i = 0; i < NC; ++i) {
+          if (n1 + 16 * i + 4 * quad >= p.N) break;
+          T4 o;
 #pragma unroll
-        for (int i = 0; i < NC; ++i) store_four<T>(p, m1 + 16 * j, n1 + 16 * i, sa[j], sb[i], acc[i][j]);
+          for (int e = 0; e < 4; ++e) {
+            float v = (float)acc[i][j][e] * sa[j] * sb[i][e];
+            if (p.accumulate) v += to_f(old[i].v[e]);
+            o.v[e] = from_f<T>(v);
+          }
+          *(T4*)(c + 16 * i) = o;
+        }
+      }
     } else {   // ragged or unaligned: through the wave's piece of LDS, so that lanes write along a row
       ops_barrier();
-      int* mine = (int*)(s_ring + wave * NC * 1024);
+      constexpr int U4 = 4 * NC, PER = 4 * NC;   // four-value units of a row; values a lane stores for 16 tokens
+      float* mine = (float*)(s_ring + (wave % (WT * WC)) * NC * 1024);
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
 #pragma unroll
-        for (int i = 0; i < NC; ++i) *(i32x4*)(mine + row * 16 * NC + 16 * i + 4 * quad) = acc[i][j];
+        for (int i = 0; i < NC; ++i) {
+          f32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (float)acc[i][j][e] * sa[j] * sb[i][e];
+          *(f32x4*)(mine + 4 * (row * U4 + ((4 * i + quad) ^ (row & (U4 - 1))))) = v;
+        }
         __builtin_amdgcn_wave_barrier();
-        const int m1 = m0 + (wt * NT + j) * 16, n1 = n0 + wc * NC * 16;
 #pragma unroll 1
-        for (int e = lane; e < 256 * NC; e += 64) {
-          const int m = m1 + e / (16 * NC), n = n1 + e % (16 * NC);
-          if (m < p.M && n < p.N) store_one<T>(p, m, n, mine[e]);
+        for (int x0 = 0; x0 < PER; x0 += 8) {
+          float v[8];
+          T* c[8];
+          bool in[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int at = (x0 + x) * 64 + lane, r = at / (4 * U4), col = at % (4 * U4);
+            const int m = m1 + 16 * j + r, n = n1 + col;
+            in[x] = m < p.M && n < p.N;
+            c[x] = (T*)p.c + m * p.ldc + n;
+            v[x] = mine[4 * (r * U4 + ((col / 4) ^ (r & (U4 - 1)))) + col % 4];
+          }
+          if (p.accumulate) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              if (in[x]) v[x] += to_f(*c[x]);
+          }
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+            if (in[x]) *c[x] = from_f<T>(v[x]);
         }
         __builtin_amdgcn_wave_barrier();
       }
