@@ -374,7 +374,295 @@ struct RouteArgs {
 
 constexpr int kRouteE = 1024;
 
-// One wave a token; expert e sits in lane e % 64.
+// exp(x) to an ulp or two for x <= 709 (below -745: 0): x = n ln 2 + r, |r| <= ln(2) / 2, and e^r by its
+// power series to r^13 (the next term is below 2^-57).
+__device__ __forceinline__ double exp64(double x) {
+  const double n = __builtin_rint(__builtin_fmax(x, -1100.0) * 1.4426950408889634);
+  const double y = __builtin_fmax(x, -1100.0);
+  const double r = __builtin_fma(-n, 2.3190468138462996e-17, __builtin_fma(-n, 0.6931471805599453, y));
+  double e = 1.0 / 6227020800.0;
+  e = __builtin_fma(e, r, 1.0 / 479001600.0);
+  e = __builtin_fma(e, r, 1.0 / 39916800.0);
+  e = __builtin_fma(e, r, 1.0 / 3628800.0);
+  e = __builtin_fma(e, r, 1.0 / 362880.0);
+  e = __builtin_fma(e, r, 1.0 / 40320.0);
+  e = __builtin_fma(e, r, 1.0 / 5040.0);
+  e = __builtin_fma(e, r, 1.0 / 720.0);
+  e = __builtin_fma(e, r, 1.0 / 120.0);
+  e = __builtin_fma(e, r, 1.0 / 24.0);
+  e = __builtin_fma(e, r, 1.0 / 6.0);
+  e = __builtin_fma(e, r, 0.5);
+  e = __builtin_fma(e, r, 1.0);
+  e = __builtin_fma(e, r, 1.0);
+  return __builtin_ldexp(e, (int)n);
+}
+
+// A logit as the definition takes it: NaN as -infinity, at most the largest float32, no negative zero.
+__device__ __forceinline__ float route_logit(float l) {
+  return l != l ? -__builtin_inff() : __builtin_fminf(l, 3.40282347e38f) + 0.0f;
+}
+
+// Sorting keys: a 64-bit value whose last ten bits say which expert (0..1023), so that one maximum decides
+// value and tie: the lower expert is the larger key. A float32 logit leaves those bits empty; a 64-bit
+// score loses them, which the caller has to look after.
+__device__ __forceinline__ double key_of(double v, int e) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (b & ~(uint64_t)1023) | (uint64_t)((int64_t)b < 0 ? e : 1023 - e));
+}
+__device__ __forceinline__ int expert_of(double key) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, key);
+  return (int64_t)b < 0 ? (int)(b & 1023) : 1023 - (int)(b & 1023);
+}
+__device__ __forceinline__ uint64_t class_of(double key) { return __builtin_bit_cast(uint64_t, key) >> 10; }
+
+constexpr double kMaskedKey = -0x1p960;   // a masked expert of a kept group; every score is above (|c| <= 2^700)
+constexpr double kMostScore = 0x1p700;
+
+// Larger to a, smaller to b. The instructions themselves: the keys are never NaN, and the compiler's own
+// maximum would quiet its operands first.
+__device__ __forceinline__ double max64(double a, double b) {
+  double r;
+  asm("v_max_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ double min64(double a, double b) {
+  double r;
+  asm("v_min_f64 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ void exchange(double& a, double& b) {
+  const double m = max64(a, b);
+  b = min64(a, b);
+  a = m;
+}
+// A bitonic list of N into descending order.
+template <int N>
+__device__ __forceinline__ void bitonic(double* v) {
+  if constexpr (N > 1) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) exchange(v[i], v[i + N / 2]);
+    bitonic<N / 2>(v);
+    bitonic<N / 2>(v + N / 2);
+  }
+}
+// Any N values into descending order: the halves, then the second backwards after the first.
+template <int N>
+__device__ __forceinline__ void sort_down(double* v) {
+  if constexpr (N > 1) {
+    sort_down<N / 2>(v);
+    sort_down<N / 2>(v + N / 2);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) exchange(v[i], v[N - 1 - i]);
+    bitonic<N / 2>(v);
+    bitonic<N / 2>(v + N / 2);
+  }
+}
+// The N largest of two descending lists, descending.
+template <int N>
+__device__ __forceinline__ void merge_top(double* a, const double* b) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = max64(a[i], b[N - 1 - i]);
+  bitonic<N>(a);
+}
+
+// Lanes of a row of 16 in four steps: the neighbour, the other pair, the other quad, the other half.
+template <int CTRL>
+__device__ __forceinline__ double row_lane(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+template <int CTRL>
+__device__ __forceinline__ int row_lane(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <typename F>
+__device__ __forceinline__ void row_steps(F f) {
+  f(std::integral_constant<int, 0xB1>{});
+  f(std::integral_constant<int, 0x4E>{});
+  f(std::integral_constant<int, 0x141>{});
+  f(std::integral_constant<int, 0x140>{});
+}
+
+// 16 lanes a token, four tokens a wave; a lane keeps up to V neighbouring experts in registers, a group
+// (of 1, 2, 4, 8 or 16) in whole lanes, KL >= k. The lanes sort their keys, and four steps merge the
+// lists of KL: no step waits on a round of choosing. Without a bias the keys are exact (the logits). With
+// one they hold 42 of a score's 52 bits: where two of the chosen, or the last of them and one left out,
+// agree in those, the token is chosen again by whole scores, one expert at a time.
+template <int V, int KL>
+__global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
+  const int lane = threadIdx.x & 15, E = a.E, per = E / a.n_groups, lanes = 16 / a.n_groups, share = (per + lanes - 1) / lanes;
+  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 4), t = tok < T ? tok : T - 1;
+  const int group = lane / lanes, sub = lane % lanes, e0 = group * per + sub * share;
+  const int count = max(0, min(share, per - sub * share));
+  const bool softmax = a.score == MOE_SCORE_SOFTMAX, scored = a.bias || a.n_groups > 1;
+  float l[V];
+  {
+    auto load = [&](auto type) {
+      using Ty = decltype(type);
+      const Ty* p = (const Ty*)a.logits + t * a.ld;
+      constexpr int PIECE = V < 8 ? V : 8;
+#pragma unroll
+      for (int j0 = 0; j0 < V; j0 += PIECE) {
+        if (e0 + j0 + PIECE <= E) {
+          Ty v[PIECE];
+          __builtin_memcpy(v, p + e0 + j0, sizeof v);
+#pragma unroll
+          for (int j = 0; j < PIECE; ++j) l[j0 + j] = to_f(v[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < PIECE; ++j) l[j0 + j] = e0 + j0 + j < E ? to_f(p[e0 + j0 + j]) : 0.0f;
+        }
+      }
+    };
+    if (a.dtype == MOE_F32) load(float{});
+    else if (a.dtype == MOE_BF16) load(bf16_t{});
+    else load(f16_t{});
+  }
+  float peak = -__builtin_inff();
+#pragma unroll
+  for (int j = 0; j < V; ++j) {
+    l[j] = route_logit(l[j]);
+    if (j < count) peak = __builtin_fmaxf(peak, l[j]);
+  }
+  row_steps([&](auto c) { peak = __builtin_fmaxf(peak, dpp<c()>(peak)); });
+  double total = 1.0;   // softmax's sum, where it does not cancel
+  if (softmax && (scored || !a.renorm)) {
+    total = 0.0;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      if (j < count && l[j] > -__builtin_inff()) total += exp64((double)l[j] - (double)peak);
+    row_steps([&](auto c) { total += row_lane<c()>(total); });
+    if (total == 0.0) total = 1.0;
+  }
+  auto score = [&](float v) -> double {
+    if (!(v > -__builtin_inff())) return 0.0;
+    return softmax ? exp64((double)v - (double)peak) / total : 1.0 / (1.0 + exp64(-__builtin_fmax((double)v, -1000.0)));
+  };
+  auto biased = [&](int j) {   // c of the lane's expert j
+    return __builtin_fmin(__builtin_fmax(score(l[j]) + (double)a.bias[e0 + j], -kMostScore), kMostScore);
+  };
+  const double none = -__builtin_inf();   // not to be chosen
+  double key[V];
+  bool kept = true;
+  if (!scored) {
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+      key[j] = j >= count ? none : key_of(l[j] > -__builtin_inff() ? (double)l[j] : kMaskedKey, e0 + j);
+  } else {
+    double b0 = none, b1 = none;   // the lane's, then the group's two largest
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+      double c = none;
+      if (j < count && l[j] > -__builtin_inff()) c = a.bias ? biased(j) : score(l[j]);
+      b1 = max64(b1, min64(b0, c));
+      b0 = max64(b0, c);
+      const double v = c == none ? kMaskedKey : a.bias ? c + 0.0 : (double)l[j];
+      key[j] = j >= count ? none : key_of(v, e0 + j);
+    }
+    if (a.n_groups > 1) {
+      auto with = [&](auto c) {
+        const double o0 = row_lane<c()>(b0), o1 = row_lane<c()>(b1);
+        b1 = max64(min64(b0, o0), max64(b1, o1));
+        b0 = max64(b0, o0);
+      };
+      if (lanes >= 2) with(std::integral_constant<int, 0xB1>{});
+      if (lanes >= 4) with(std::integral_constant<int, 0x4E>{});
+      if (lanes >= 8) with(std::integral_constant<int, 0x141>{});
+      const double gs = a.top == 2 && b1 > none ? b0 + b1 : b0;
+      int ahead = 0;
+      for (int g = 1; g < a.n_groups; ++g) {
+        const int other = (lane + g * lanes) & 15;
+        const double o = __shfl(gs, ((int)threadIdx.x & 48) | other);
+        ahead += o > gs || (o == gs && other / lanes < group);
+      }
+      kept = ahead < a.keep;
+#pragma unroll
+      for (int j = 0; j < V; ++j) key[j] = kept ? key[j] : none;
+    }
+  }
+  double top[KL];
+  {
+    constexpr int N = V < KL ? V : KL;   // a list of KL from pieces of N
+#pragma unroll
+    for (int j0 = 0; j0 < V; j0 += N) {
+      double piece[KL];
+#pragma unroll
+      for (int j = 0; j < KL; ++j) piece[j] = j < N ? key[j0 + j] : none;
+      sort_down<N>(piece);
+      if (j0 == 0) {
+#pragma unroll
+        for (int j = 0; j < KL; ++j) top[j] = piece[j];
+      } else {
+        merge_top<KL>(top, piece);
+      }
+    }
+    row_steps([&](auto c) {
+      double other[KL];
+#pragma unroll
+      for (int j = 0; j < KL; ++j) other[j] = row_lane<c()>(top[j]);
+      merge_top<KL>(top, other);
+    });
+  }
+  double mine = top[0], last = top[0];
+  bool again = false;
+#pragma unroll
+  for (int j = 1; j < KL; ++j) {
+    if (lane == j) mine = top[j];
+    if (a.bias && j < a.k) {
+      again = again || (class_of(top[j]) == class_of(top[j - 1]) && top[j] > kMaskedKey / 2);
+      last = top[j];
+    }
+  }
+  int choice = expert_of(mine);
+  if (a.bias) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, last);
+    const double low = __builtin_bit_cast(double, (int64_t)b < 0 ? b | 1023 : b & ~(uint64_t)1023);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) n += key[j] >= low;
+    row_steps([&](auto c) { n += row_lane<c()>(n); });
+    again = again || (n > a.k && last > kMaskedKey / 2);
+    if (__any(again)) {
+#pragma unroll
+      for (int j = 0; j < V; ++j)
+        key[j] = !kept || j >= count ? none : l[j] > -__builtin_inff() ? biased(j) : kMaskedKey;
+#pragma unroll 1
+      for (int r = 0; r < a.k; ++r) {
+        double best = none;
+        int at = 1 << 20;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (key[j] > best) best = key[j], at = e0 + j;
+        row_steps([&](auto c) {
+          const double ob = row_lane<c()>(best);
+          const int oa = row_lane<c()>(at);
+          if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
+        });
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (e0 + j == at) key[j] = none;
+        if (lane == r) choice = at;
+      }
+    }
+  }
+  double s = 0.0;
+  if (lane < a.k) s = score(route_logit(load_f(a.logits, a.dtype, t * a.ld + choice)));
+  double sum = 1.0;
+  if (a.renorm) {
+    sum = s;
+    row_steps([&](auto c) { sum += row_lane<c()>(sum); });
+    if (sum == 0.0) sum = 1.0;
+  }
+  if (lane < a.k && tok < T) {
+    a.ids[tok * a.k + lane] = choice;
+    a.w[tok * a.k + lane] = (float)(s / sum * (double)a.factor);
+  }
+}
+
+// Any number of groups, up to 1024 experts and 32 choices: one wave a token, its scores in LDS; expert e
+// belongs to lane e % 64.
 __global__ __launch_bounds__(64) void k_route_scores(RouteArgs a) {
   __shared__ double s_c[kRouteE];        // scores to order by; -inf: masked
   __shared__ float s_l[kRouteE];         // logits as float32
@@ -386,8 +674,7 @@ __global__ __launch_bounds__(64) void k_route_scores(RouteArgs a) {
   const int64_t t = blockIdx.x;
   float peak = -__builtin_inff();
   for (int e = lane; e < E; e += 64) {
-    float l = load_f(a.logits, a.dtype, t * a.ld + e);
-    l = l != l ? -__builtin_inff() : __builtin_fminf(l, 3.40282347e38f);
+    const float l = route_logit(load_f(a.logits, a.dtype, t * a.ld + e));
     s_l[e] = l;
     peak = __builtin_fmaxf(peak, l);
   }
@@ -395,17 +682,18 @@ __global__ __launch_bounds__(64) void k_route_scores(RouteArgs a) {
   double total = 0.0;
   if (a.score == MOE_SCORE_SOFTMAX) {
     for (int e = lane; e < E; e += 64)
-      if (s_l[e] > -__builtin_inff()) total += exp((double)s_l[e] - (double)peak);
+      if (s_l[e] > -__builtin_inff()) total += exp64((double)s_l[e] - (double)peak);
     for (int o = 32; o; o >>= 1) total += __shfl_xor(total, o);
   }
   auto score = [&](float l) -> double {
     if (!(l > -__builtin_inff())) return 0.0;
-    return a.score == MOE_SCORE_SOFTMAX ? exp((double)l - (double)peak) / total : 1.0 / (1.0 + exp(-(double)l));
+    return a.score == MOE_SCORE_SOFTMAX ? exp64((double)l - (double)peak) / total
+                                        : 1.0 / (1.0 + exp64(-__builtin_fmax((double)l, -1000.0)));
   };
   for (int e = lane; e < E; e += 64) {
     const bool masked = !(s_l[e] > -__builtin_inff());
     double c = score(s_l[e]);
-    if (a.bias) c = fmin(fmax(c + (double)a.bias[e], -1e300), 1e300);
+    if (a.bias) c = __builtin_fmin(__builtin_fmax(c + (double)a.bias[e], -kMostScore), kMostScore);
     s_c[e] = masked ? -__builtin_inf() : c;
     s_alive[e] = 1;
   }
@@ -1083,7 +1371,16 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
       !aligned(w, 4))
     return MOE_E_ARG;
   const RouteArgs a{logits, bias, ids, w, ld, dtype, E, k, score, n_groups, keep_groups, group_top, renorm, factor};
-  hipLaunchKernelGGL(k_route_scores, dim3(T), dim3(64), 0, (hipStream_t)stream, a);
+  // Lists in registers where a group is whole lanes and a lane's share is up to 32 experts (16384 x 256: 6 us,
+  // and 118 by one wave a token).
+  const int lanes = 16 / n_groups, share = lanes ? (per + lanes - 1) / lanes : 0;
+  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)((T + 3ll) / 4)), dim3(64), 0, (hipStream_t)stream, a, T); };
+  if (!lanes || 16 % n_groups || share > 32 || k > 16)
+    hipLaunchKernelGGL(k_route_scores, dim3(T), dim3(64), 0, (hipStream_t)stream, a);
+  else if (k <= 8)
+    share <= 4 ? go(k_route_lists<4, 8>) : share <= 8 ? go(k_route_lists<8, 8>) : share <= 16 ? go(k_route_lists<16, 8>) : go(k_route_lists<32, 8>);
+  else
+    share <= 4 ? go(k_route_lists<4, 16>) : share <= 8 ? go(k_route_lists<8, 16>) : share <= 16 ? go(k_route_lists<16, 16>) : go(k_route_lists<32, 16>);
   return launched("moe_route_scores");
 }
 
