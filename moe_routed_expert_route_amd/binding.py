@@ -445,14 +445,10 @@ def _packed(what, name, t, shape, dtype, device):
                          "call's GPU")
 
 
-def _new_i8(like, rows, n):
-    q = like.new_empty((rows, (n + 15) // 16 * 16), dtype=torch.int8)
-    return (q if n % 16 == 0 else q[:, :n]), like.new_empty(rows, dtype=torch.float32)
-
-
 def i8_rows(rows, n, device="cuda"):
     """New int8 rows and their scales: q [rows, n] (rows 16-byte aligned), scale [rows] float32."""
-    return _new_i8(torch.empty(0, device=device), rows, n)
+    q = torch.empty((rows, (n + 15) // 16 * 16), dtype=torch.int8, device=device)
+    return (q if n % 16 == 0 else q[:, :n]), torch.empty(rows, dtype=torch.float32, device=device)
 
 
 def moe_add_rmsnorm(x, weight, eps, res=None, res_out=None, y=None, q=None, scale=None, q8_1=None, stream=None):
@@ -519,7 +515,7 @@ def moe_swiglu_i8(g, u, q=None, scale=None, stream=None):
     if (q is None) != (scale is None):
         raise ValueError(f"{what}: q and scale come together")
     if q is None:
-        q, scale = _new_i8(g, rows, n)
+        q, scale = i8_rows(rows, n, g.device)
         ldq = q.stride(0)
     else:
         ldq = _rows(what, "q", q, size, _INT8, dev)

@@ -86,7 +86,12 @@ __device__ __forceinline__ void load_piece(const T* p, int i, int n, float (&f)[
     for (int e = 0; e < kPiece; ++e) f[e] = to_f(v[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < kPiece; ++e) f[e] = i + e < n ? to_f(p[i + e]) : 0.0f;
+    for (int e = 0; e < kPiece; ++e) f[e] = 0.0f;
+    if (i < n) {
+#pragma unroll
+      for (int e = 0; e < kPiece - 1; ++e)
+        if (i + e < n) f[e] = to_f(p[i + e]);
+    }
   }
 }
 __device__ __forceinline__ void load_piece(const void* p, int dtype, int i, int n, float (&f)[kPiece]) {
@@ -101,9 +106,9 @@ __device__ __forceinline__ void store_piece(T* p, int i, int n, const float (&f)
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) v[e] = from_f<T>(f[e]);
     __builtin_memcpy(p + i, v, sizeof v);
-  } else {
+  } else if (i < n) {
 #pragma unroll
-    for (int e = 0; e < kPiece; ++e)
+    for (int e = 0; e < kPiece - 1; ++e)
       if (i + e < n) p[i + e] = from_f<T>(f[e]);
   }
 }
@@ -246,9 +251,11 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
   for (int c = 0; c < C; ++c) load_piece(a.weight, a.w_dtype, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, w[c]);
   double sum = 0.0;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if ((c * THREADS + (int)threadIdx.x) * kPiece >= a.n) break;   // whole waves, but for one
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) sum = __builtin_fma((double)r[c][e], (double)r[c][e], sum);
+  }
   if (a.res_out) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -257,13 +264,15 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
   sum = row_sum<THREADS>(sum, s_sum);
   const double rinv = 1.0 / __builtin_sqrt(sum / a.n + (double)a.eps);
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    const int i = (c * THREADS + (int)threadIdx.x) * kPiece;
+    if (i >= a.n) break;
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) {
-      const int i = (c * THREADS + (int)threadIdx.x) * kPiece + e;
       const float y = (float)((double)r[c][e] * rinv * (double)w[c][e]);
-      r[c][e] = i < a.n ? y : 0.0f;   // past the row 0 * rinv * 0, where rinv may not be finite
+      r[c][e] = i + e < a.n ? y : 0.0f;   // past the row 0 * rinv * 0, where rinv may not be finite
     }
+  }
   if (a.y) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -351,12 +360,14 @@ __global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
     load_piece(up, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, u[c]);
   }
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if ((c * THREADS + (int)threadIdx.x) * kPiece >= a.n) break;   // whole waves, but for one
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) {
       const double gd = (double)g[c][e];
       g[c][e] = (float)(gd * sigmoid64(gd) * (double)u[c][e]);
     }
+  }
   write_i8_row<THREADS, C>(g, a.n, a.q + row * a.ldq, a.scale + row, s_max);
 }
 
