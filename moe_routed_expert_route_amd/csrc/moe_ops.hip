@@ -175,24 +175,65 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
   }
   return v;
 }
-// |y| as its bits: they order like the values, infinities and NaNs above all.
-__device__ __forceinline__ uint32_t abs_bits(float y) { return __builtin_bit_cast(uint32_t, y) & 0x7FFFFFFFu; }
+// |y| goes as its bits: they order like the values, infinities and NaNs above all.
+// The largest |y| of a piece as bits, in two running maxima: of the bits as signed numbers (the positive
+// values) and as unsigned (the negative).
+struct AbsMax {
+  int pos = 0;
+  uint32_t neg = 0x80000000u;
+  __device__ __forceinline__ void add(const float (&y)[kPiece]) {
+#pragma unroll
+    for (int e = 0; e < kPiece; ++e) {
+      pos = max(pos, __builtin_bit_cast(int, y[e]));
+      neg = max(neg, __builtin_bit_cast(uint32_t, y[e]));
+    }
+  }
+  __device__ __forceinline__ uint32_t bits() const { return max((uint32_t)pos, neg & 0x7FFFFFFFu); }
+};
 
-__device__ __forceinline__ void codes8(const float (&y)[kPiece], const QScale& s, uint32_t (&q)[2]) {
-  const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
-  q[0] = quant_pack4(lo, s);
-  q[1] = quant_pack4(hi, s);
+// A float32 whose last mantissa bits are the integer nearest to x rd, and how far x rd is from it.
+constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23
+__device__ __forceinline__ float to_code(float x, float rd, float& off) {
+  const float y = __builtin_fmaf(x, rd, kMagic);
+  off = __builtin_fabsf(__builtin_fmaf(x, rd, kMagic - y));
+  return y;
+}
+__device__ __forceinline__ uint32_t low_bytes(const float (&y)[4]) {
+  const uint32_t a = __builtin_bit_cast(uint32_t, y[0]), b = __builtin_bit_cast(uint32_t, y[1]);
+  const uint32_t c = __builtin_bit_cast(uint32_t, y[2]), d = __builtin_bit_cast(uint32_t, y[3]);
+  return __builtin_amdgcn_perm(b, a, 0x0C0C0400u) | __builtin_amdgcn_perm(d, c, 0x04000C0Cu);
+}
+
+// The codes of eight values in a block of scale s (|y| <= amax), as the division gives them, mostly without it:
+// x rd is within 2^-16 of x / d (rcp is good to 1 ulp) and the rounded quotient within 2^-18, so that
+// where x rd is more than 2^-15 from every half-integer all three round alike; the sum and distance above are
+// exact to far less. Elsewhere (2^-13 is asked), and where the scale is out of range, the division.
+__device__ __forceinline__ void codes8(const float (&x)[kPiece], const QScale& s, uint32_t (&q)[2]) {
+#pragma unroll
+  for (int w = 0; w < 2; ++w) {
+    float y[4], most = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float off;
+      y[e] = to_code(x[4 * w + e], s.rd, off);
+      most = __builtin_fmaxf(most, off);
+    }
+    q[w] = low_bytes(y);
+    if (!s.ok || !(most < 0.5f - 0x1p-13f)) {
+      q[w] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[w] |= ((uint32_t)code_of(x[4 * w + e] / s.d) & 0xFFu) << (8 * e);
+    }
+  }
 }
 
 // The int8 row of y.
 template <int THREADS, int C>
 __device__ __forceinline__ void write_i8_row(const float (&y)[C][kPiece], int n, int8_t* q, float* scale, uint32_t* red) {
-  uint32_t m = 0;
+  AbsMax most;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int e = 0; e < kPiece; ++e) m = max(m, abs_bits(y[c][e]));
-  m = row_max<THREADS>(m, red);
+  for (int c = 0; c < C; ++c) most.add(y[c]);
+  const uint32_t m = row_max<THREADS>(most.bits(), red);
   const bool finite = m < 0x7F800000u;
   const QScale s = q_scale(__builtin_bit_cast(float, m));
   const bool codes = finite && s.d != 0.0f;
@@ -269,8 +310,12 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
     if (i >= a.n) break;
 #pragma unroll
     for (int e = 0; e < kPiece; ++e) {
-      const float y = (float)((double)r[c][e] * rinv * (double)w[c][e]);
-      r[c][e] = i + e < a.n ? y : 0.0f;   // past the row 0 * rinv * 0, where rinv may not be finite
+      r[c][e] = (float)((double)r[c][e] * rinv * (double)w[c][e]);
+    }
+    if (i + kPiece > a.n) {   // past the row 0 * rinv * 0, where rinv may not be finite
+#pragma unroll
+      for (int e = 1; e < kPiece; ++e)
+        if (i + e >= a.n) r[c][e] = 0.0f;
     }
   }
   if (a.y) {
