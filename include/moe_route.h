@@ -324,8 +324,9 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * are fastest). Row elements past the row length and rows past the last are neither read nor
  * written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
  * NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
- * as their outputs do not. Outputs may not overlap inputs unless a comment says so. Results do not
- * depend on the number of rows of the call: a row gives the same bits alone and among others.
+ * as their outputs do not. Outputs may not overlap inputs or each other unless a comment says so (rows of
+ * one buffer side by side, of one stride, do not). Results do not depend on the number of rows of the
+ * call: a row gives the same bits alone and among others.
  *
  * int8 rows ("i8"): a row of n float32 values y is kept as int8 codes q and one float32 scale d by
  * the q8_1 rule with the row as the block: d = max|y| / 127 (float32), q = clamp(round-half-away(
@@ -333,6 +334,7 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * NaN gives d = NaN and zero codes. The value a code stands for is q * d. */
 typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element types of rows */
 #define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
+#define MOE_MAX_ROWS 4194303      /* max rows of those and tokens of moe_route_scores (a launch's threads) */
 #define MOE_MAX_MATMUL_K 131071   /* max K of moe_matmul_i8: K * 128 * 128 stays below 2^31 */
 
 /* RMS norm with the residual's addition and outputs in 8 bits, beside moe_quantize_q8_1. Per row:
@@ -344,7 +346,8 @@ typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element 
  * (both or neither) = i8 rows of y, for moe_matmul_i8; q8_1 = q8_1 blocks of y, byte for byte
  * moe_quantize_q8_1 of the float32 y (rows of n/32 blocks, 4-byte aligned; n % 32 == 0), for
  * moe_prefill_gate_up. Errors: MOE_E_ARG (null or misaligned pointer, bad type, stride, eps not
- * finite and positive, overlap), MOE_E_SHAPE (n not in 1..MOE_MAX_ROW, or n % 32 with q8_1). */
+ * finite and positive, overlap), MOE_E_SHAPE (n not in 1..MOE_MAX_ROW, rows > MOE_MAX_ROWS, or n % 32
+ * with q8_1). */
 int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const void* res, int64_t ldres,
                     int w_dtype, const void* weight, float eps, int rows, int n, void* res_out,
                     int64_t ldro, int y_dtype, void* yout, int64_t ldy, int8_t* q, int64_t ldq, float* scale,
@@ -365,7 +368,8 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
  * counts as the largest finite float32. The selection is that of 64-bit arithmetic; w is float32.
  * logits [T][ld] in `dtype`; ids int32 [T][k], w float32 [T][k], as moe_build_plan and
  * moe_prefill_plan take them. 1 <= E <= 1024, n_groups <= 64 and a divisor of E, 1 <= k <= 32 and
- * k <= keep_groups * (E / n_groups), group_top <= E / n_groups; else MOE_E_ARG. */
+ * k <= keep_groups * (E / n_groups), group_top <= E / n_groups; else MOE_E_ARG (also a null or misaligned
+ * pointer, a bad stride, overlap); T > MOE_MAX_ROWS gives MOE_E_SHAPE. */
 typedef enum { MOE_SCORE_SOFTMAX = 1, MOE_SCORE_SIGMOID = 2 } moe_score;
 int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, int T, int E, int k, int score,
                      const float* bias, int n_groups, int keep_groups, int group_top, int renorm,
@@ -374,8 +378,8 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
 /* SwiGLU into i8 rows, beside moe_swiglu_q8_1: h = float32(g / (1 + exp(-g)) * u), evaluated in 64 bits
  * and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in `dtype` of strides ldg
  * and ldu (the two halves of one product's rows: u = g + n, both strides that product's).
- * Errors: MOE_E_ARG (null or misaligned pointer, bad type or stride), MOE_E_SHAPE (n not in
- * 1..MOE_MAX_ROW). */
+ * Errors: MOE_E_ARG (null or misaligned pointer, bad type or stride, overlap), MOE_E_SHAPE (n not in
+ * 1..MOE_MAX_ROW, rows > MOE_MAX_ROWS). */
 int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const void* u, int64_t ldu, int rows,
                   int n, int8_t* q, int64_t ldq, float* scale);
 
@@ -385,8 +389,8 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
  * the sum exact in 32-bit integers (codes -128..127), plus C's previous value when accumulate = 1
  * (one float32 sum, the routed experts' Y for example), rounded to c_dtype.
  * a [M][lda], b [N][ldb] (weights, one row a channel), sa [M], sb [N] float32, C [M][ldc]. M = 0 or N = 0 does
- * nothing. Errors: MOE_E_ARG (null or misaligned pointer, negative size, bad type or stride),
- * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K). */
+ * nothing. Errors: MOE_E_ARG (null or misaligned pointer, negative size, bad type or stride, overlap),
+ * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K, or a product past 2^32 threads of a launch). */
 int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb,
                   const float* sb, int M, int N, int K, int c_dtype, void* C, int64_t ldc, int accumulate);
 

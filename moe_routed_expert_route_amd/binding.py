@@ -399,10 +399,9 @@ _FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.
 
 # These calls can be a few microseconds long: the checks below ask each tensor for as little as they can,
 # pointers go to ctypes as plain numbers, and the stream comes without a Stream object.
-def _call(what, device, stream, *args):
-    """Enqueues on `stream` (default: the current one of the tensors' GPU `device`, an index), with that
-    GPU current."""
-    st = stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
+def _call(what, device, *args):
+    """Enqueues on the current stream of the tensors' GPU `device` (an index), with that GPU current."""
+    st = torch._C._cuda_getCurrentRawStream(device)
     fn = getattr(lib(), what)
     if torch.cuda.current_device() == device:
         rc = fn(st, *args)
@@ -411,6 +410,12 @@ def _call(what, device, stream, *args):
             rc = fn(st, *args)
     if rc:
         _check(rc, what)
+
+
+def _on(stream, f, *args):
+    """f(*args), and what it allocates, on `stream`."""
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def _gpu(what, name, t):
@@ -455,6 +460,8 @@ def moe_add_rmsnorm(x, weight, eps, res=None, res_out=None, y=None, q=None, scal
     """RMS norm of x (+ res) rows [rows, n] into the outputs given: res_out (the sum, may be x or
     res), y (float rows), q and scale (int8 rows), q8_1 (uint8 [rows, n / 32 * 36])."""
     what = "moe_add_rmsnorm"
+    if stream is not None:
+        return _on(stream, moe_add_rmsnorm, x, weight, eps, res, res_out, y, q, scale, q8_1)
     dev, size, same = _gpu(what, "x", x), x.shape, (x.dtype,)
     ldx = _rows(what, "x", x, None, _FLOATS, dev)
     rows, n = size
@@ -476,7 +483,7 @@ def moe_add_rmsnorm(x, weight, eps, res=None, res_out=None, y=None, q=None, scal
         if n % 32:
             raise ValueError(f"{what}: q8_1 rows need a multiple of 32 values, not {n}")
         _packed(what, "q8_1", q8_1, (rows, n // 32 * 36), torch.uint8, dev)
-    _call(what, dev, stream, _DTYPE[x.dtype], x.data_ptr(), ldx, res.data_ptr() if res is not None else 0, ldres,
+    _call(what, dev, _DTYPE[x.dtype], x.data_ptr(), ldx, res.data_ptr() if res is not None else 0, ldres,
           _DTYPE[weight.dtype], weight.data_ptr(), eps, rows, n, res_out.data_ptr() if res_out is not None else 0, ldro,
           y_type, y.data_ptr() if y is not None else 0, ldy, q.data_ptr() if q is not None else 0, ldq,
           scale.data_ptr() if scale is not None else 0, q8_1.data_ptr() if q8_1 is not None else 0)
@@ -486,6 +493,8 @@ def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep
                      factor=1.0, ids=None, w=None, stream=None):
     """The k experts of each token (int32 [T, k]) and their weights (float32 [T, k]) from logits [T, E]."""
     what = "moe_route_scores"
+    if stream is not None:
+        return _on(stream, moe_route_scores, logits, k, score, bias, n_groups, keep_groups, group_top, renorm, factor, ids, w)
     dev = _gpu(what, "logits", logits)
     ld = _rows(what, "logits", logits, None, _FLOATS, dev)
     T, E = logits.shape
@@ -499,7 +508,7 @@ def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep
         w = logits.new_empty((T, k), dtype=torch.float32)
     else:
         _packed(what, "w", w, (T, k), torch.float32, dev)
-    _call(what, dev, stream, _DTYPE[logits.dtype], logits.data_ptr(), ld, T, E, k, score,
+    _call(what, dev, _DTYPE[logits.dtype], logits.data_ptr(), ld, T, E, k, score,
           bias.data_ptr() if bias is not None else 0, n_groups, keep_groups, group_top, 1 if renorm else 0, factor,
           ids.data_ptr(), w.data_ptr())
     return ids, w
@@ -508,6 +517,8 @@ def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep
 def moe_swiglu_i8(g, u, q=None, scale=None, stream=None):
     """int8 rows (q, scale) of silu(g) * u for rows g, u [rows, n], each of its own row stride."""
     what = "moe_swiglu_i8"
+    if stream is not None:
+        return _on(stream, moe_swiglu_i8, g, u, q, scale)
     dev, size = _gpu(what, "g", g), g.shape
     ldg = _rows(what, "g", g, None, _FLOATS, dev)
     ldu = _rows(what, "u", u, size, (g.dtype,), dev)
@@ -520,7 +531,7 @@ def moe_swiglu_i8(g, u, q=None, scale=None, stream=None):
     else:
         ldq = _rows(what, "q", q, size, _INT8, dev)
         _packed(what, "scale", scale, (rows,), torch.float32, dev)
-    _call(what, dev, stream, _DTYPE[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu, rows, n, q.data_ptr(), ldq,
+    _call(what, dev, _DTYPE[g.dtype], g.data_ptr(), ldg, u.data_ptr(), ldu, rows, n, q.data_ptr(), ldq,
           scale.data_ptr())
     return q, scale
 
@@ -529,6 +540,8 @@ def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, s
     """C [M, N] (+)= (a [M, K] . b [N, K]^T) * sa [M] * sb [N] for int8 rows a, b; c, or a new tensor
     of `dtype`."""
     what = "moe_matmul_i8"
+    if stream is not None:
+        return _on(stream, moe_matmul_i8, a, sa, b, sb, c, dtype, accumulate)
     dev = _gpu(what, "a", a)
     lda, ldb = _rows(what, "a", a, None, _INT8, dev), _rows(what, "b", b, None, _INT8, dev)
     M, K = a.shape
@@ -543,7 +556,7 @@ def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, s
         c, ldc = a.new_empty((M, N), dtype=dtype), N
     else:
         dtype, ldc = c.dtype, _rows(what, "c", c, (M, N), _FLOATS, dev)
-    _call(what, dev, stream, a.data_ptr(), lda, sa.data_ptr(), b.data_ptr(), ldb, sb.data_ptr(), M, N, K, _DTYPE[dtype],
+    _call(what, dev, a.data_ptr(), lda, sa.data_ptr(), b.data_ptr(), ldb, sb.data_ptr(), M, N, K, _DTYPE[dtype],
           c.data_ptr(), ldc, 1 if accumulate else 0)
     return c
 

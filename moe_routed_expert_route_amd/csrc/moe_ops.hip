@@ -336,10 +336,11 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) {
       const int i = (c * THREADS + (int)threadIdx.x) * kPiece, part = threadIdx.x & 3;
-      float amax = 0.0f;
+      float amax = 0.0f, y[kPiece];
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) {
-        const float v = __builtin_fabsf(r[c][e]);
+        y[e] = r[c][e] == r[c][e] ? r[c][e] : 0.0f;   // the block quantizer gives a NaN code 0
+        const float v = __builtin_fabsf(y[e]);
         amax = v > amax ? v : amax;
       }
       float o = dpp<0xB1>(amax);   // quad_perm: the neighbour, then the other pair
@@ -348,7 +349,7 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
       amax = o > amax ? o : amax;
       const QScale qs = q_scale(amax);
       uint32_t v[2] = {0, 0};
-      if (amax != 0.0f) codes8(r[c], qs, v);
+      if (amax != 0.0f) codes8(y, qs, v);
       int isum = 0;
 #pragma unroll
       for (int e = 0; e < kPiece; ++e) isum += (int)(int8_t)(v[e / 4] >> (8 * (e & 3)));
@@ -1383,12 +1384,23 @@ __global__ __launch_bounds__(64 * W) void k_matmul_thin(MatmulArgs p) {
 
 bool aligned(const void* p, int size) { return ((uintptr_t)p & (uintptr_t)(size - 1)) == 0; }
 
-// Whether two sets of rows share a byte (their whole spans, padding included).
-bool overlap(const void* p, int64_t ldp, int sp, const void* q, int64_t ldq, int sq, int rows, int n) {
-  if (!p || !q) return false;
-  const uintptr_t a = (uintptr_t)p, b = (uintptr_t)q;
-  const uintptr_t na = (uintptr_t)(((rows - 1) * ldp + n) * sp), nb = (uintptr_t)(((rows - 1) * ldq + n) * sq);
-  return a < b + nb && b < a + na;
+// Rows in memory, in bytes: `rows` of `len`, `step` apart.
+struct Rows {
+  const void* p;
+  int64_t rows, len, step;
+};
+Rows rows_of(const void* p, int64_t rows, int64_t n, int64_t ld, int size) { return Rows{p, rows, n * size, ld * size}; }
+
+// Whether two sets of rows share a byte (for different steps: whether their spans do).
+bool overlap(const Rows& a, const Rows& b) {
+  if (!a.p || !b.p || !a.rows || !b.rows) return false;
+  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
+  if (pa >= pb + (uintptr_t)((b.rows - 1) * b.step + b.len) || pb >= pa + (uintptr_t)((a.rows - 1) * a.step + a.len))
+    return false;
+  if (a.step != b.step) return true;
+  const int64_t shift = (int64_t)((pb > pa ? pb - pa : pa - pb) % (uintptr_t)a.step);   // of the later rows' columns
+  const int64_t first = pb > pa ? a.len : b.len, second = pb > pa ? b.len : a.len;
+  return shift < first || shift + second > a.step;
 }
 
 // A row call's type and workgroup: by the row length alone, so that a row's sums have one order.
@@ -1415,7 +1427,7 @@ int launched(const char* what) {
 template <int BT, int BC, int WT, int WC, int KG, int BK, int S, int BK_HELD, int S_HELD>
 int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
   const int64_t tn = (p.N + BC - 1) / BC, tiles = tn * ((p.M + BT - 1) / BT);
-  if (tiles > 0x7FFFFFFF) return MOE_E_SHAPE;
+  if (tiles * 64 * WT * WC * KG > 0xFFFFFFFFll) return MOE_E_SHAPE;   // threads of a launch
   p.tiles_n = (int)tn;
   p.tiles = (int)tiles;
   auto go = [&](auto kern, int lds) {
@@ -1486,7 +1498,7 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
                     int y_dtype, void* yout, int64_t ldy, int8_t* q, int64_t ldq, float* scale, void* q8_1) {
   if (!type_ok(dtype) || !type_ok(w_dtype) || (yout && !type_ok(y_dtype)) || rows < 0) return MOE_E_ARG;
   if (!(eps > 0.0f) || !(eps < __builtin_inff())) return MOE_E_ARG;
-  if (n < 1 || n > MOE_MAX_ROW || (q8_1 && n % 32)) return MOE_E_SHAPE;
+  if (n < 1 || n > MOE_MAX_ROW || (q8_1 && n % 32) || rows > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !weight || !q != !scale || (!res_out && !yout && !q && !q8_1)) return MOE_E_ARG;
   if (ldx < n || (res && ldres < n) || (res_out && ldro < n) || (yout && ldy < n) || (q && ldq < n)) return MOE_E_ARG;
@@ -1495,12 +1507,15 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
       (yout && !aligned(yout, szy)) || !aligned(scale, 4) || !aligned(q8_1, 4))
     return MOE_E_ARG;
   const int64_t nb8 = (int64_t)n / 32 * 36;
-  for (int i = 0; i < 2; ++i) {   // outputs over inputs: r over x or res, the very same rows, and nothing else
-    const void* in = i ? res : x;
-    const int64_t ldi = i ? ldres : ldx;
-    if (!(in == res_out && ldi == ldro) && overlap(in, ldi, sz, res_out, ldro, sz, rows, n)) return MOE_E_ARG;
-    if (overlap(in, ldi, sz, yout, ldy, szy, rows, n) || overlap(in, ldi, sz, q, ldq, 1, rows, n)) return MOE_E_ARG;
-    if (overlap(in, ldi * sz, 1, q8_1, nb8, 1, rows, std::max<int>(n * sz, (int)nb8))) return MOE_E_ARG;
+  const Rows in[] = {rows_of(x, rows, n, ldx, sz), rows_of(res, rows, n, ldres, sz),
+                     rows_of(weight, 1, n, n, type_size(w_dtype))};
+  const Rows out[] = {rows_of(res_out, rows, n, ldro, sz), rows_of(yout, rows, n, ldy, szy), rows_of(q, rows, n, ldq, 1),
+                      rows_of(scale, 1, rows, rows, 4), rows_of(q8_1, rows, nb8, nb8, 1)};
+  for (int i = 0; i < 5; ++i) {
+    for (const Rows& r : in)   // r over x or res: the very same rows
+      if (!(i == 0 && r.p == out[0].p && r.step == out[0].step) && overlap(out[i], r)) return MOE_E_ARG;
+    for (int j = 0; j < i; ++j)
+      if (overlap(out[i], out[j])) return MOE_E_ARG;
   }
   const NormArgs a{x, res, weight, res_out, yout, q8_1, q, scale, ldx, ldres, ldro, ldy, ldq, w_dtype, y_dtype, n, eps};
   with_row(dtype, n, [&](auto t, auto threads, auto pieces) {
@@ -1518,10 +1533,13 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
   const int per = E / n_groups;
   if (k > keep_groups * per || group_top < 1 || group_top > 2 || group_top > per) return MOE_E_ARG;
   if ((renorm != 0 && renorm != 1) || !(factor == factor) || ld < E) return MOE_E_ARG;
+  if (T > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !w || !aligned(logits, type_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||
       !aligned(w, 4))
     return MOE_E_ARG;
+  const Rows out[] = {rows_of(ids, T, k, k, 4), rows_of(w, T, k, k, 4)}, in = rows_of(logits, T, E, ld, type_size(dtype));
+  if (overlap(out[0], in) || overlap(out[1], in) || overlap(out[0], out[1])) return MOE_E_ARG;
   const RouteArgs a{logits, bias, ids, w, ld, dtype, E, k, score, n_groups, keep_groups, group_top, renorm, factor};
   // Lists in registers where a group is whole lanes and a lane's share is up to 32 experts (16384 x 256: 10 us
   // by logits, 22 by scores in groups; 119 and 126 by one wave a token).
@@ -1539,12 +1557,15 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
 int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const void* u, int64_t ldu, int rows, int n,
                   int8_t* q, int64_t ldq, float* scale) {
   if (!type_ok(dtype) || rows < 0) return MOE_E_ARG;
-  if (n < 1 || n > MOE_MAX_ROW) return MOE_E_SHAPE;
+  if (n < 1 || n > MOE_MAX_ROW || rows > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (rows == 0) return MOE_OK;
   const int sz = type_size(dtype);
   if (!g || !u || !q || !scale || ldg < n || ldu < n || ldq < n) return MOE_E_ARG;
   if (!aligned(g, sz) || !aligned(u, sz) || !aligned(scale, 4)) return MOE_E_ARG;
-  if (overlap(g, ldg, sz, q, ldq, 1, rows, n) || overlap(u, ldu, sz, q, ldq, 1, rows, n)) return MOE_E_ARG;
+  const Rows out[] = {rows_of(q, rows, n, ldq, 1), rows_of(scale, 1, rows, rows, 4)};
+  for (const Rows& o : out)
+    if (overlap(o, rows_of(g, rows, n, ldg, sz)) || overlap(o, rows_of(u, rows, n, ldu, sz))) return MOE_E_ARG;
+  if (overlap(out[0], out[1])) return MOE_E_ARG;
   const SwigluArgs a{g, u, q, scale, ldg, ldu, ldq, n};
   with_row(dtype, n, [&](auto t, auto threads, auto pieces) {
     hipLaunchKernelGGL((k_swiglu_i8<decltype(t), threads(), pieces()>), dim3(rows), dim3(threads()), 0, (hipStream_t)stream, a);
@@ -1559,6 +1580,10 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
   if (M == 0 || N == 0) return MOE_OK;
   if (!a || !sa || !b || !sb || !C || lda < K || ldb < K || ldc < N) return MOE_E_ARG;
   if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(C, type_size(c_dtype))) return MOE_E_ARG;
+  const Rows c = rows_of(C, M, N, ldc, type_size(c_dtype));
+  if (overlap(c, rows_of(a, M, K, lda, 1)) || overlap(c, rows_of(b, N, K, ldb, 1)) || overlap(c, rows_of(sa, 1, M, M, 4)) ||
+      overlap(c, rows_of(sb, 1, N, N, 4)))
+    return MOE_E_ARG;
   return run_matmul((hipStream_t)stream, MatmulArgs{a, b, sa, sb, C, lda, ldb, ldc, M, N, K, accumulate, 0, 0, 0, c_dtype});
 }
 

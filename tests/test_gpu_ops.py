@@ -163,7 +163,26 @@ def test_norm_rows_of_zeros_infinities_and_nans():
         codes, scale = code_rule(yh[i:i + 1], 1)
         assert np.array_equal(q[i], codes[0]) and d[i] == scale[0]
     assert (np.abs(yh[5]) == 1).all()
-    assert torch.equal(blocks[[0, 1, 4, 5]], B.moe_quantize_q8_1(y)[[0, 1, 4, 5]])
+    assert torch.equal(blocks, B.moe_quantize_q8_1(y))
+    w[3] = float("nan")   # a NaN among finite values, in every row
+    w[4] = float("inf")
+    B.moe_add_rmsnorm(x, w, 1e-6, y=y, q8_1=blocks)
+    assert torch.equal(blocks, B.moe_quantize_q8_1(y))
+
+
+def test_norm_rows_side_by_side_in_one_buffer():
+    """x, its sum, float rows and int8 rows as column ranges of one buffer: no byte is shared."""
+    buf = torch.zeros((5, 512), device=DEV)
+    x, r, y = buf[:, :100], buf[:, 100:200], buf[:, 200:300]
+    q = buf.view(torch.int8)[:, 1200:1300]
+    x.copy_(randn((5, 100), F32, 15))
+    keep, d, w = x.clone(), torch.empty(5, device=DEV), randn((100,), F32, 16)
+    B.moe_add_rmsnorm(x, w, 1e-6, res_out=r, y=y, q=q, scale=d)
+    assert torch.equal(x, keep) and torch.equal(r, keep) and not buf[:, 325:].any()
+    codes, scale = code_rule(y.cpu().numpy(), 1)
+    assert np.array_equal(q.cpu().numpy(), codes) and np.array_equal(d.cpu().numpy(), scale)
+    with pytest.raises(RuntimeError, match="bad argument"):
+        B.moe_add_rmsnorm(x, w, 1e-6, y=buf[:, 50:150])
 
 
 # ------------------------------------------------------------------ router ----------------------
@@ -573,6 +592,20 @@ def test_block_captured_and_replayed(T):
         torch.cuda.synchronize()
         for got, w in zip(b.outputs(), want):
             assert torch.equal(got, w)
+
+
+def test_named_stream_allocates_there_too():
+    side = torch.cuda.Stream()
+    a, b, s = i8((40, 640), 92), i8((300, 640), 93), torch.ones(300, device=DEV)
+    want = B.moe_matmul_i8(a, s[:40], b, s)
+    torch.cuda.synchronize()
+    for _ in range(20):   # results of the side stream outlive work of the current one that could take their memory
+        got = B.moe_matmul_i8(a, s[:40], b, s, stream=side)
+        torch.full((40, 300), float("nan"), device=DEV)
+        side.synchronize()
+        assert torch.equal(got, want)
+        del got
+    assert torch.cuda.current_stream() != side
 
 
 def test_two_streams_at_once():

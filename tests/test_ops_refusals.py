@@ -37,7 +37,13 @@ BAD = [
     ("moe_add_rmsnorm", dict(n=63, q8_1=P4 + (1 << 20)), SHAPE), ("moe_add_rmsnorm", dict(q8_1=P4 + 2 + (1 << 20)), ARG),
     ("moe_add_rmsnorm", dict(res_out=P2 + 4), ARG), ("moe_add_rmsnorm", dict(res_out=P2, ldro=65), ARG),
     ("moe_add_rmsnorm", dict(y=P), ARG), ("moe_add_rmsnorm", dict(q=P + 100), ARG), ("moe_add_rmsnorm", dict(q8_1=P2 + 64), ARG),
-    ("moe_route_scores", dict(dtype=0), ARG), ("moe_route_scores", dict(T=-1), ARG), ("moe_route_scores", dict(E=0, ld=64), ARG),
+    ("moe_add_rmsnorm", dict(q=P4 + 64), ARG), ("moe_add_rmsnorm", dict(scale=P5 + 16), ARG), ("moe_add_rmsnorm", dict(y=P3), ARG),
+    ("moe_add_rmsnorm", dict(rows=1 << 22), SHAPE), ("moe_add_rmsnorm", dict(y=P2 + 128, ldy=32), ARG),
+    ("moe_add_rmsnorm", dict(x=P, ldx=128, y=P + 192, ldy=128), ARG), ("moe_add_rmsnorm", dict(x=P, ldx=128, y=P - 192, ldy=128), ARG),
+    ("moe_route_scores", dict(T=1 << 22), SHAPE), ("moe_route_scores", dict(ids=P + 64), ARG), ("moe_route_scores", dict(w=P3 + 64), ARG),
+    ("moe_swiglu_i8", dict(rows=1 << 22), SHAPE), ("moe_swiglu_i8", dict(scale=P3 + 8), ARG),
+    ("moe_matmul_i8", dict(c=P + 64), ARG), ("moe_matmul_i8", dict(c=P3 + 32), ARG), ("moe_matmul_i8", dict(c=P2 - 8), ARG),
+    ("moe_matmul_i8", dict(c=P4 + 64), ARG), ("moe_route_scores", dict(dtype=0), ARG), ("moe_route_scores", dict(T=-1), ARG), ("moe_route_scores", dict(E=0, ld=64), ARG),
     ("moe_route_scores", dict(E=1025, ld=2048, n_groups=1, keep=1), ARG), ("moe_route_scores", dict(k=0), ARG),
     ("moe_route_scores", dict(k=33), ARG), ("moe_route_scores", dict(k=9, keep=1), ARG), ("moe_route_scores", dict(score=0), ARG),
     ("moe_route_scores", dict(score=3), ARG), ("moe_route_scores", dict(n_groups=0), ARG), ("moe_route_scores", dict(n_groups=7), ARG),
