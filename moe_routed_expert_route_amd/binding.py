@@ -402,8 +402,8 @@ _FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.
 def _call(what, device, *args):
     """Enqueues on the current stream of the tensors' GPU `device` (an index), with that GPU current."""
     st = torch._C._cuda_getCurrentRawStream(device)
-    fn = getattr(lib(), what)
-    if torch.cuda.current_device() == device:
+    fn = getattr(_lib or lib(), what)
+    if torch._C._cuda_getDevice() == device:
         rc = fn(st, *args)
     else:
         with torch.cuda.device(device):
@@ -429,15 +429,17 @@ def _gpu(what, name, t):
 def _rows(what, name, t, shape, dtypes, device):
     """The row stride of t, checked to be rows (any stride, elements next to each other) of `shape` (None:
     any) and one of `dtypes` on GPU `device`."""
-    strides, size = t.stride(), t.shape
+    size = t.shape
     if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{what}: {name} has shape {tuple(size)}, not " + ("rows" if shape is None else str(tuple(shape))))
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: {name} is {t.dtype}, not one of {dtypes}")
     if t.get_device() != device:
         raise ValueError(f"{what}: {name} is on {t.device}, not on the call's GPU")
+    if t.is_contiguous():
+        return size[1]
     rows, n = size
-    ld, step = strides
+    ld, step = t.stride()
     if step != 1 and n > 1:
         raise ValueError(f"{what}: {name}'s row elements are not next to each other")
     return ld if rows > 1 or ld > n else n

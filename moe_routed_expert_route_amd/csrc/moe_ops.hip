@@ -1014,7 +1014,7 @@ __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p)
   constexpr int W = WT * WC * KG, R = BT + BC, RP = 1024 / BK;   // RP: rows of a 1 KB piece, one load of a wave
   constexpr int L = KG * R / RP / W;                             // pieces a wave loads per step
   constexpr int NT = BT / WT / 16, NC = BC / WC / 16, KK = BK / 64, G = NC * KK;
-  constexpr int LG = G >= 16 ? 4 : G - 2;   // groups beside which a step's loads go
+  constexpr int LG = G >= 16 ? 2 : G - 2;   // groups beside which a step's loads go
   constexpr int STEP = KG * BK, STAGE = R * STEP, RING = DIRECT ? S : 2;
   static_assert((BK == 64 || BK == 128) && KG * R % (RP * W) == 0 && R % RP == 0 && BT % (16 * WT) == 0 &&
                 BC % (16 * WC) == 0 && NC >= 2 && G % 4 == 0, "tile split");
@@ -1478,7 +1478,7 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
     case 0: return launch_tile<32, 32, 2, 1, 2, 128, 4, 128, 2>(st, p, direct);
     case 1: return launch_tile<64, 32, 4, 1, 2, 128, 3, 128, 2>(st, p, direct);
     case 2: return launch_tile<64, 64, 2, 2, 1, 128, 4, 128, 2>(st, p, direct);
-    case 3: return launch_tile<128, 64, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 3: return launch_tile<128, 64, 4, 2, 1, 128, 4, 128, 1>(st, p, direct);
     case 4: return launch_tile<128, 128, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
     case 5: return launch_tile<256, 128, 4, 2, 1, 128, 3, 128, 2>(st, p, direct);
     default: return launch_tile<256, 256, 4, 2, 1, 128, 2, 64, 1>(st, p, direct);
