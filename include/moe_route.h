@@ -336,6 +336,7 @@ typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element 
 #define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
 #define MOE_MAX_ROWS 4194303      /* max rows of those and tokens of moe_route_scores (a launch's threads) */
 #define MOE_MAX_MATMUL_K 131071   /* max K of moe_matmul_i8: K * 128 * 128 stays below 2^31 */
+#define MOE_MAX_MATMUL_MN 2147483136   /* max M and N: a tile past the last row still counts in 32 bits */
 
 /* RMS norm with the residual's addition and outputs in 8 bits, beside moe_quantize_q8_1. Per row:
  *   r = x + res, rounded to float32 and then to the type of x (r = x when res is NULL);
@@ -390,7 +391,8 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
  * (one float32 sum, the routed experts' Y for example), rounded to c_dtype.
  * a [M][lda], b [N][ldb] (weights, one row a channel), sa [M], sb [N] float32, C [M][ldc]. M = 0 or N = 0 does
  * nothing. Errors: MOE_E_ARG (null or misaligned pointer, negative size, bad type or stride, overlap),
- * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K, or a product past 2^32 threads of a launch). */
+ * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K, M or N above MOE_MAX_MATMUL_MN, or a product past 2^32
+ * threads of a launch: some 10^8 channels of up to 16 tokens, 10^11 values of C above). */
 int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb,
                   const float* sb, int M, int N, int K, int c_dtype, void* C, int64_t ldc, int accumulate);
 

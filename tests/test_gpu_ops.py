@@ -237,7 +237,9 @@ SIG, SOFT = B.SCORE_SIGMOID, B.SCORE_SOFTMAX
     (33, 7, 7, SOFT, True, 1, 1, 1, False), (65, 256, 8, SIG, True, 8, 4, 2, True), (5, 63, 32, SOFT, True, 1, 1, 1, True),
     (9, 160, 6, SOFT, False, 8, 3, 1, False), (130, 64, 4, SIG, True, 4, 2, 2, True), (3, 1024, 32, SIG, True, 64, 13, 2, True),
     (3, 1000, 10, SOFT, False, 1, 1, 1, False), (6, 65, 5, SOFT, True, 13, 2, 1, True), (2, 64, 32, SIG, True, 64, 40, 1, True),
-    (21, 192, 12, SIG, False, 3, 2, 2, False), (7, 320, 1, SOFT, True, 2, 1, 2, True)])
+    (21, 192, 12, SIG, False, 3, 2, 2, False), (7, 320, 1, SOFT, True, 2, 1, 2, True), (40, 512, 12, SIG, True, 1, 1, 1, True),
+    (17, 96, 16, SOFT, False, 1, 1, 1, False), (9, 64, 10, SIG, True, 4, 2, 2, True), (6, 128, 9, SOFT, True, 16, 5, 2, True),
+    (5, 500, 16, SOFT, True, 4, 1, 1, False), (11, 256, 11, SIG, False, 8, 3, 2, True), (3, 16, 16, SIG, True, 16, 16, 1, True)])
 def test_route(T, E, k, score, bias, groups, keep, top, renorm, dtype):
     logits = randn((T, E), dtype, T, E, k, scale=2.0)
     b = randn((E,), F32, E, 1, scale=0.1) if bias else None
@@ -262,20 +264,23 @@ def test_route_ties_go_to_the_lower_index(score, groups, keep, top):
     check_route(flat, 8, score, torch.full((64,), 0.25, device=DEV), groups, keep, top)
 
 
-def test_route_order_of_64_bits():
+@pytest.mark.parametrize("E,k", [(64, 8), (128, 12), (256, 8), (512, 16), (640, 8), (64, 20)])
+def test_route_order_of_64_bits(E, k):
     """Scores that float32 cannot tell apart: logits a step from each other, and biases that leave sums
-    apart by less than a float32 step, for either score."""
-    g = synth.rng(21)
+    apart by less than a float32 step, for either score; and equal scores with equal biases."""
+    g = synth.rng(21, E)
     base = np.float32(1.0 + g.random((40, 1)))
-    logits = (base + np.float32(2.0 ** -23) * g.permuted(np.tile(np.arange(64), (40, 1)), axis=1)).astype(np.float32)
+    logits = (base + np.float32(2.0 ** -23) * g.permuted(np.tile(np.arange(E), (40, 1)), axis=1)).astype(np.float32)
     lt = torch.from_numpy(logits).to(DEV)
-    bias = torch.from_numpy((0.5 + 2.0 ** -24 * g.permutation(64)).astype(np.float32)).to(DEV)
+    bias = torch.from_numpy((0.5 + 2.0 ** -24 * g.permutation(E)).astype(np.float32)).to(DEV)
     for score in (SIG, SOFT):
-        check_route(lt, 8, score)
-        check_route(lt, 8, score, bias)
-        check_route(lt, 8, score, bias, 8, 3, 2)
+        check_route(lt, k, score)
+        check_route(lt, k, score, bias)
+        check_route(lt, k, score, bias, 8, 3, 2)
+        check_route(lt.bfloat16(), k, score, torch.zeros_like(bias))
+        check_route(randn((40, E), BF16, E, 27, scale=2.0), k, score, torch.full_like(bias, 0.125), 4, 2, 2)
     # saturated sigmoids order by logit as long as no bias is given
-    check_route(lt * 30 + 40, 8, SIG)
+    check_route(lt * 30 + 40, k, SIG)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
@@ -408,7 +413,8 @@ SIZES = [(1, 1, 1), (1, 16, 64), (1, 17, 63), (2, 1536, 2560), (3, 100, 1000), (
          (7, 64, 8192), (8, 129, 512), (9, 640, 2560), (15, 128, 128), (16, 16, 16), (17, 257, 129), (31, 512, 640), (33, 31, 33),
          (48, 1000, 1001), (64, 1536, 2560), (65, 65, 65), (100, 2560, 768), (127, 129, 255), (128, 128, 128), (129, 300, 2048),
          (200, 640, 1111), (256, 256, 256), (257, 511, 384), (300, 1024, 1024), (509, 517, 523), (520, 2560, 768),
-         (4100, 3301, 200), (3330, 4096, 384), (2048, 6400, 129), (4096, 4096, 144), (700, 777, 130), (1030, 1536, 640), (2050, 513, 192), (1, 8200, 4096), (40, 4096, 97)]
+         (100, 2560, 256), (100, 2561, 255), (512, 1536, 256), (500, 1530, 250), (1024, 1536, 384), (1000, 1531, 383),
+         (2048, 1536, 320), (2000, 1533, 321), (4096, 1536, 256), (4090, 1531, 257), (4100, 3301, 200), (3330, 4096, 384), (2048, 6400, 129), (4096, 4096, 144), (700, 777, 130), (1030, 1536, 640), (2050, 513, 192), (1, 8200, 4096), (40, 4096, 97)]
 
 
 @pytest.mark.parametrize("M,N,K", SIZES)

@@ -42,6 +42,8 @@ BAD = [
     ("moe_add_rmsnorm", dict(x=P, ldx=128, y=P + 192, ldy=128), ARG), ("moe_add_rmsnorm", dict(x=P, ldx=128, y=P - 192, ldy=128), ARG),
     ("moe_route_scores", dict(T=1 << 22), SHAPE), ("moe_route_scores", dict(ids=P + 64), ARG), ("moe_route_scores", dict(w=P3 + 64), ARG),
     ("moe_swiglu_i8", dict(rows=1 << 22), SHAPE), ("moe_swiglu_i8", dict(scale=P3 + 8), ARG),
+    ("moe_matmul_i8", dict(N=2147483137, ldc=1 << 31), SHAPE), ("moe_matmul_i8", dict(M=2147483137), SHAPE),
+    ("moe_matmul_i8", dict(a=1 << 50, b=1 << 51, sa=1 << 52, sb=1 << 53, c=1 << 54, N=1 << 28, ldc=1 << 28), SHAPE),
     ("moe_matmul_i8", dict(c=P + 64), ARG), ("moe_matmul_i8", dict(c=P3 + 32), ARG), ("moe_matmul_i8", dict(c=P2 - 8), ARG),
     ("moe_matmul_i8", dict(c=P4 + 64), ARG), ("moe_route_scores", dict(dtype=0), ARG), ("moe_route_scores", dict(T=-1), ARG), ("moe_route_scores", dict(E=0, ld=64), ARG),
     ("moe_route_scores", dict(E=1025, ld=2048, n_groups=1, keep=1), ARG), ("moe_route_scores", dict(k=0), ARG),
