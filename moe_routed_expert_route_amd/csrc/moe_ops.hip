@@ -919,6 +919,7 @@ struct MatmulArgs {
   int M, N, K, accumulate;
   int tiles_n, tiles;   // tile grid: channels, all
   int vec;              // rows of C and sb take four-value accesses
+  int wide;             // 16-bit rows of C take 16-byte stores, and are only written
   int c_dtype;
 };
 
@@ -1213,7 +1214,30 @@ __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p)
     struct alignas(4 * sizeof(T)) T4 {
       T v[4];
     };
-    if (whole) {
+    constexpr int CHUNKS = 2 * NC, PITCH = 16 * CHUNKS + 16;   // 16-byte chunks of a row of the wave's 16-bit values
+    static_assert(RING * STAGE >= W / KG * 16 * PITCH, "the rows of 16-bit values fit");
+    if (sizeof(T) == 2 && p.wide) {   // through the wave's piece of LDS into whole lines
+      ops_barrier();
+      uint8_t* mine = s_ring + (wave % (WT * WC)) * 16 * PITCH;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+          T4 o;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o.v[e] = from_f<T>((float)acc[i][j][e] * sa[j] * sb[i][e]);
+          *(T4*)(mine + row * PITCH + 32 * i + 8 * quad) = o;
+        }
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int x = 0; x < 16 * CHUNKS / 64; ++x) {
+          const int at = x * 64 + lane, r = at / CHUNKS, c = at % CHUNKS, m = m1 + 16 * j + r, n = n1 + 8 * c;
+          const i32x4 v = *(const i32x4*)(mine + r * PITCH + 16 * c);
+          if (m < p.M && n < p.N) *(i32x4*)((T*)p.c + m * p.ldc + n) = v;
+        }
+        __builtin_amdgcn_wave_barrier();
+      }
+    } else if (whole) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
         const int m = m1 + 16 * j + row;
@@ -1452,6 +1476,7 @@ int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
 int run_matmul(hipStream_t st, MatmulArgs p) {
   const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
                       std::max(p.lda, p.ldb) < (1 << 22);   // 256 rows and K within 2^31 bytes
+  p.wide = type_size(p.c_dtype) == 2 && !p.accumulate && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % 8 == 0 && p.N % 8 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
   // up to 32 tokens where K is short: 32 x 2560, K = 768 3.7 us, and 4.4 in tiles; K = 2560 10.8 and 7.3
   if (p.M <= 16 || (p.M <= 32 && p.K <= 1024)) {
@@ -1593,7 +1618,7 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
   if (overlap(c, rows_of(a, M, K, lda, 1)) || overlap(c, rows_of(b, N, K, ldb, 1)) || overlap(c, rows_of(sa, 1, M, M, 4)) ||
       overlap(c, rows_of(sb, 1, N, N, 4)))
     return MOE_E_ARG;
-  return run_matmul((hipStream_t)stream, MatmulArgs{a, b, sa, sb, C, lda, ldb, ldc, M, N, K, accumulate, 0, 0, 0, c_dtype});
+  return run_matmul((hipStream_t)stream, MatmulArgs{a, b, sa, sb, C, lda, ldb, ldc, M, N, K, accumulate, 0, 0, 0, 0, c_dtype});
 }
 
 }  // extern "C"
