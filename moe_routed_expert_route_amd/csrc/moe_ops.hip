@@ -919,7 +919,7 @@ struct MatmulArgs {
   int M, N, K, accumulate;
   int tiles_n, tiles;   // tile grid: channels, all
   int vec;              // rows of C and sb take four-value accesses
-  int wide;             // 16-bit rows of C take 16-byte stores, and are only written
+  int wide;             // rows of C take 16-byte accesses, and 16-bit ones are only written
   int c_dtype;
 };
 
@@ -1007,13 +1007,16 @@ __device__ __forceinline__ void wait_loads(int n) {
 // memory pipe sees them all at once; the next step's first reads follow the barrier ahead of the last
 // two groups. The loads go beside the first two groups of a long step: spread over four or eight the large
 // tile took 2-7% more.
-// Measured (GPU time of a launch, inputs not in a cache): 8192 x 8192 x 4096 245 us (2250 TOPS; the matrix
-// instruction alone, from registers, 4240), x 8192 437 us (2510); zeros instead of random codes run 10%
-// faster, so power is part of the bound, LDS reads and writes (about 2000 of a 128-byte step's cycles, as
-// the matrix instructions) another. 512 x 1536 x 2560 8.5 us, 64 x 5120 x 2560 9.6: few steps whose loads
-// a CU takes at 50-75 GB/s. A tile 64 bytes of K deep and four stages: 270-280 us for the largest (each
-// line of memory twice); four waves of 128 x 128: 285; workgroups that go on to further tiles while C
-// is stored: 259.
+// C leaves in whole lines through LDS: straight from the lanes, in 32- or 64-byte parts of them, the largest
+// product took 245 us and 8192 x 2560 x 768 42 us instead of 34.
+// Measured (GPU time of a launch, inputs not in a cache): 8192 x 8192 x 4096 231 us (2380 TOPS; the matrix
+// instruction alone, from registers, 4240), x 8192 426 us (2580). A step takes 1.5 us where its matrix
+// instructions take 1.0 to 1.2, its loads 0.5 and its LDS reads 0.4: the barrier and the first reads after it
+// stand between; zeros instead of random codes run 10% faster, so power counts too. The rest is each tile's
+// first loads and C. 512 x 1536 x 2560 8.4 us, 64 x 5120 x 2560 9.5: a launch, a latency and few steps.
+// Slower for the largest: a tile 64 bytes of K deep in four stages (each line of memory twice; 270-280 us where
+// this took 250), four waves of 128 x 128 (285), workgroups that go on to further tiles while C is
+// stored (259), touching the lines of the step after next (262 where this took 244).
 template <int BT, int BC, int WT, int WC, int KG, int BK, bool DIRECT, int S>
 __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p) {
   extern __shared__ __align__(16) uint8_t s_ring[];
@@ -1214,29 +1217,47 @@ __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p)
     struct alignas(4 * sizeof(T)) T4 {
       T v[4];
     };
-    constexpr int CHUNKS = 2 * NC, PITCH = 16 * CHUNKS + 16;   // 16-byte chunks of a row of the wave's 16-bit values
-    static_assert(RING * STAGE >= W / KG * 16 * PITCH, "the rows of 16-bit values fit");
-    if (sizeof(T) == 2 && p.wide) {   // through the wave's piece of LDS into whole lines
+    // Wide rows of C go through the wave's piece of LDS into whole lines: HALVES parts of the channels, one
+    // after the other, of CHUNKS 16-byte chunks a row for 16 tokens.
+    constexpr int HALVES = sizeof(T) / 2, NP = NC / HALVES, CHUNKS = 2 * NC, PITCH = 16 * CHUNKS + 16, X = CHUNKS / 4;
+    static_assert(RING * STAGE >= W / KG * 16 * PITCH, "the rows fit");
+    if (p.wide) {
       ops_barrier();
       uint8_t* mine = s_ring + (wave % (WT * WC)) * 16 * PITCH;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
-          T4 o;
+        for (int h = 0; h < HALVES; ++h) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o.v[e] = from_f<T>((float)acc[i][j][e] * sa[j] * sb[i][e]);
-          *(T4*)(mine + row * PITCH + 32 * i + 8 * quad) = o;
+          for (int i = 0; i < NP; ++i) {
+            T4 o;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              o.v[e] = from_f<T>((float)acc[h * NP + i][j][e] * sa[j] * sb[h * NP + i][e]);
+            *(T4*)(mine + row * PITCH + (16 * i + 4 * quad) * sizeof(T)) = o;
+          }
+          __builtin_amdgcn_wave_barrier();
+          const int n = n1 + 16 * h * NP + 16 / (int)sizeof(T) * (lane % CHUNKS);   // 64 is a multiple of CHUNKS
+          i32x4 v[X];
+          i32x4* c[X];
+          bool in[X];
+#pragma unroll
+          for (int x = 0; x < X; ++x) {
+            const int r = (x * 64 + lane) / CHUNKS, m = m1 + 16 * j + r;
+            in[x] = m < p.M && n < p.N;
+            c[x] = (i32x4*)((T*)p.c + m * p.ldc + n);
+            v[x] = *(const i32x4*)(mine + r * PITCH + 16 * (lane % CHUNKS));
+          }
+          if (sizeof(T) == 4 && p.accumulate) {
+#pragma unroll
+            for (int x = 0; x < X; ++x)
+              if (in[x]) v[x] = __builtin_bit_cast(i32x4, __builtin_bit_cast(f32x4, v[x]) + *(const f32x4*)c[x]);
+          }
+#pragma unroll
+          for (int x = 0; x < X; ++x)
+            if (in[x]) *c[x] = v[x];
+          __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
-#pragma unroll
-        for (int x = 0; x < 16 * CHUNKS / 64; ++x) {
-          const int at = x * 64 + lane, r = at / CHUNKS, c = at % CHUNKS, m = m1 + 16 * j + r, n = n1 + 8 * c;
-          const i32x4 v = *(const i32x4*)(mine + r * PITCH + 16 * c);
-          if (m < p.M && n < p.N) *(i32x4*)((T*)p.c + m * p.ldc + n) = v;
-        }
-        __builtin_amdgcn_wave_barrier();
-      }
     } else if (whole) {
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
@@ -1476,7 +1497,8 @@ int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
 int run_matmul(hipStream_t st, MatmulArgs p) {
   const bool direct = aligned(p.a, 16) && aligned(p.b, 16) && p.lda % 16 == 0 && p.ldb % 16 == 0 &&
                       std::max(p.lda, p.ldb) < (1 << 22);   // 256 rows and K within 2^31 bytes
-  p.wide = type_size(p.c_dtype) == 2 && !p.accumulate && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % 8 == 0 && p.N % 8 == 0;
+  const int in16 = 16 / type_size(p.c_dtype);   // values of 16 bytes
+  p.wide = (in16 == 4 || !p.accumulate) && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % in16 == 0 && p.N % in16 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
   // up to 32 tokens where K is short: 32 x 2560, K = 768 3.7 us, and 4.4 in tiles; K = 2560 10.8 and 7.3
   if (p.M <= 16 || (p.M <= 32 && p.K <= 1024)) {
@@ -1500,7 +1522,7 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
     int bt, bc;
     double us;
   };
-  static constexpr Tile tiles[] = {{32, 32, 5.6}, {64, 32, 6.9}, {64, 64, 8.2}, {128, 64, 14}, {128, 128, 19.5}, {256, 128, 27.5}, {256, 256, 43}};
+  static constexpr Tile tiles[] = {{32, 32, 5.6}, {64, 32, 6.9}, {64, 64, 8.2}, {128, 64, 13.5}, {128, 128, 18.8}, {256, 128, 25.8}, {256, 256, 41}};
   int best = 0;
   double least = 0;
   for (int i = 0; i < 7; ++i) {
