@@ -608,39 +608,46 @@ __device__ __forceinline__ void merge_top(double* a, const double* b) {
   bitonic<N>(a);
 }
 
-// Lanes of a row of 16 in four steps: the neighbour, the other pair, the other quad, the other half.
-template <int CTRL>
-__device__ __forceinline__ double row_lane(double v) {
+// The value of the lane's partner in step STEP of a butterfly: the neighbour, the other pair, the other quad,
+// the other half of 16 lanes, the other 16 of 32, the other half.
+template <int STEP>
+__device__ __forceinline__ int partner(int v) {
+  if constexpr (STEP < 4) return __builtin_amdgcn_update_dpp(0, v, STEP == 0 ? 0xB1 : STEP == 1 ? 0x4E : STEP == 2 ? 0x141 : 0x140, 0xF, 0xF, false);
+  else return __shfl_xor(v, STEP == 4 ? 16 : 32);
+}
+template <int STEP>
+__device__ __forceinline__ float partner(float v) { return __builtin_bit_cast(float, partner<STEP>(__builtin_bit_cast(int, v))); }
+template <int STEP>
+__device__ __forceinline__ double partner(double v) {
   const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, false);
-  return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)partner<STEP>((int)(uint32_t)b) |
+                                        (uint64_t)(uint32_t)partner<STEP>((int)(uint32_t)(b >> 32)) << 32);
 }
-template <int CTRL>
-__device__ __forceinline__ int row_lane(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
-}
-template <typename F>
-__device__ __forceinline__ void row_steps(F f) {
-  f(std::integral_constant<int, 0xB1>{});
-  f(std::integral_constant<int, 0x4E>{});
-  f(std::integral_constant<int, 0x141>{});
-  f(std::integral_constant<int, 0x140>{});
+// f(step) for the steps that meet LANES lanes.
+template <int LANES, typename F>
+__device__ __forceinline__ void butterfly(F f) {
+  f(std::integral_constant<int, 0>{});
+  f(std::integral_constant<int, 1>{});
+  f(std::integral_constant<int, 2>{});
+  f(std::integral_constant<int, 3>{});
+  if constexpr (LANES == 64) {
+    f(std::integral_constant<int, 4>{});
+    f(std::integral_constant<int, 5>{});
+  }
 }
 
-// 16 lanes a token, four tokens a wave; a lane keeps up to V neighbouring experts in registers, a group
-// (of 1, 2, 4, 8 or 16) in whole lanes, KL >= k. The lanes sort their keys, and four steps merge the
+// LANES (16, four tokens a wave, or 64) lanes a token; a lane keeps up to V neighbouring experts in registers, a group
+// (of 1, 2, 4, 8 or 16) in whole lanes, KL >= k. The lanes sort their keys, and four (six) steps merge the
 // lists of KL: no step waits on a round of choosing. Without a bias the keys are exact (the logits). With
 // one they hold 42 of a score's 52 bits: where two of the chosen, or the last of them and one left out,
 // agree in those, the token is chosen again by whole scores, one expert at a time.
-// Measured: 16384 tokens of 256 bfloat16 logits 10 us, by sigmoid scores with a bias in 8 groups 22 us, 512
-// tokens of those 10.4 us: sixteen 64-bit scores a lane, about 5 us of it. float32 scores with 64 bits where
-// two are near: 7.7 us for 512 tokens without such, 9.7 with, 23 us for 16384 and 37 instead of 20 for 4096 x
-// 512 (registers).
-template <int V, int KL>
+// Measured: 16384 tokens of 256 bfloat16 logits 10 us, by sigmoid scores with a bias in 8 groups 22 us (sixteen
+// 64-bit scores a lane, about half of it), 512 tokens of those, 64 lanes each, 6.7 us. float32 scores with 64 bits
+// where two are near: 23 us for the 16384, and 37 instead of 20 for 4096 x 512 (registers).
+template <int V, int KL, int LANES>
 __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
-  const int lane = threadIdx.x & 15, E = a.E, per = E / a.n_groups, lanes = 16 / a.n_groups, share = (per + lanes - 1) / lanes;
-  const int64_t tok = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 4), t = tok < T ? tok : T - 1;
+  const int lane = threadIdx.x % LANES, E = a.E, per = E / a.n_groups, lanes = LANES / a.n_groups, share = (per + lanes - 1) / lanes;
+  const int64_t tok = (int64_t)blockIdx.x * (64 / LANES) + threadIdx.x / LANES, t = tok < T ? tok : T - 1;
   const int group = lane / lanes, sub = lane % lanes, e0 = group * per + sub * share;
   const int count = max(0, min(share, per - sub * share));
   const bool softmax = a.score == MOE_SCORE_SOFTMAX, scored = a.bias || a.n_groups > 1;
@@ -673,14 +680,22 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
     l[j] = route_logit(l[j]);
     if (j < count) peak = __builtin_fmaxf(peak, l[j]);
   }
-  row_steps([&](auto c) { peak = __builtin_fmaxf(peak, dpp<c()>(peak)); });
+  butterfly<LANES>([&](auto c) { peak = __builtin_fmaxf(peak, partner<c()>(peak)); });
   double total = 1.0;   // softmax's sum, where it does not cancel
   if (softmax && (scored || !a.renorm)) {
-    total = 0.0;
+    // Each term (at most 1) in multiples of 2^-26 and a rest in multiples of 2^-60: 1024 of either add up without
+    // rounding, so that the sum is the same however the experts lie in the lanes.
+    double coarse = 0.0, fine = 0.0;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-      if (j < count && l[j] > -__builtin_inff()) total += exp64((double)l[j] - (double)peak);
-    row_steps([&](auto c) { total += row_lane<c()>(total); });
+      if (j < count && l[j] > -__builtin_inff()) {
+        const double e = exp64((double)l[j] - (double)peak), big = (e + 0x1.8p26) - 0x1.8p26;
+        coarse += big;
+        fine += ((e - big) + 0x1.8p-8) - 0x1.8p-8;
+      }
+    butterfly<LANES>([&](auto c) { coarse += partner<c()>(coarse); });
+    butterfly<LANES>([&](auto c) { fine += partner<c()>(fine); });
+    total = coarse + fine;
     if (total == 0.0) total = 1.0;
   }
   const double part = inverse64(total);
@@ -712,18 +727,18 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
     }
     if (a.n_groups > 1) {
       auto with = [&](auto c) {
-        const double o0 = row_lane<c()>(b0), o1 = row_lane<c()>(b1);
+        const double o0 = partner<c()>(b0), o1 = partner<c()>(b1);
         b1 = max64(min64(b0, o0), max64(b1, o1));
         b0 = max64(b0, o0);
       };
-      if (lanes >= 2) with(std::integral_constant<int, 0xB1>{});
-      if (lanes >= 4) with(std::integral_constant<int, 0x4E>{});
-      if (lanes >= 8) with(std::integral_constant<int, 0x141>{});
+      butterfly<LANES>([&](auto c) {
+        if (lanes >= 2 << c()) with(c);
+      });
       const double gs = a.top == 2 && b1 > none ? b0 + b1 : b0;
       int ahead = 0;
       for (int g = 1; g < a.n_groups; ++g) {
-        const int other = (lane + g * lanes) & 15;
-        const double o = __shfl(gs, ((int)threadIdx.x & 48) | other);
+        const int other = (lane + g * lanes) % LANES;
+        const double o = __shfl(gs, (int)threadIdx.x - lane + other);
         ahead += o > gs || (o == gs && other / lanes < group);
       }
       kept = ahead < a.keep;
@@ -747,10 +762,10 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
         merge_top<KL>(top, piece);
       }
     }
-    row_steps([&](auto c) {
+    butterfly<LANES>([&](auto c) {
       double other[KL];
 #pragma unroll
-      for (int j = 0; j < KL; ++j) other[j] = row_lane<c()>(top[j]);
+      for (int j = 0; j < KL; ++j) other[j] = partner<c()>(top[j]);
       merge_top<KL>(top, other);
     });
   }
@@ -771,7 +786,7 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
     int n = 0;
 #pragma unroll
     for (int j = 0; j < V; ++j) n += key[j] >= low;
-    row_steps([&](auto c) { n += row_lane<c()>(n); });
+    butterfly<LANES>([&](auto c) { n += partner<c()>(n); });
     again = again || (n > a.k && last > kMaskedKey / 2);
     if (__any(again)) {
 #pragma unroll
@@ -784,9 +799,9 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
 #pragma unroll
         for (int j = 0; j < V; ++j)
           if (key[j] > best) best = key[j], at = e0 + j;
-        row_steps([&](auto c) {
-          const double ob = row_lane<c()>(best);
-          const int oa = row_lane<c()>(at);
+        butterfly<LANES>([&](auto c) {
+          const double ob = partner<c()>(best);
+          const int oa = partner<c()>(at);
           if (ob > best || (ob == best && oa < at)) best = ob, at = oa;
         });
 #pragma unroll
@@ -801,7 +816,7 @@ __global__ __launch_bounds__(64) void k_route_lists(RouteArgs a, int T) {
   double sum = 1.0;
   if (a.renorm) {
     sum = s;
-    row_steps([&](auto c) { sum += row_lane<c()>(sum); });
+    butterfly<LANES>([&](auto c) { sum += partner<c()>(sum); });
     if (sum == 0.0) sum = 1.0;
   }
   if (lane < a.k && tok < T) {
@@ -1599,14 +1614,28 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
   const RouteArgs a{logits, bias, ids, w, ld, dtype, E, k, score, n_groups, keep_groups, group_top, renorm, factor};
   // Lists in registers where a group is whole lanes and a lane's share is up to 32 experts (16384 x 256: 10 us
   // by logits, 22 by scores in groups; 119 and 126 by one wave a token).
-  const int lanes = 16 / n_groups, share = lanes ? (per + lanes - 1) / lanes : 0;
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)((T + 3ll) / 4)), dim3(64), 0, (hipStream_t)stream, a, T); };
-  if (!lanes || 16 % n_groups || share > 32 || k > 16)
+  // Few tokens of scored experts take 64 lanes each, which spread the scores' 64-bit arithmetic (the bits are the
+  // same: softmax's sum does not round): 512 x 256 10.4 -> 6.7 us, 2048 x 256 11.0 -> 8.1, 4096 x 256 11.6 -> 11.5;
+  // 1024 x 128 6.6 -> 5.9, 4096 x 128 7.3 -> 9.5; 512 x 64 5.0 -> 5.3.
+  const bool whole = n_groups <= 16 && 16 % n_groups == 0;
+  auto shares = [&](int lanes) { return whole ? (per + lanes / n_groups - 1) / (lanes / n_groups) : kRouteE; };
+  const bool wide = (bias || n_groups > 1) && shares(16) > 4 && T <= (shares(16) > 8 ? 2048 : 1024) && shares(64) <= 8;
+  const int share = shares(wide ? 64 : 16);
+  auto go = [&](auto kern, int tokens) {
+    hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)T + tokens - 1) / tokens)), dim3(64), 0, (hipStream_t)stream, a, T);
+  };
+  if (share > 32 || k > 16)
     hipLaunchKernelGGL(k_route_scores, dim3(T), dim3(64), 0, (hipStream_t)stream, a);
+  else if (wide && k <= 8)
+    share <= 4 ? go(k_route_lists<4, 8, 64>, 1) : go(k_route_lists<8, 8, 64>, 1);
+  else if (wide)
+    share <= 4 ? go(k_route_lists<4, 16, 64>, 1) : go(k_route_lists<8, 16, 64>, 1);
   else if (k <= 8)
-    share <= 4 ? go(k_route_lists<4, 8>) : share <= 8 ? go(k_route_lists<8, 8>) : share <= 16 ? go(k_route_lists<16, 8>) : go(k_route_lists<32, 8>);
+    share <= 4 ? go(k_route_lists<4, 8, 16>, 4) : share <= 8 ? go(k_route_lists<8, 8, 16>, 4)
+    : share <= 16 ? go(k_route_lists<16, 8, 16>, 4) : go(k_route_lists<32, 8, 16>, 4);
   else
-    share <= 4 ? go(k_route_lists<4, 16>) : share <= 8 ? go(k_route_lists<8, 16>) : share <= 16 ? go(k_route_lists<16, 16>) : go(k_route_lists<32, 16>);
+    share <= 4 ? go(k_route_lists<4, 16, 16>, 4) : share <= 8 ? go(k_route_lists<8, 16, 16>, 4)
+    : share <= 16 ? go(k_route_lists<16, 16, 16>, 4) : go(k_route_lists<32, 16, 16>, 4);
   return launched("moe_route_scores");
 }
 

@@ -246,6 +246,21 @@ def test_route(T, E, k, score, bias, groups, keep, top, renorm, dtype):
     check_route(logits, k, score, b, groups, keep, top, renorm, factor=1.0 if T % 2 else 2.5)
 
 
+@pytest.mark.parametrize("score", [SIG, SOFT])
+@pytest.mark.parametrize("E,k,groups", [(256, 8, 8), (200, 12, 1), (128, 8, 2), (512, 10, 16)])
+def test_route_few_tokens_and_among_many(E, k, groups, score):
+    """The bits of a token's choice do not depend on the call's tokens (which may take another kernel)."""
+    logits, b = randn((2600, E), F32, E, 28, scale=2.0), randn((E,), F32, E, 29, scale=0.05)
+    logits[5, ::3] = float("-inf")
+    for renorm in (True, False):
+        kw = dict(score=score, bias=b, n_groups=groups, keep_groups=max(1, groups // 2), group_top=2, renorm=renorm)
+        ids, w = B.moe_route_scores(logits, k, **kw)
+        for rows in (slice(0, 1), slice(3, 9), slice(0, 1000), slice(100, 2000)):
+            i, v = B.moe_route_scores(logits[rows], k, **kw)
+            assert torch.equal(i, ids[rows]) and torch.equal(v, w[rows])
+    check_route(logits[:40], k, score, b, groups, max(1, groups // 2), 2, False)
+
+
 def test_route_many_tokens_agree_with_the_softmax_router():
     logits = randn((3000, 128), F32, 20, scale=2.0)
     ids, w = B.moe_route_scores(logits, 8)
@@ -423,7 +438,9 @@ def test_matmul(M, N, K):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16, F16])
-@pytest.mark.parametrize("M,N,K", [(1, 130, 320), (6, 257, 511), (37, 300, 640), (130, 192, 256), (300, 515, 1000), (600, 1024, 512), (3400, 4100, 272)])
+@pytest.mark.parametrize("M,N,K", [(1, 130, 320), (6, 257, 511), (37, 300, 640), (130, 192, 256), (300, 515, 1000), (600, 1024, 512), (3400, 4100, 272),
+                                   (100, 2560, 256), (512, 1536, 256), (1024, 1536, 384), (2048, 1536, 320), (4096, 1536, 256),
+                                   (3330, 4096, 384), (500, 1532, 250)])
 def test_matmul_types_and_accumulation(M, N, K, dtype):
     a, b = i8((M, K), M, 50), i8((N, K), N, 51)
     check_matmul(a, b, dtype)
