@@ -414,6 +414,9 @@ def _call(what, device, *args):
 
 def _on(stream, f, *args):
     """f(*args), and what it allocates, on `stream`."""
+    device = args[0].get_device()
+    if device >= 0 and stream.device_index != device:
+        raise ValueError(f"{f.__name__}: the stream is of GPU {stream.device_index}, the tensors are on {device}")
     with torch.cuda.stream(stream):
         return f(*args)
 
@@ -432,6 +435,8 @@ def _rows(what, name, t, shape, dtypes, device):
     size = t.shape
     if len(size) != 2 or (shape is not None and size != shape):
         raise ValueError(f"{what}: {name} has shape {tuple(size)}, not " + ("rows" if shape is None else str(tuple(shape))))
+    if shape is None and (size[0] | size[1]) >> 31:
+        raise ValueError(f"{what}: {name} has shape {tuple(size)}, past 32 bits")
     if t.dtype not in dtypes:
         raise ValueError(f"{what}: {name} is {t.dtype}, not one of {dtypes}")
     if t.get_device() != device:
@@ -500,6 +505,8 @@ def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep
     dev = _gpu(what, "logits", logits)
     ld = _rows(what, "logits", logits, None, _FLOATS, dev)
     T, E = logits.shape
+    if not 0 < k <= E >= n_groups >= keep_groups > 0 < group_top <= E:
+        raise ValueError(f"{what}: k {k}, groups {n_groups}, {keep_groups} kept by {group_top}, of {E} experts")
     if bias is not None:
         _packed(what, "bias", bias, (E,), torch.float32, dev)
     if ids is None:

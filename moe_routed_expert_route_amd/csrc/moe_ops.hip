@@ -1583,8 +1583,8 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
   const Rows out[] = {rows_of(res_out, rows, n, ldro, sz), rows_of(yout, rows, n, ldy, szy), rows_of(q, rows, n, ldq, 1),
                       rows_of(scale, 1, rows, rows, 4), rows_of(q8_1, rows, nb8, nb8, 1)};
   for (int i = 0; i < 5; ++i) {
-    for (const Rows& r : in)   // r over x or res: the very same rows
-      if (!(i == 0 && r.p == out[0].p && r.step == out[0].step) && overlap(out[i], r)) return MOE_E_ARG;
+    for (int j = 0; j < 3; ++j)   // r over x or res: the very same rows
+      if (!(i == 0 && j < 2 && in[j].p == out[0].p && in[j].step == out[0].step) && overlap(out[i], in[j])) return MOE_E_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(out[i], out[j])) return MOE_E_ARG;
   }
@@ -1609,8 +1609,11 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
   if (!logits || !ids || !w || !aligned(logits, type_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||
       !aligned(w, 4))
     return MOE_E_ARG;
-  const Rows out[] = {rows_of(ids, T, k, k, 4), rows_of(w, T, k, k, 4)}, in = rows_of(logits, T, E, ld, type_size(dtype));
-  if (overlap(out[0], in) || overlap(out[1], in) || overlap(out[0], out[1])) return MOE_E_ARG;
+  const Rows out[] = {rows_of(ids, T, k, k, 4), rows_of(w, T, k, k, 4)};
+  const Rows in[] = {rows_of(logits, T, E, ld, type_size(dtype)), rows_of(bias, 1, E, E, 4)};
+  if (overlap(out[0], out[1])) return MOE_E_ARG;
+  for (const Rows& r : in)
+    if (overlap(out[0], r) || overlap(out[1], r)) return MOE_E_ARG;
   const RouteArgs a{logits, bias, ids, w, ld, dtype, E, k, score, n_groups, keep_groups, group_top, renorm, factor};
   // Lists in registers where a group is whole lanes and a lane's share is up to 32 experts (16384 x 256: 10 us
   // by logits, 22 by scores in groups; 119 and 126 by one wave a token).

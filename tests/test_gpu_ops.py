@@ -617,6 +617,14 @@ def test_block_captured_and_replayed(T):
             assert torch.equal(got, w)
 
 
+def test_router_counts_are_refused_before_they_lose_bits():
+    l = randn((2, 8), F32, 17)
+    for bad in (dict(k=0), dict(k=9), dict(k=(1 << 32) + 1), dict(k=1, n_groups=(1 << 32) + 1), dict(k=1, n_groups=2, keep_groups=3),
+                dict(k=1, group_top=(1 << 32) + 1), dict(k=1, keep_groups=0)):
+        with pytest.raises(ValueError, match="of 8 experts"):
+            B.moe_route_scores(l, **bad)
+
+
 def test_named_stream_allocates_there_too():
     side = torch.cuda.Stream()
     a, b, s = i8((40, 640), 92), i8((300, 640), 93), torch.ones(300, device=DEV)

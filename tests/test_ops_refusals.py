@@ -105,3 +105,17 @@ def test_binding_refuses_shapes_types_and_strides():
             B._packed("call", "t", t, (4,), torch.float32, -1)
     with pytest.raises(ValueError, match="call's GPU"):
         B._packed("call", "t", torch.zeros(4), (4,), torch.float32, 0)
+
+
+@pytest.mark.parametrize("name,change", [
+    ("moe_add_rmsnorm", dict(rows=1, res_out=P3)),                       # the weight's row is not the residual's
+    ("moe_route_scores", dict(ids=P2)), ("moe_route_scores", dict(w=P2 + 128)),   # over the bias
+])
+def test_refuses_outputs_over_the_weight_and_the_bias(name, change):
+    assert getattr(B.lib(), name)(None, *dict(CALLS[name], **change).values()) == ARG
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    for shape in ((1 << 31, 1), (1, (1 << 32) + 16)):   # of no memory: one element, expanded
+        with pytest.raises(ValueError, match="past 32 bits"):
+            B._rows("call", "t", torch.zeros(1, 1).expand(shape), None, (torch.float32,), -1)
