@@ -391,8 +391,9 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
  * (one float32 sum, the routed experts' Y for example), rounded to c_dtype.
  * a [M][lda], b [N][ldb] (weights, one row a channel), sa [M], sb [N] float32, C [M][ldc]. M = 0 or N = 0 does
  * nothing. Errors: MOE_E_ARG (null or misaligned pointer, negative size, bad type or stride, overlap),
- * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K, M or N above MOE_MAX_MATMUL_MN, or a product past 2^32
- * threads of a launch: some 10^8 channels of up to 16 tokens, 10^11 values of C above). */
+ * MOE_E_SHAPE (K not in 1..MOE_MAX_MATMUL_K, M or N above MOE_MAX_MATMUL_MN, or a product past a launch's
+ * threads: more than 134217712 channels of up to 16 tokens; from 17 tokens on, 2^23 or more pieces
+ * of 256 x 256 values of C, ragged ones counted whole: 5 * 10^11 values). */
 int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb,
                   const float* sb, int M, int N, int K, int c_dtype, void* C, int64_t ldc, int accumulate);
 

@@ -1491,18 +1491,46 @@ int launched(const char* what) {
   return e == hipSuccess ? MOE_OK : hip_fail(e, what);
 }
 
-template <int BT, int BC, int WT, int WC, int KG, int BK, int S, int BK_HELD, int S_HELD>
+constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;   // of one launch, at most
+
+// A tile's cost is its time over K (the one measured: K = 2560, one round of up to 256 tiles, us) times
+// the rounds that 256 CUs need. Small tiles bring the chip's CUs to a small product (512 x 1536: 64 x 64
+// 8.2 us, 128 x 128 14.2, 256 x 256 34), large ones read less for each product of a large one (8192 x
+// 1536: 256 x 256 51 us, 64 x 64 72). The largest tile takes the fewest threads for any product.
+struct Tile {
+  int bt, bc, threads;
+  double us;
+};
+constexpr Tile kTiles[] = {{32, 32, 256, 5.6}, {64, 32, 512, 6.9}, {64, 64, 256, 8.2}, {128, 64, 512, 13.5},
+                           {128, 128, 512, 18.8}, {256, 128, 512, 25.8}, {256, 256, 512, 41}};
+int64_t tiles_of(const Tile& t, int M, int N) {
+  return (((int64_t)M + t.bt - 1) / t.bt) * (((int64_t)N + t.bc - 1) / t.bc);
+}
+// The tile of least cost among those whose launch is possible; -1: none.
+int choose_tile(int M, int N) {
+  int best = -1;
+  double least = 0;
+  for (int i = 0; i < 7; ++i) {
+    const int64_t n = tiles_of(kTiles[i], M, N);
+    if (n * kTiles[i].threads > kLaunchThreads) continue;
+    const double cost = kTiles[i].us * (double)((n + 255) / 256);
+    if (best < 0 || cost < least) best = i, least = cost;
+  }
+  return best;
+}
+
+template <int I, int WT, int WC, int KG, int BK, int S, int BK_HELD, int S_HELD>
 int launch_tile(hipStream_t st, MatmulArgs p, bool direct) {
-  const int64_t tn = ((int64_t)p.N + BC - 1) / BC, tiles = tn * (((int64_t)p.M + BT - 1) / BT);
-  if (tiles * 64 * WT * WC * KG > 0xFFFFFFFFll) return MOE_E_SHAPE;   // threads of a launch
-  p.tiles_n = (int)tn;
-  p.tiles = (int)tiles;
+  constexpr int BT = kTiles[I].bt, BC = kTiles[I].bc, THREADS = kTiles[I].threads;
+  static_assert(THREADS == 64 * WT * WC * KG, "the table's threads are the kernel's");
+  p.tiles_n = (int)(((int64_t)p.N + BC - 1) / BC);
+  p.tiles = (int)tiles_of(kTiles[I], p.M, p.N);
   auto go = [&](auto kern, int lds) {
     if (lds > 64 * 1024) {
       const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
       if (e != hipSuccess) return hip_fail(e, "moe_matmul_i8");
     }
-    hipLaunchKernelGGL(kern, dim3((unsigned)tiles), dim3(64 * WT * WC * KG), lds, st, p);
+    hipLaunchKernelGGL(kern, dim3((unsigned)p.tiles), dim3(THREADS), lds, st, p);
     return launched("moe_matmul_i8");
   };
   return direct ? go(k_matmul_tile<BT, BC, WT, WC, KG, BK, true, S>, S * (BT + BC) * KG * BK)
@@ -1516,11 +1544,11 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
   p.wide = (in16 == 4 || !p.accumulate) && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % in16 == 0 && p.N % in16 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
   // up to 32 tokens where K is short: 32 x 2560, K = 768 3.7 us, and 4.4 in tiles; K = 2560 10.8 and 7.3
-  if (p.M <= 16 || (p.M <= 32 && p.K <= 1024)) {
+  const bool launches = p.N <= kLaunchThreads / 512 * 16;   // 512 threads for 16 channels
+  if (p.M <= 16 || (p.M <= 32 && p.K <= 1024 && launches)) {
+    if (!launches) return MOE_E_SHAPE;
     auto go = [&](auto kern, int channels, int threads) {
-      const int64_t groups = ((int64_t)p.N + channels - 1) / channels;
-      if (groups * threads > 0xFFFFFFFFll) return (int)MOE_E_SHAPE;   // threads of a launch
-      hipLaunchKernelGGL(kern, dim3((unsigned)groups), dim3(threads), 0, st, p);
+      hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)p.N + channels - 1) / channels)), dim3(threads), 0, st, p);
       return launched("moe_matmul_i8");
     };
     // as few pieces of K side by side as leave two workgroups a CU
@@ -1529,30 +1557,15 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
     if (p.M <= 16) return go(k_matmul_thin<1, 1, 8>, 16, 512);
     return go(k_matmul_thin<2, 1, 8>, 16, 512);
   }
-  // A tile's cost is its time over K (the one measured: K = 2560, one round of up to 256 tiles, us) times
-  // the rounds that 256 CUs need. Small tiles bring the chip's CUs to a small product (512 x 1536: 64 x 64
-  // 8.2 us, 128 x 128 14.2, 256 x 256 34), large ones read less for each product of a large one (8192 x
-  // 1536: 256 x 256 51 us, 64 x 64 72).
-  struct Tile {
-    int bt, bc;
-    double us;
-  };
-  static constexpr Tile tiles[] = {{32, 32, 5.6}, {64, 32, 6.9}, {64, 64, 8.2}, {128, 64, 13.5}, {128, 128, 18.8}, {256, 128, 25.8}, {256, 256, 41}};
-  int best = 0;
-  double least = 0;
-  for (int i = 0; i < 7; ++i) {
-    const int64_t n = (((int64_t)p.M + tiles[i].bt - 1) / tiles[i].bt) * (((int64_t)p.N + tiles[i].bc - 1) / tiles[i].bc);
-    const double cost = tiles[i].us * (double)((n + 255) / 256);
-    if (i == 0 || cost < least) best = i, least = cost;
-  }
-  switch (best) {
-    case 0: return launch_tile<32, 32, 2, 1, 2, 128, 4, 128, 2>(st, p, direct);
-    case 1: return launch_tile<64, 32, 4, 1, 2, 128, 3, 128, 2>(st, p, direct);
-    case 2: return launch_tile<64, 64, 2, 2, 1, 128, 4, 128, 2>(st, p, direct);
-    case 3: return launch_tile<128, 64, 4, 2, 1, 128, 4, 128, 1>(st, p, direct);
-    case 4: return launch_tile<128, 128, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
-    case 5: return launch_tile<256, 128, 4, 2, 1, 128, 3, 128, 2>(st, p, direct);
-    default: return launch_tile<256, 256, 4, 2, 1, 128, 2, 64, 1>(st, p, direct);
+  switch (choose_tile(p.M, p.N)) {
+    case 0: return launch_tile<0, 2, 1, 2, 128, 4, 128, 2>(st, p, direct);
+    case 1: return launch_tile<1, 4, 1, 2, 128, 3, 128, 2>(st, p, direct);
+    case 2: return launch_tile<2, 2, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 3: return launch_tile<3, 4, 2, 1, 128, 4, 128, 1>(st, p, direct);
+    case 4: return launch_tile<4, 4, 2, 1, 128, 4, 128, 2>(st, p, direct);
+    case 5: return launch_tile<5, 4, 2, 1, 128, 3, 128, 2>(st, p, direct);
+    case 6: return launch_tile<6, 4, 2, 1, 128, 2, 64, 1>(st, p, direct);
+    default: return MOE_E_SHAPE;
   }
 }
 

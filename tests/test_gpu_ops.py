@@ -653,3 +653,25 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for got, w in zip(a.outputs() + b.outputs(), want):
         assert torch.equal(got, w)
+
+
+def test_matmul_with_more_channels_than_the_usual_launch_takes():
+    """17 tokens past the few-token kernel's channels, and 33 past those of the tile of least cost."""
+    for M, N in ((17, 134217712 + 96), (33, 1 << 30)):
+        K = 3
+        need = 2 * M * N + K * N + 4 * N + (8 << 30)
+        if torch.cuda.mem_get_info()[0] < need:
+            pytest.skip(f"{need >> 30} GiB of memory are not free")
+        g = torch.Generator(device=DEV).manual_seed(M)
+        a = torch.randint(-128, 128, (M, K), generator=g, device=DEV, dtype=torch.int8)
+        b = torch.randint(-128, 128, (N, K), generator=g, device=DEV, dtype=torch.int8)
+        sa, sb = torch.rand(M, generator=g, device=DEV) + 0.5, torch.rand(N, generator=g, device=DEV) + 0.5
+        c = torch.full((M, N), float("nan"), dtype=BF16, device=DEV)
+        B.moe_matmul_i8(a, sa, b, sb, c=c)
+        for n in range(0, N, 1 << 26):
+            e = min(N, n + (1 << 26))
+            for m in range(M):
+                sums = sum(a[m, i].float() * b[n:e, i].float() for i in range(K))   # whole numbers below 2^24
+                assert torch.equal(c[m, n:e], (sums * sa[m] * sb[n:e]).to(BF16))
+        del a, b, sa, sb, c
+        torch.cuda.empty_cache()

@@ -119,3 +119,20 @@ def test_binding_refuses_sizes_past_32_bits():
     for shape in ((1 << 31, 1), (1, (1 << 32) + 16)):   # of no memory: one element, expanded
         with pytest.raises(ValueError, match="past 32 bits"):
             B._rows("call", "t", torch.zeros(1, 1).expand(shape), None, (torch.float32,), -1)
+
+
+HIP = -4
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch kernels on pointers that are fakes")
+@pytest.mark.parametrize("M,N,K,launches", [
+    (16, 134217712, 64, True), (16, 134217713, 64, False),     # 512 threads for 16 channels
+    (17, 134217712, 64, True), (17, 134217713, 64, True), (32, 1 << 28, 1024, True), (17, 1 << 27, 1025, True),
+    (33, (1 << 30) - 64, 16, True), (33, 1 << 30, 16, True),   # 64 x 64 tiles up to 2^30 - 64 channels, then larger ones
+    (257, 1 << 29, 16, True), (1 << 30, 33, 16, True), (256, 2147483136, 16, True), (2147483136, 17, 16, True),
+    (1 << 19, (1 << 20) - 256, 16, True), (1 << 19, (1 << 20) - 255, 16, False), (2147483136, 257, 16, False)])
+def test_matmul_sizes_are_refused_only_past_a_launch(M, N, K, launches):
+    """Without a GPU a call that passes its checks ends in the launch's own error."""
+    far = dict(a=1 << 50, b=1 << 52, sa=1 << 54, sb=1 << 55, c=1 << 57)
+    got = getattr(B.lib(), "moe_matmul_i8")(None, *dict(MATMUL, **far, M=M, N=N, K=K, lda=1024 + K, ldb=1024 + K, ldc=N).values())
+    assert got == (HIP if launches else SHAPE)
