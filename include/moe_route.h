@@ -320,8 +320,8 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * dense half that every token takes) in 8-bit integers. Each call takes one token or thousands.
  *
  * Conventions beside those at the top: row strides (ld*) count elements and are at least the row
- * length; any stride and any row alignment an element type allows is accepted (16-byte aligned rows
- * are fastest). Row elements past the row length and rows past the last are neither read nor
+ * length and at most MOE_MAX_SPAN / rows; any such stride and any row alignment an element type allows is
+ * accepted (16-byte aligned rows are fastest). Row elements past the row length and rows past the last are neither read nor
  * written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
  * NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
  * as their outputs do not. Outputs may not overlap inputs or each other unless a comment says so (rows of
@@ -335,6 +335,7 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
 typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element types of rows */
 #define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
 #define MOE_MAX_ROWS 4194303      /* max rows of those and tokens of moe_route_scores (a launch's threads) */
+#define MOE_MAX_SPAN (1ll << 50)  /* max rows x stride of one operand, elements: more than any memory */
 #define MOE_MAX_MATMUL_K 131071   /* max K of moe_matmul_i8: K * 128 * 128 stays below 2^31 */
 #define MOE_MAX_MATMUL_MN 2147483136   /* max M and N: a tile past the last row still counts in 32 bits */
 

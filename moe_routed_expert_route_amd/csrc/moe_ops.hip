@@ -1451,23 +1451,26 @@ __global__ __launch_bounds__(64 * W) void k_matmul_thin(MatmulArgs p) {
 
 bool aligned(const void* p, int size) { return ((uintptr_t)p & (uintptr_t)(size - 1)) == 0; }
 
-// Rows in memory, in bytes: `rows` of `len`, `step` apart.
+// Rows in memory, in bytes: `rows` of `len`, `step` apart (one row: its length).
 struct Rows {
   const void* p;
   int64_t rows, len, step;
 };
-Rows rows_of(const void* p, int64_t rows, int64_t n, int64_t ld, int size) { return Rows{p, rows, n * size, ld * size}; }
+Rows rows_of(const void* p, int64_t rows, int64_t n, int64_t ld, int size) { return Rows{p, rows, n * size, (rows > 1 ? ld : n) * size}; }
+
+// Whether a row stride is none: below the row length, or rows that no memory holds (offsets and spans in bytes,
+// also those of a tile's rows past the last, then stay far below 2^63).
+bool bad_stride(int64_t ld, int64_t n, int64_t rows) { return ld < n || ld > MOE_MAX_SPAN / rows; }
 
 // Whether two sets of rows share a byte (for different steps: whether their spans do).
 bool overlap(const Rows& a, const Rows& b) {
   if (!a.p || !b.p || !a.rows || !b.rows) return false;
-  const uintptr_t pa = (uintptr_t)a.p, pb = (uintptr_t)b.p;
-  if (pa >= pb + (uintptr_t)((b.rows - 1) * b.step + b.len) || pb >= pa + (uintptr_t)((a.rows - 1) * a.step + a.len))
-    return false;
-  if (a.step != b.step) return true;
-  const int64_t shift = (int64_t)((pb > pa ? pb - pa : pa - pb) % (uintptr_t)a.step);   // of the later rows' columns
-  const int64_t first = pb > pa ? a.len : b.len, second = pb > pa ? b.len : a.len;
-  return shift < first || shift + second > a.step;
+  const Rows &x = (uintptr_t)a.p <= (uintptr_t)b.p ? a : b, &y = &x == &a ? b : a;   // x starts first
+  const uint64_t gap = (uintptr_t)y.p - (uintptr_t)x.p;
+  if (gap >= (uint64_t)((x.rows - 1) * x.step + x.len)) return false;
+  if (x.step != y.step) return true;
+  const int64_t shift = (int64_t)(gap % (uint64_t)x.step);   // of y's columns
+  return shift < x.len || shift + y.len > x.step;
 }
 
 // A row call's type and workgroup: by the row length alone, so that a row's sums have one order.
@@ -1585,7 +1588,9 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
   if (n < 1 || n > MOE_MAX_ROW || (q8_1 && n % 32) || rows > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (rows == 0) return MOE_OK;
   if (!x || !weight || !q != !scale || (!res_out && !yout && !q && !q8_1)) return MOE_E_ARG;
-  if (ldx < n || (res && ldres < n) || (res_out && ldro < n) || (yout && ldy < n) || (q && ldq < n)) return MOE_E_ARG;
+  if (bad_stride(ldx, n, rows) || (res && bad_stride(ldres, n, rows)) || (res_out && bad_stride(ldro, n, rows)) ||
+      (yout && bad_stride(ldy, n, rows)) || (q && bad_stride(ldq, n, rows)))
+    return MOE_E_ARG;
   const int sz = type_size(dtype), szy = type_size(y_dtype);
   if (!aligned(x, sz) || !aligned(res, sz) || !aligned(res_out, sz) || !aligned(weight, type_size(w_dtype)) ||
       (yout && !aligned(yout, szy)) || !aligned(scale, 4) || !aligned(q8_1, 4))
@@ -1619,7 +1624,7 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
   if ((renorm != 0 && renorm != 1) || !(factor == factor) || ld < E) return MOE_E_ARG;
   if (T > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (T == 0) return MOE_OK;
-  if (!logits || !ids || !w || !aligned(logits, type_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||
+  if (!logits || !ids || !w || bad_stride(ld, E, T) || !aligned(logits, type_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||
       !aligned(w, 4))
     return MOE_E_ARG;
   const Rows out[] = {rows_of(ids, T, k, k, 4), rows_of(w, T, k, k, 4)};
@@ -1661,7 +1666,8 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
   if (n < 1 || n > MOE_MAX_ROW || rows > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (rows == 0) return MOE_OK;
   const int sz = type_size(dtype);
-  if (!g || !u || !q || !scale || ldg < n || ldu < n || ldq < n) return MOE_E_ARG;
+  if (!g || !u || !q || !scale || bad_stride(ldg, n, rows) || bad_stride(ldu, n, rows) || bad_stride(ldq, n, rows))
+    return MOE_E_ARG;
   if (!aligned(g, sz) || !aligned(u, sz) || !aligned(scale, 4)) return MOE_E_ARG;
   const Rows out[] = {rows_of(q, rows, n, ldq, 1), rows_of(scale, 1, rows, rows, 4)};
   for (const Rows& o : out)
@@ -1679,7 +1685,8 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
   if (!type_ok(c_dtype) || M < 0 || N < 0 || (accumulate != 0 && accumulate != 1)) return MOE_E_ARG;
   if (K < 1 || K > MOE_MAX_MATMUL_K || std::max(M, N) > MOE_MAX_MATMUL_MN) return MOE_E_SHAPE;
   if (M == 0 || N == 0) return MOE_OK;
-  if (!a || !sa || !b || !sb || !C || lda < K || ldb < K || ldc < N) return MOE_E_ARG;
+  if (!a || !sa || !b || !sb || !C || bad_stride(lda, K, M) || bad_stride(ldb, K, N) || bad_stride(ldc, N, M))
+    return MOE_E_ARG;
   if (!aligned(sa, 4) || !aligned(sb, 4) || !aligned(C, type_size(c_dtype))) return MOE_E_ARG;
   const Rows c = rows_of(C, M, N, ldc, type_size(c_dtype));
   if (overlap(c, rows_of(a, M, K, lda, 1)) || overlap(c, rows_of(b, N, K, ldb, 1)) || overlap(c, rows_of(sa, 1, M, M, 4)) ||

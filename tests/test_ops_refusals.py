@@ -136,3 +136,31 @@ def test_matmul_sizes_are_refused_only_past_a_launch(M, N, K, launches):
     far = dict(a=1 << 50, b=1 << 52, sa=1 << 54, sb=1 << 55, c=1 << 57)
     got = getattr(B.lib(), "moe_matmul_i8")(None, *dict(MATMUL, **far, M=M, N=N, K=K, lda=1024 + K, ldb=1024 + K, ldc=N).values())
     assert got == (HIP if launches else SHAPE)
+
+
+FAR = {"moe_add_rmsnorm": dict(scale=P5 + (1 << 31)), "moe_route_scores": {}, "moe_swiglu_i8": {}, "moe_matmul_i8": dict(ldc=1 << 20)}
+STRIDES = [("moe_add_rmsnorm", "rows", ("ldx", "ldres", "ldro", "ldy", "ldq")), ("moe_route_scores", "T", ("ld",)),
+           ("moe_swiglu_i8", "rows", ("ldg", "ldu", "ldq")), ("moe_matmul_i8", "M", ("lda", "ldc")), ("moe_matmul_i8", "N", ("ldb",))]
+
+
+@pytest.mark.parametrize("rows", [1, 2, 5, 1 << 20])
+@pytest.mark.parametrize("ld", [(1 << 50) + 1, 1 << 60, 1 << 62, (1 << 62) + 1, (1 << 63) - 1])
+@pytest.mark.parametrize("name,count,strides", STRIDES)
+def test_strides_past_any_memory_are_refused(name, count, strides, ld, rows):
+    """Each stride alone and all together: in bytes, or times the rows, they wrap in 64 bits."""
+    for change in [{s: ld} for s in strides] + [{s: ld for s in strides}, {s: (1 << 50) // rows + 1 for s in strides}]:
+        args = dict(CALLS[name], **{**FAR[name], count: rows, **change})
+        assert getattr(B.lib(), name)(None, *args.values()) == ARG, change
+
+
+def test_huge_strides_of_overlapping_rows_are_refused():
+    for rows, ld in ((1, 1 << 62), (5, 1 << 60), (3, 1 << 61), (1 << 20, 1 << 42)):
+        args = dict(NORM, rows=rows, res=None, res_out=None, q=None, scale=None, ldx=ld, ldy=ld, y=P + 16)
+        assert B.lib().moe_add_rmsnorm(None, *args.values()) == ARG
+
+
+@pytest.mark.parametrize("q,want", [(P + 16, ARG), (P + 255, ARG), (P - 63, ARG), (P + 256, HIP), (P - 64, HIP), (P + (1 << 20), HIP)])
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch kernels on pointers that are fakes")
+def test_one_row_of_any_stride_overlaps_by_its_bytes(q, want):
+    args = dict(NORM, rows=1, res=None, res_out=None, y=None, q=q, scale=P4, ldx=1 << 50, ldq=1 << 48)
+    assert B.lib().moe_add_rmsnorm(None, *args.values()) == want
