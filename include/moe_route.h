@@ -378,7 +378,7 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
                      float factor, int32_t* ids, float* w);
 
 /* SwiGLU into i8 rows, beside moe_swiglu_q8_1: h = float32(g / (1 + exp(-g)) * u), evaluated in 64 bits
- * and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in `dtype` of strides ldg
+ * (within 2^-50 of its size) and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in `dtype` of strides ldg
  * and ldu (the two halves of one product's rows: u = g + n, both strides that product's).
  * Errors: MOE_E_ARG (null or misaligned pointer, bad type or stride, overlap), MOE_E_SHAPE (n not in
  * 1..MOE_MAX_ROW, rows > MOE_MAX_ROWS). */

@@ -360,31 +360,44 @@ __global__ __launch_bounds__(THREADS) void k_add_rmsnorm(NormArgs a) {
   if (a.q) write_i8_row<THREADS, C>(r, a.n, a.q + row * a.ldq, a.scale + row, s_max);
 }
 
-// ------------------------------------------------------------------ SwiGLU ------------------
+// ------------------------------------------------------------------ 64 bits -----------------
 
-// 1 / (1 + exp(-g)) within some 2^-45 relative: exp(-g) = 2^n 2^f with n = rint(t), t = -g log2(e), and
-// 2^f, |f| <= 1/2, by its power series to f^11 (the next term is below 2^-47); the reciprocal's seed takes
-// one Newton step. t is held to +-1000: beyond, the result times any two float32 values rounds as it
-// does there.
-__device__ __forceinline__ double sigmoid64(double g) {
-  const double t = __builtin_fmin(__builtin_fmax(g * -1.4426950408889634, -1000.0), 1000.0);
-  const double n = __builtin_rint(t), f = t - n;
-  double e = 4.44553827187081e-10;
-  e = __builtin_fma(e, f, 7.054911620801121e-09);
-  e = __builtin_fma(e, f, 1.0178086009239696e-07);
-  e = __builtin_fma(e, f, 1.3215486790144305e-06);
-  e = __builtin_fma(e, f, 1.5252733804059838e-05);
-  e = __builtin_fma(e, f, 0.00015403530393381606);
-  e = __builtin_fma(e, f, 0.0013333558146428441);
-  e = __builtin_fma(e, f, 0.009618129107628477);
-  e = __builtin_fma(e, f, 0.055504108664821576);
-  e = __builtin_fma(e, f, 0.2402265069591007);
-  e = __builtin_fma(e, f, 0.6931471805599453);
-  e = __builtin_fma(e, f, 1.0);
-  const double den = 1.0 + __builtin_ldexp(e, (int)n);
-  const double x = __builtin_amdgcn_rcp(den);
-  return __builtin_fma(__builtin_fma(-den, x, 1.0), x, x);
+// exp(x) to an ulp or two for x <= 709 (below -745: 0): x = n ln 2 + r, |r| <= ln(2) / 2, and e^r by its
+// power series to r^13 (the next term is below 2^-57).
+__device__ __forceinline__ double exp64(double x) {
+  const double n = __builtin_rint(__builtin_fmax(x, -1100.0) * 1.4426950408889634);
+  const double y = __builtin_fmax(x, -1100.0);
+  const double r = __builtin_fma(-n, 2.3190468138462996e-17, __builtin_fma(-n, 0.6931471805599453, y));
+  double e = 1.0 / 6227020800.0;
+  e = __builtin_fma(e, r, 1.0 / 479001600.0);
+  e = __builtin_fma(e, r, 1.0 / 39916800.0);
+  e = __builtin_fma(e, r, 1.0 / 3628800.0);
+  e = __builtin_fma(e, r, 1.0 / 362880.0);
+  e = __builtin_fma(e, r, 1.0 / 40320.0);
+  e = __builtin_fma(e, r, 1.0 / 5040.0);
+  e = __builtin_fma(e, r, 1.0 / 720.0);
+  e = __builtin_fma(e, r, 1.0 / 120.0);
+  e = __builtin_fma(e, r, 1.0 / 24.0);
+  e = __builtin_fma(e, r, 1.0 / 6.0);
+  e = __builtin_fma(e, r, 0.5);
+  e = __builtin_fma(e, r, 1.0);
+  e = __builtin_fma(e, r, 1.0);
+  return __builtin_ldexp(e, (int)n);
 }
+
+// 1 / x to an ulp for normal x (infinity gives 0): the seed and two Newton steps.
+__device__ __forceinline__ double inverse64(double x) {
+  const double s = __builtin_amdgcn_rcp(x);
+  const double r = __builtin_fma(__builtin_fma(-x, s, 1.0), s, s);
+  const double y = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
+  return x < __builtin_inf() ? y : 0.0;
+}
+
+// 1 / (1 + exp(-x)) within 4.3 * 2^-53 relative (exp 2.2 of them: r, the last two steps of the series and its end;
+// the sum 1, the inverse 1); 0 where exp(-x) passes the largest double.
+__device__ __forceinline__ double sigmoid64(double x) { return inverse64(1.0 + exp64(-__builtin_fmax(x, -1000.0))); }
+
+// ------------------------------------------------------------------ SwiGLU ------------------
 
 struct SwigluArgs {
   const void *g, *u;
@@ -394,7 +407,7 @@ struct SwigluArgs {
   int n;
 };
 
-// h, the one that counts: 64 bits, rounded once.
+// h, the one that counts: 64 bits (within 2^-50: the sigmoid and two products), rounded once.
 __device__ __forceinline__ float swiglu64(float g, float u) {
   return (float)((double)g * sigmoid64((double)g) * (double)u);
 }
@@ -508,37 +521,6 @@ struct RouteArgs {
 };
 
 constexpr int kRouteE = 1024;
-
-// exp(x) to an ulp or two for x <= 709 (below -745: 0): x = n ln 2 + r, |r| <= ln(2) / 2, and e^r by its
-// power series to r^13 (the next term is below 2^-57).
-__device__ __forceinline__ double exp64(double x) {
-  const double n = __builtin_rint(__builtin_fmax(x, -1100.0) * 1.4426950408889634);
-  const double y = __builtin_fmax(x, -1100.0);
-  const double r = __builtin_fma(-n, 2.3190468138462996e-17, __builtin_fma(-n, 0.6931471805599453, y));
-  double e = 1.0 / 6227020800.0;
-  e = __builtin_fma(e, r, 1.0 / 479001600.0);
-  e = __builtin_fma(e, r, 1.0 / 39916800.0);
-  e = __builtin_fma(e, r, 1.0 / 3628800.0);
-  e = __builtin_fma(e, r, 1.0 / 362880.0);
-  e = __builtin_fma(e, r, 1.0 / 40320.0);
-  e = __builtin_fma(e, r, 1.0 / 5040.0);
-  e = __builtin_fma(e, r, 1.0 / 720.0);
-  e = __builtin_fma(e, r, 1.0 / 120.0);
-  e = __builtin_fma(e, r, 1.0 / 24.0);
-  e = __builtin_fma(e, r, 1.0 / 6.0);
-  e = __builtin_fma(e, r, 0.5);
-  e = __builtin_fma(e, r, 1.0);
-  e = __builtin_fma(e, r, 1.0);
-  return __builtin_ldexp(e, (int)n);
-}
-
-// 1 / x to an ulp for normal x (infinity gives 0): the seed and two Newton steps.
-__device__ __forceinline__ double inverse64(double x) {
-  const double s = __builtin_amdgcn_rcp(x);
-  const double r = __builtin_fma(__builtin_fma(-x, s, 1.0), s, s);
-  const double y = __builtin_fma(__builtin_fma(-x, r, 1.0), r, r);
-  return x < __builtin_inf() ? y : 0.0;
-}
 
 // A logit as the definition takes it: NaN as -infinity, at most the largest float32, no negative zero.
 __device__ __forceinline__ float route_logit(float l) {

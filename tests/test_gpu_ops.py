@@ -675,3 +675,32 @@ def test_matmul_with_more_channels_than_the_usual_launch_takes():
                 assert torch.equal(c[m, n:e], (sums * sa[m] * sb[n:e]).to(BF16))
         del a, b, sa, sb, c
         torch.cuda.empty_cache()
+
+
+# g:u as the bits of float32 values, found by search: h lies 2^-50 to 2^-48 of itself from a float32 rounding border
+NEAR_BORDERS = """
+    c072d972:3fe4a77a c0d300c6:3fb6113f c0486ecd:3fbee7a5 c0bd25f6:3fb1b527 c0a6ed55:3fadda4b bf840b27:3fd8f94f
+    c09056d9:3fa1b680 c0e83ba2:3ff76784 bf87d31c:3fafa216 c0e9097a:3fb29b5d c0d2fb8e:3fc4fdbd bfe12f6e:3fe50595
+    bf8261b4:3fcde385 c0a6c65b:3ffaa4e3 c0d25320:3fa15396 c0fe6fb5:3f9688db c0e88e0a:3f8210bf c0e88e0a:3f8799a1
+    c0e88e0a:3f8d2283 c0e88e0a:3f92ab65 c0e88e0a:3f983447 c0e88e0a:3f9dbd29 c0e88e0a:3fa3460b c0e88e0a:3fa8ceed
+    c0e88e0a:3fae57cf c0e88e0a:3fb3e0b1 c0e88e0a:3fb96993 c0e88e0a:3fbef275 c0e88e0a:3fc47b57 c0e88e0a:3fccc8aa
+    c0e88e0a:3fd7da6e c0e88e0a:3fe2ec32 c0e88e0a:3fedfdf6 c0e88e0a:3ff90fba 40fd3151:3fa257d2 c0738925:3ff84e5d
+    c0e22195:3f9900d2 c0e22195:3fc4b1d5 40ab697a:3fbd09f5 3fbfbcb9:3f885aaa 40f03471:3ffce735 4061beee:3f889fef
+    c1715532:3fb00a54 c09fab02:3fdcb560 c09fab02:3ff9a72e c12c6c71:3fe1505f c09910b5:3fb20f30 c09910b5:3feb3875
+    c0dc5444:3fe4026d 3fc07060:3fb9384d c17e0489:3fc0a33d 3f0be38e:3f92e251 c0a3fb05:3fccfc29 bee03084:3fbeccac
+    40338a84:3f9fd911 40418082:3fe7a83b c18e0513:3fabf7de 40ee06f8:3f802bf6
+"""
+
+
+def test_swiglu_next_to_rounding_borders():
+    """h is within 2^-50 of its exact value before its rounding, so these round as the exact values do (in 80 bits
+    here). A row of one value: its scale is float32(|h| / 127)."""
+    assert np.finfo(np.longdouble).nmant >= 63
+    bits = np.array([[int(v, 16) for v in pair.split(":")] for pair in NEAR_BORDERS.split()], np.uint32)
+    g, u = bits.view(np.float32).T.astype(np.longdouble)
+    h = np.abs(g / (1 + np.exp(-g)) * u)
+    m = np.frexp(h)[0] * np.longdouble(2) ** 24
+    assert (np.abs(m - np.floor(m) - 0.5) > m * np.longdouble(2) ** -50).all()
+    q, d = B.moe_swiglu_i8(*(torch.from_numpy(x.astype(np.float32)[:, None]).to(DEV) for x in (g, u)))
+    assert np.array_equal(d.cpu().numpy(), h.astype(np.float32) / np.float32(127))
+    assert np.array_equal(q.cpu().numpy()[:, 0], (127 * np.sign(g)).astype(np.int8))
