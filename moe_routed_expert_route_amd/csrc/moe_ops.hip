@@ -429,7 +429,7 @@ __global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
   const T* up = (const T*)a.u + row * a.ldu;
   T g[C][kPiece], u[C][kPiece];
   float h[C][kPiece];
-  uint32_t most[C];   // |h| of each piece
+  uint32_t most[C];   // |h| of each piece; like h, set for pieces of the row
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     load_raw(gp, (c * THREADS + (int)threadIdx.x) * kPiece, a.n, g[c]);
@@ -438,7 +438,6 @@ __global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
   uint32_t m = 0;
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    most[c] = 0;
     if ((c * THREADS + (int)threadIdx.x) * kPiece >= a.n) break;   // whole waves, but for one
     float far = 0.0f, low = 1.0f;
 #pragma unroll
@@ -468,13 +467,15 @@ __global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
   const float near = __builtin_bit_cast(float, m) * (1.0f - 0x1p-18f);
   m = 0;
 #pragma unroll
-  for (int c = 0; c < C; ++c)
+  for (int c = 0; c < C; ++c) {
+    if ((c * THREADS + (int)threadIdx.x) * kPiece >= a.n) break;   // h and most are set up to here
     if (__builtin_bit_cast(float, most[c]) >= near) {
 #pragma unroll
       for (int e = 0; e < kPiece; ++e)
         if (__builtin_fabsf(h[c][e]) >= near)
           m = max(m, __builtin_bit_cast(uint32_t, __builtin_fabsf(swiglu64(to_f(g[c][e]), to_f(u[c][e])))));
     }
+  }
   m = row_max<THREADS>(m, s_max);
   const QScale s = q_scale(__builtin_bit_cast(float, m));
   const bool codes = finite && s.d != 0.0f;

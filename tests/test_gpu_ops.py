@@ -704,3 +704,14 @@ def test_swiglu_next_to_rounding_borders():
     q, d = B.moe_swiglu_i8(*(torch.from_numpy(x.astype(np.float32)[:, None]).to(DEV) for x in (g, u)))
     assert np.array_equal(d.cpu().numpy(), h.astype(np.float32) / np.float32(127))
     assert np.array_equal(q.cpu().numpy()[:, 0], (127 * np.sign(g)).astype(np.int8))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [1, 7, 8, 9, 505, 513, 1025, 2048, 2049, 2056, 2560, 4095, 4097, 5461, 8193, 8200, 16377])
+def test_swiglu_rows_of_zeros_between_others(n, dtype):
+    """Rows of zeros, of either sign and from either factor, where some threads hold no piece of the row, or one of two."""
+    g, u = randn((6, n), dtype, n, 37), randn((6, n), dtype, n, 38)
+    g[1], u[2], g[3], u[4] = 0, 0, -0.0, -0.0
+    q, d = B.moe_swiglu_i8(g, u)
+    assert not q[1:5].any() and not d[1:5].any()
+    check_codes(q[::5], d[::5], swiglu_ref(host(g[::5]), host(u[::5])))
