@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import os
 import subprocess
+import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -29,18 +30,17 @@ def _run(cmd) -> str:
 
 
 def build(verbose: bool = False) -> str:
-    """Always recompiles (the sources side by side); writes the library atomically."""
+    """Always recompiles (the sources side by side), in a folder of its own; replaces the library atomically."""
     hipcc = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
-    objs = [os.path.splitext(s)[0] + ".o" for s in SRCS]
-    with ThreadPoolExecutor(len(SRCS)) as pool:
-        logs = list(pool.map(lambda so: _run([hipcc, *HIPCC_FLAGS, "-c", "-o", so[1], so[0]]), zip(SRCS, objs)))
-    tmp = LIB + ".tmp"
-    logs.append(_run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objs]))
+    with tempfile.TemporaryDirectory(prefix="build.", dir=os.path.dirname(LIB)) as work:
+        objs = [os.path.join(work, os.path.splitext(os.path.basename(s))[0] + ".o") for s in SRCS]
+        with ThreadPoolExecutor(len(SRCS)) as pool:
+            logs = list(pool.map(lambda so: _run([hipcc, *HIPCC_FLAGS, "-c", "-o", so[1], so[0]]), zip(SRCS, objs)))
+        tmp = os.path.join(work, os.path.basename(LIB))
+        logs.append(_run([hipcc, "--offload-arch=gfx950", "-fPIC", "-shared", "-o", tmp, *objs]))
+        os.replace(tmp, LIB)
     if verbose:
         print("".join(logs))
-    os.replace(tmp, LIB)
-    for o in objs:
-        os.remove(o)
     return LIB
 
 
