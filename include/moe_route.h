@@ -363,7 +363,7 @@ int moe_add_rmsnorm(void* stream, int dtype, const void* x, int64_t ldx, const v
  *   (1 or 2) largest c; the keep_groups best groups stay (n_groups = 1: all experts);
  *   ids = the k experts of those groups with the largest c, largest first (without a bias: by logit,
  *   the same order also where scores round to one value); w = their s (not c), divided by their sum
- *   when renorm = 1, times `factor`. Ties go to the lower index, for experts and for groups.
+ *   when renorm = 1, times `factor` (finite). Ties go to the lower index, for experts and for groups.
  * A logit of -infinity or NaN masks its expert: s = 0, it adds nothing to its group's score (a group
  * of masked experts comes after every other), and it is chosen only after every unmasked expert
  * of the groups kept, lowest index first. A token with every expert masked gets weights 0. +infinity

@@ -1604,7 +1604,7 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
   if (n_groups < 1 || n_groups > 64 || E % n_groups || keep_groups < 1 || keep_groups > n_groups) return MOE_E_ARG;
   const int per = E / n_groups;
   if (k > keep_groups * per || group_top < 1 || group_top > 2 || group_top > per) return MOE_E_ARG;
-  if ((renorm != 0 && renorm != 1) || !(factor == factor) || ld < E) return MOE_E_ARG;
+  if ((renorm != 0 && renorm != 1) || !(__builtin_fabsf(factor) < __builtin_inff()) || ld < E) return MOE_E_ARG;
   if (T > MOE_MAX_ROWS) return MOE_E_SHAPE;
   if (T == 0) return MOE_OK;
   if (!logits || !ids || !w || bad_stride(ld, E, T) || !aligned(logits, type_size(dtype)) || !aligned(bias, 4) || !aligned(ids, 4) ||

@@ -164,3 +164,9 @@ def test_huge_strides_of_overlapping_rows_are_refused():
 def test_one_row_of_any_stride_overlaps_by_its_bytes(q, want):
     args = dict(NORM, rows=1, res=None, res_out=None, y=None, q=q, scale=P4, ldx=1 << 50, ldq=1 << 48)
     assert B.lib().moe_add_rmsnorm(None, *args.values()) == want
+
+
+@pytest.mark.parametrize("factor", [INF, -INF])
+def test_route_factor_has_to_be_finite(factor):
+    """A masked token's weights are 0, which no infinite factor leaves."""
+    assert B.lib().moe_route_scores(None, *dict(ROUTE, factor=factor).values()) == ARG
