@@ -507,6 +507,8 @@ def moe_route_scores(logits, k, score=SCORE_SOFTMAX, bias=None, n_groups=1, keep
     T, E = logits.shape
     if not 0 < k <= E >= n_groups >= keep_groups > 0 < group_top <= E:
         raise ValueError(f"{what}: k {k}, groups {n_groups}, {keep_groups} kept by {group_top}, of {E} experts")
+    if score != SCORE_SOFTMAX and score != SCORE_SIGMOID:
+        raise ValueError(f"{what}: score {score}")
     if bias is not None:
         _packed(what, "bias", bias, (E,), torch.float32, dev)
     if ids is None:

@@ -715,3 +715,10 @@ def test_swiglu_rows_of_zeros_between_others(n, dtype):
     q, d = B.moe_swiglu_i8(g, u)
     assert not q[1:5].any() and not d[1:5].any()
     check_codes(q[::5], d[::5], swiglu_ref(host(g[::5]), host(u[::5])))
+
+
+def test_router_score_kind_is_refused_before_it_loses_bits():
+    l = randn((2, 8), F32, 18)
+    for score in (0, 3, -1, (1 << 32) + 1, (1 << 32) + 2):
+        with pytest.raises(ValueError, match="score"):
+            B.moe_route_scores(l, 2, score=score)
