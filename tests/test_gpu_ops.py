@@ -722,3 +722,83 @@ def test_router_score_kind_is_refused_before_it_loses_bits():
     for score in (0, 3, -1, (1 << 32) + 1, (1 << 32) + 2):
         with pytest.raises(ValueError, match="score"):
             B.moe_route_scores(l, 2, score=score)
+
+
+def buffers(b):
+    """Every buffer that Block.run writes, but for the plan."""
+    return [b.sum, b.y, b.q, b.d, b.xq, b.logits, b.ids, b.w, b.ent_of, b.g, b.u, b.hq, b.O, b.Y, b.gu, b.sq, b.ss]
+
+
+def test_two_streams_at_once_into_cleared_buffers():
+    """Each run has to write every output again."""
+    blocks = [Block(33, key=1), Block(34, key=2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    want = []
+    for b in blocks:
+        b.run()
+        torch.cuda.synchronize()
+        want.append(b.outputs())
+    for _ in range(5):
+        for b in blocks:
+            for t in buffers(b):
+                t.fill_(float("nan") if t.is_floating_point() else 77)
+            for got, w in zip(b.outputs(), want[0] if b is blocks[0] else want[1]):
+                assert not torch.equal(got, w)
+        torch.cuda.synchronize()
+        for b, s in zip(blocks, streams):
+            with torch.cuda.stream(s):
+                b.run()
+        torch.cuda.synchronize()
+        for b, outs in zip(blocks, want):
+            for got, w in zip(b.outputs(), outs):
+                assert torch.equal(got, w)
+
+
+def test_results_on_a_named_stream_are_of_its_memory():
+    """A result of the current stream takes the block that was just freed there; one of a named stream does not."""
+    a, b, s = i8((900, 640), 94), i8((2900, 640), 95), torch.ones(2900, device=DEV)
+    logits, g = randn((9000, 300), F32, 96), randn((900, 2000), BF16, 97)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for call in (lambda **kw: B.moe_matmul_i8(a, s[:900], b, s, **kw), lambda **kw: B.moe_route_scores(logits, 30, **kw)[0],
+                 lambda **kw: B.moe_route_scores(logits, 30, **kw)[1], lambda **kw: B.moe_swiglu_i8(g, g, **kw)[0]):
+        place = call().data_ptr()
+        assert call().data_ptr() == place
+        want = call()
+        torch.cuda.synchronize()
+        keep = want.clone()
+        del want
+        torch.cuda.synchronize()
+        got = call(stream=side)
+        assert got.data_ptr() != place
+        filled = torch.full_like(keep, 77)       # takes the block again, while the side stream may still run
+        assert filled.data_ptr() == place
+        torch.cuda.synchronize()
+        assert torch.equal(got, keep)
+        del got, filled, keep
+
+
+@pytest.mark.parametrize("off", [0, 1])
+@pytest.mark.parametrize("M,N,K", [(1, 256, 512), (6, 256, 512), (12, 256, 512), (24, 256, 512), (40, 2560, 768), (100, 2560, 256),
+                                   (512, 1536, 256), (1024, 1536, 384), (2048, 1536, 320), (4096, 1536, 256), (3330, 4096, 384)])
+def test_matmul_captured_and_replayed(M, N, K, off):
+    """Each of the kernels, rows aligned and not, in a graph of two products, the second added to the first."""
+    a, _ = rows_in(M, K, torch.int8, K + 16 + off, off)
+    b, _ = rows_in(N, K, torch.int8, K + 16 + off, off)
+    sa, sb = torch.rand(M, device=DEV) + 0.5, torch.rand(N, device=DEV) + 0.5
+    c, e = torch.empty((M, N), device=DEV), torch.empty((M, N), device=DEV)
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=side):
+        B.moe_matmul_i8(a, sa, b, sb, c=c)
+        B.moe_matmul_i8(a, sa, b, sb, c=c, accumulate=True)
+    for i in range(4):
+        a.copy_(i8((M, K), M, i, 98))
+        b.copy_(i8((N, K), N, i, 99))
+        B.moe_matmul_i8(a, sa, b, sb, c=e)
+        B.moe_matmul_i8(a, sa, b, sb, c=e, accumulate=True)
+        torch.cuda.synchronize()
+        c.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(c, e) and torch.equal(e, 2 * matmul_ref(a, sa, b, sb, F32).to(DEV))
