@@ -62,3 +62,35 @@ def test_sq_summary(tmp_path, monkeypatch):
     text = open(tmp_path / "sq_w.md").read()
     assert "| VALU instructions per wave | 640.000 | 200.000 |" in text
     assert "| VALU lane-instructions per weight (x 64) | 1.000 |" in text
+
+
+def test_ops_table(tmp_path, monkeypatch):
+    from moe_routed_expert_route_amd import opsprof
+    rows, at = [], 1000
+    for i, case in enumerate(opsprof.cases()):
+        for p in range(2 * opsprof.PASSES):
+            dur = 4000 + 100 * i if p < opsprof.PASSES else 8000 + 100 * i
+            if p in (0, 1, opsprof.PASSES):          # the first two of each kind do not count
+                dur = 90000
+            rows += [["at::native::fill(x)", at - 500, at - 400, 256, 2560],
+                     [f"void moe::k_case{i}<moe::bf16_t, 4>(moe::Args)", at, at + dur, 128, 128 * (i + 1)]]
+            at += 100000
+    hdr = ["Kernel_Name", "Start_Timestamp", "End_Timestamp", "Workgroup_Size_X", "Grid_Size_X"]
+    _write(tmp_path / "t.csv", hdr, reversed(rows))
+    _write(tmp_path / "c.csv", ["Dispatch_Id", "Kernel_Name", "Counter_Name", "Counter_Value"],
+           [[1, "__amd_rocclr_copyBuffer", "FETCH_SIZE", 131072], [2, "void moe::k_case2<moe::bf16_t, 4>(moe::Args)", "FETCH_SIZE", 70]])
+    monkeypatch.setattr(profsum, "PROFILES", str(tmp_path))
+    opsprof.table(str(tmp_path / "t.csv"), [str(tmp_path / "c.csv")], "cmd")
+    text = open(tmp_path / "kernels_ops.md").read()
+    case = opsprof.cases()[2]
+    gbs = opsprof.work(case)["bytes"] / 8.2 / 1e3
+    assert f"| {case['name']} | `k_case2<bf16_t, 4>` | 3 × 128 | 4.20 | 4.20 | 8.20 | {gbs:.0f} |" in text
+    assert "| FETCH_SIZE | the copy | 131072 |" in text and "| FETCH_SIZE | `k_case2<bf16_t, 4>` | 70 |" in text
+    assert opsprof.source_digest() in text
+    _write(tmp_path / "t.csv", hdr, rows[:-2])
+    try:
+        opsprof.table(str(tmp_path / "t.csv"), [], "cmd")
+    except ValueError as e:
+        assert "launches" in str(e)
+    else:
+        raise AssertionError("a trace with a launch missing was taken")
