@@ -802,3 +802,96 @@ def test_matmul_captured_and_replayed(M, N, K, off):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(c, e) and torch.equal(e, 2 * matmul_ref(a, sa, b, sb, F32).to(DEV))
+
+
+def same(got, want):
+    """Equal bits, any NaN equal to any."""
+    g, w = got.cpu(), want.cpu()
+    assert g.dtype == w.dtype and g.shape == w.shape
+    return bool(((g == w) | (g.isnan() & w.isnan())).all())
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("M,N", [(3, 48), (3, 47), (24, 64), (40, 64), (40, 61), (300, 328), (1100, 1536)])
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_matmul_scales_of_every_size(M, N, dtype, accumulate):
+    """Products below the smallest normal value, past the largest, infinite and NaN scales, also of sums of zero."""
+    K = 80
+    a, b = i8((M, K), M, 100), i8((N, K), N, 101)
+    a[0], b[0] = 0, 0
+    sa = torch.exp2(torch.from_numpy(synth.rng(M, 102).uniform(-100, 40, M)).float()).to(DEV)
+    sb = torch.exp2(torch.from_numpy(synth.rng(N, 103).uniform(-60, 60, N)).float()).to(DEV)
+    sa[1], sb[1] = float("inf"), float("nan")
+    sa[2], sb[2] = 0.0, float("-inf")
+    sb[3:9] = 1e-45
+    c = randn((M, N), F32, M, N, 104).to(dtype)
+    c[:, 5] = float("inf")
+    c[-1] = float("-inf")
+    c[:, 6] = 0
+    with np.errstate(all="ignore"):
+        want = matmul_ref(a, sa, b, sb, dtype, c if accumulate else None)
+    assert same(B.moe_matmul_i8(a, sa, b, sb, c=c, accumulate=accumulate), want)
+
+
+def test_rows_of_tiny_and_huge_values():
+    """Rows whose scale has no normal float32, and rows next to its largest: the rule in float32 on the call's own values."""
+    n = 320
+    x = randn((9, n), F32, 105)
+    w = torch.ones(n, device=DEV)
+    for power in (-149, -146, -140, -133, -127, -120, -100, 0, 100, 125):
+        w.fill_(2.0 ** power)
+        w[::7] *= 0.5
+        y, blocks = torch.empty_like(x), torch.empty((9, n // 32 * 36), dtype=torch.uint8, device=DEV)
+        q, d = B.i8_rows(9, n, DEV)
+        B.moe_add_rmsnorm(x, w, 1e-6, y=y, q=q, scale=d, q8_1=blocks)
+        want = norm_ref(host(x), host(w), float(np.float32(1e-6))).astype(np.float32)
+        assert (np.abs(host(y) - want) <= np.abs(want) * 2.0 ** -23 + TINY[F32]).all()
+        codes, scale = code_rule(y.cpu().numpy(), 1)
+        assert np.array_equal(q.cpu().numpy(), codes) and np.array_equal(d.cpu().numpy(), scale)
+        assert torch.equal(blocks, B.moe_quantize_q8_1(y))
+        for dtype in (BF16, F16):
+            z = torch.empty((9, n), dtype=dtype, device=DEV)
+            B.moe_add_rmsnorm(x, w, 1e-6, y=z)
+            assert torch.equal(z.cpu(), y.cpu().to(dtype))
+        # 1 + exp(-90) is 1 in 64 bits, so h is 90 u there
+        g = torch.full_like(y, 90.0)
+        q, d = B.moe_swiglu_i8(g, y / 128)
+        codes, scale = code_rule((host(y / 128) * 90).astype(np.float32), 1)
+        assert np.array_equal(q.cpu().numpy(), codes) and np.array_equal(d.cpu().numpy(), scale)
+
+
+@pytest.mark.parametrize("k", [6, 20])
+@pytest.mark.parametrize("groups,keep,top", [(1, 1, 1), (4, 2, 2)])
+def test_route_values_that_64_bits_cannot_tell_apart(groups, keep, top, k):
+    """Logits below the smallest normal float32 order as they are; biases that swallow the scores leave ties."""
+    g = synth.rng(106)
+    tiny = torch.from_numpy((g.integers(-40, 41, (9, 64)) * 2.0 ** -149).astype(np.float32)).to(DEV)
+    check_route(tiny, k, SOFT, None, groups, keep, top)
+    check_route(tiny, k, SIG, None, groups, keep, top)
+    logits = randn((9, 64), F32, 107)
+    for value in (1e18, -1e18, 3.4e38, -3.4e38, 2.0 ** 54, 2.0 ** 30):
+        bias = torch.full((64,), value, device=DEV)
+        bias[::5] = 0.5
+        check_route(logits, k, SIG, bias, groups, keep, top)
+        check_route(logits, k, SOFT, bias, groups, keep, top, False, -1.5)
+
+
+def test_as_many_rows_as_a_call_takes():
+    rows = 4194303
+    g = torch.Generator(device=DEV).manual_seed(108)
+    x = torch.randn((rows, 16), generator=g, device=DEV).to(BF16)
+    w, part = torch.ones(16, device=DEV), slice(rows - 1000, rows)
+    q, d = B.i8_rows(rows, 16, DEV)
+    B.moe_add_rmsnorm(x, w, 1e-6, q=q, scale=d)
+    q1, d1 = B.i8_rows(1000, 16, DEV)
+    B.moe_add_rmsnorm(x[part], w, 1e-6, q=q1, scale=d1)
+    assert torch.equal(q[part], q1) and torch.equal(d[part], d1)
+    assert bool((q.abs().amax(1) == 127).all())
+    q, d = B.moe_swiglu_i8(x, x)
+    q1, d1 = B.moe_swiglu_i8(x[part], x[part])
+    assert torch.equal(q[part], q1) and torch.equal(d[part], d1)
+    assert bool((q.abs().amax(1) == 127).all())
+    first = torch.where(x == x.amax(1, keepdim=True), torch.arange(16, device=DEV), 16).amin(1).int()
+    for k, groups in ((1, 1), (2, 1), (1, 16), (2, 8)):
+        ids, v = B.moe_route_scores(x, k, n_groups=groups, keep_groups=groups)
+        assert torch.equal(ids[:, 0], first) and bool((v.sum(1) - 1).abs().max() < 2.0 ** -22)
