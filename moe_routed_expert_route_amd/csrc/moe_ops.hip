@@ -1529,7 +1529,9 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
   const int in16 = 16 / type_size(p.c_dtype);   // values of 16 bytes
   p.wide = (in16 == 4 || !p.accumulate) && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % in16 == 0 && p.N % in16 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
-  // up to 32 tokens where K is short: 32 x 2560, K = 768 3.7 us, and 4.4 in tiles; K = 2560 10.8 and 7.3
+  // Up to 16 tokens: 16 x 1536, K = 2560 4.7 us, and 5.7 in tiles; 16 x 2560, 768 3.3 and 4.4; 16 x 7936, 2560 8.2 and
+  // 7.8; 16 x 8448, 2560 10.1 and 10.4. Up to 32 where K is short: 32 x 2560, 768 3.6 and 4.4; 32 x 5120, 768 4.7 and 4.4;
+  // 32 x 4352, 2560 10.0 and 7.1.
   const bool launches = p.N <= kLaunchThreads / 512 * 16;   // 512 threads for 16 channels
   if (p.M <= 16 || (p.M <= 32 && p.K <= 1024 && launches)) {
     if (!launches) return MOE_E_SHAPE;
@@ -1537,9 +1539,18 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
       hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)p.N + channels - 1) / channels)), dim3(threads), 0, st, p);
       return launched("moe_matmul_i8");
     };
-    // as few pieces of K side by side as leave two workgroups a CU
-    if (p.M <= 4 && p.N < 8 * 512) return go(k_matmul_thin<1, 4, 8>, 4, 512);
-    if (p.M <= 8 && p.N < 16 * 512) return go(k_matmul_thin<1, 2, 8>, 8, 512);
+    // Pieces of K side by side: more, and fewer channels a workgroup, where K is long and 256 CUs are not filled. us
+    // by 1, 2 and 4 pieces (M x N, K): 1 x 1024, 8192 6.8 4.8 4.1; 1 x 1024, 1280 3.1 2.9 3.4; 1 x 1536, 2560 3.8 3.5 3.7;
+    // 8 x 1536, 2560 4.3 3.8 -; 1 x 2560, 768 3.0 3.2 3.9; 4 x 2560, 2560 4.1 4.5 4.6; 1 x 2560, 8192 8.6 8.2 7.4;
+    // 1 x 5120, 8192 14.2 11.1 10.9; 8 x 5120, 4096 9.6 8.6 -; 1 x 7936, 1024 3.9 4.1 6.2; 1 x 8448, 2560 7.8 - 9.2.
+    int pieces = 1;
+    if (p.M <= 8 && p.K >= 1024) {
+      if (p.N <= 2048) pieces = p.M <= 4 && p.N <= 1024 && p.K >= 2048 ? 4 : 2;
+      else if (p.N < 4096) pieces = p.K < 4096 ? 1 : p.M <= 4 ? 4 : 2;
+      else if (p.N < 8192) pieces = 2;
+    }
+    if (pieces == 4) return go(k_matmul_thin<1, 4, 8>, 4, 512);
+    if (pieces == 2) return go(k_matmul_thin<1, 2, 8>, 8, 512);
     if (p.M <= 16) return go(k_matmul_thin<1, 1, 8>, 16, 512);
     return go(k_matmul_thin<2, 1, 8>, 16, 512);
   }

@@ -895,3 +895,10 @@ def test_as_many_rows_as_a_call_takes():
     for k, groups in ((1, 1), (2, 1), (1, 16), (2, 8)):
         ids, v = B.moe_route_scores(x, k, n_groups=groups, keep_groups=groups)
         assert torch.equal(ids[:, 0], first) and bool((v.sum(1) - 1).abs().max() < 2.0 ** -22)
+
+
+@pytest.mark.parametrize("M", [1, 4, 5, 8])
+@pytest.mark.parametrize("N", [1024, 1025, 2048, 2049, 4095, 4096, 8191, 8192])
+@pytest.mark.parametrize("K", [1023, 1024, 2047, 2048, 4095, 4096])
+def test_matmul_few_tokens_next_to_the_sizes_that_decide(M, N, K):
+    check_matmul(i8((M, K), M, K, 110), i8((N, K), N, K, 111), BF16)
