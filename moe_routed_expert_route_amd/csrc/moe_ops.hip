@@ -414,13 +414,14 @@ __device__ __forceinline__ float swiglu64(float g, float u) {
 
 // The codes need h's last bits only next to a code's border, and the row's scale those of its largest value.
 // So every h is first taken in float32, within 2^-20 relative: t = -g log2(e) in two parts, exp2 of the
-// large one (2^-23) times 1 + ln(2) of the small, 1 / (1 + e) (rcp: 2^-23) and five roundings of 2^-24, under
-// 2^-21 in all, and h's own rounding. The values within 2^-18 of the largest are taken again in 64 bits and
-// give the scale; so is a value whose quotient lies within 2^-19 of its size, plus 2^-17, of a half-integer:
-// the errors of the value, of rcp and of the float32 quotient come to 2^-20 + 2^-22 of it. Pieces with a
-// value that the bound leaves out (exp2 past 2^100, a product below 2^-100 or not below 2^126) go in 64 bits
-// altogether. Every result is that of 64 bits throughout, which took 38 us for 4096 x 5632 bf16; this
-// takes 34 (3.4 TB/s). The pieces stay in their type in between: occupancy.
+// large one (2^-23) times 1 + ln(2) of the small, 1 / (1 + e) (rcp: 2^-23) and roundings of 2^-24 in the
+// product of the parts, 1 + e, times g, times u and h in 64 bits: 4.5 * 2^-23 in all, and 8 * 2^-23 is allowed.
+// The values within 2^-18 of the largest are taken again in 64 bits and give the scale; so is a value whose
+// quotient lies within 2^-19 of its size, plus 2^-17, of a half-integer: the errors of the value, of rcp and of
+// the float32 quotient come to 2^-20 + 2^-22 of it. Pieces with a value that the bound leaves out (exp2 past
+// 2^100, a product below 2^-100 or not below 2^126) go in 64 bits altogether. Every result is that of 64 bits
+// throughout, which took 38 us for 4096 x 5632 bf16; this takes 34.5 (3.4 TB/s). The pieces stay in their type
+// in between: occupancy.
 template <typename T, int THREADS, int C>
 __global__ __launch_bounds__(THREADS) void k_swiglu_i8(SwigluArgs a) {
   __shared__ uint32_t s_near[THREADS / 64], s_max[THREADS / 64];
@@ -1331,7 +1332,7 @@ __global__ __launch_bounds__(64 * WT * WC * KG) void k_matmul_tile(MatmulArgs p)
 // channels a workgroup: with P > 1 (M <= C) the instruction's 16 rows are C channels at P neighbouring
 // pieces of K and its 16 columns the tokens at the same pieces; the blocks of its result where the
 // two pieces agree are partial sums of the product. Few channels then still fill the chip. Bound by the
-// launch (1 x 1536 x 2560: 3.7 us) or the weights' bytes (1 x 8192 x 8192: 16.5 us, 4.1 TB/s); 16 tokens of
+// launch (1 x 1536 x 2560: 3.5 us) or the weights' bytes (1 x 8192 x 8192: 16.5 us, 4.1 TB/s); 16 tokens of
 // 1536 x 2560 4.7 us.
 template <int MT, int P, int W>
 __global__ __launch_bounds__(64 * W) void k_matmul_thin(MatmulArgs p) {
@@ -1456,7 +1457,11 @@ bool overlap(const Rows& a, const Rows& b) {
   return shift < x.len || shift + y.len > x.step;
 }
 
-// A row call's type and workgroup: by the row length alone, so that a row's sums have one order.
+// A row call's type and workgroup: by the row length alone, so that a row's sums have one order. Two pieces a
+// thread above 2048 values, one below. us for 8192 bf16 rows, norm / SwiGLU: 512 wide 64 x 1 11.7 / 9.5, 128 x 1
+// 13.0 / 11.2; 1024 wide 128 x 1 18.0 / 14.6, 64 x 2 18.4 / 15.7; 2048 wide 256 x 1 28.9 / 22.5, 128 x 2 30.4 /
+// 24.6; 2560 wide 256 x 2 40.3 / 32.9, 512 x 1 44.6 / 33.8; 4096 wide 52.1 / 41.1, 512 x 1 54.1 / 41.3; 5120
+// wide, norm 512 x 2 69.6, 1024 x 1 78.6. One float32 row of 2560 has it the other way: 3.5, 512 x 1 3.2.
 template <typename F>
 void with_row(int dtype, int n, F f) {
   auto size = [&](auto t) {
@@ -1482,7 +1487,8 @@ constexpr int64_t kLaunchThreads = 0xFFFFFFFFll;   // of one launch, at most
 // A tile's cost is its time over K (the one measured: K = 2560, one round of up to 256 tiles, us) times
 // the rounds that 256 CUs need. Small tiles bring the chip's CUs to a small product (512 x 1536: 64 x 64
 // 8.2 us, 128 x 128 14.2, 256 x 256 34), large ones read less for each product of a large one (8192 x
-// 1536: 256 x 256 51 us, 64 x 64 72). The largest tile takes the fewest threads for any product.
+// 1536: 256 x 256 51 us, 64 x 64 72). Rounds count one workgroup a CU, though the three small tiles leave room for
+// two. The largest tile takes the fewest threads for any product.
 struct Tile {
   int bt, bc, threads;
   double us;
@@ -1529,9 +1535,9 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
   const int in16 = 16 / type_size(p.c_dtype);   // values of 16 bytes
   p.wide = (in16 == 4 || !p.accumulate) && aligned(p.sb, 16) && aligned(p.c, 16) && p.ldc % in16 == 0 && p.N % in16 == 0;
   p.vec = aligned(p.sb, 16) && aligned(p.c, 4 * type_size(p.c_dtype)) && p.ldc % 4 == 0;
-  // Up to 16 tokens: 16 x 1536, K = 2560 4.7 us, and 5.7 in tiles; 16 x 2560, 768 3.3 and 4.4; 16 x 7936, 2560 8.2 and
-  // 7.8; 16 x 8448, 2560 10.1 and 10.4. Up to 32 where K is short: 32 x 2560, 768 3.6 and 4.4; 32 x 5120, 768 4.7 and 4.4;
-  // 32 x 4352, 2560 10.0 and 7.1.
+  // Up to 16 tokens: 16 x 1536, K = 2560 4.7 us, and 5.7 in tiles; 16 x 2560, 768 3.3 and 4.4; 16 x 7936, 2560 8.2
+  // and 7.8; 16 x 8448, 2560 10.1 and 10.4. Up to 32 where K is short: 32 x 2560, 768 3.6 and 4.4; 32 x 5120, 768 4.7
+  // and 4.4; 32 x 4352, 2560 10.0 and 7.1.
   const bool launches = p.N <= kLaunchThreads / 512 * 16;   // 512 threads for 16 channels
   if (p.M <= 16 || (p.M <= 32 && p.K <= 1024 && launches)) {
     if (!launches) return MOE_E_SHAPE;
@@ -1539,10 +1545,11 @@ int run_matmul(hipStream_t st, MatmulArgs p) {
       hipLaunchKernelGGL(kern, dim3((unsigned)(((int64_t)p.N + channels - 1) / channels)), dim3(threads), 0, st, p);
       return launched("moe_matmul_i8");
     };
-    // Pieces of K side by side: more, and fewer channels a workgroup, where K is long and 256 CUs are not filled. us
-    // by 1, 2 and 4 pieces (M x N, K): 1 x 1024, 8192 6.8 4.8 4.1; 1 x 1024, 1280 3.1 2.9 3.4; 1 x 1536, 2560 3.8 3.5 3.7;
-    // 8 x 1536, 2560 4.3 3.8 -; 1 x 2560, 768 3.0 3.2 3.9; 4 x 2560, 2560 4.1 4.5 4.6; 1 x 2560, 8192 8.6 8.2 7.4;
-    // 1 x 5120, 8192 14.2 11.1 10.9; 8 x 5120, 4096 9.6 8.6 -; 1 x 7936, 1024 3.9 4.1 6.2; 1 x 8448, 2560 7.8 - 9.2.
+    // Pieces of K side by side: more, and fewer channels a workgroup, where K is long and 256 CUs are not filled.
+    // us by 1, 2 and 4 pieces (M x N, K): 1 x 1024, 8192 6.8 4.8 4.1; 1 x 1024, 1280 3.1 2.9 3.4; 1 x 1536, 2560 3.8
+    // 3.5 3.7; 8 x 1536, 2560 4.3 3.8 -; 1 x 2560, 768 3.0 3.2 3.9; 4 x 2560, 2560 4.1 4.5 4.6; 1 x 2560, 8192 8.6
+    // 8.2 7.4; 1 x 5120, 8192 14.2 11.1 10.9; 8 x 5120, 4096 9.6 8.6 -; 1 x 7936, 1024 3.9 4.1 6.2; 1 x 8448, 2560
+    // 7.8 - 9.2.
     int pieces = 1;
     if (p.M <= 8 && p.K >= 1024) {
       if (p.N <= 2048) pieces = p.M <= 4 && p.N <= 1024 && p.K >= 2048 ? 4 : 2;
@@ -1628,7 +1635,9 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
     if (overlap(out[0], r) || overlap(out[1], r)) return MOE_E_ARG;
   const RouteArgs a{logits, bias, ids, w, ld, dtype, E, k, score, n_groups, keep_groups, group_top, renorm, factor};
   // Lists in registers where a group is whole lanes and a lane's share is up to 32 experts (16384 x 256: 10 us
-  // by logits, 22 by scores in groups; 119 and 126 by one wave a token).
+  // by logits, 22 by scores in groups; 118 and 124 by one wave a token). The least V and KL that hold the share and
+  // k: 16384 tokens of 64 / 128 / 256 experts 6.7 / 7.6 / 10.2 us, with the next V 7.6 / 9.1 / 14.1, with KL 16 for k = 8
+  // 9.1 / 10.2 / 12.8.
   // Few tokens of scored experts take 64 lanes each, which spread the scores' 64-bit arithmetic (the bits are the
   // same: softmax's sum does not round): 512 x 256 10.4 -> 6.7 us, 2048 x 256 11.0 -> 8.1, 4096 x 256 11.6 -> 11.5;
   // 1024 x 128 6.6 -> 5.9, 4096 x 128 7.3 -> 9.5; 512 x 64 5.0 -> 5.3.
