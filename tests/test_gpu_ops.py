@@ -902,3 +902,25 @@ def test_as_many_rows_as_a_call_takes():
 @pytest.mark.parametrize("K", [1023, 1024, 2047, 2048, 4095, 4096])
 def test_matmul_few_tokens_next_to_the_sizes_that_decide(M, N, K):
     check_matmul(i8((M, K), M, K, 110), i8((N, K), N, K, 111), BF16)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("M", [2, 7, 14, 40, 300, 1024])
+@pytest.mark.parametrize("offsets", [(0, 1, 0, 0, 0), (1, 0, 0, 0, 0), (0, 0, 4, 0, 0), (0, 0, 0, 8, 0), (0, 0, 0, 0, 4), (3, 2, 16, 16, 1)])
+def test_matmul_operands_at_any_place(offsets, M, dtype):
+    """Scales, rows and C each at an alignment of its own."""
+    N, K = 264, 272
+    osa, osb, oa, ob, oc = offsets
+    sa, sb = torch.rand(M + osa, device=DEV)[osa:] + 0.5, torch.rand(N + osb + 1, device=DEV)[osb:osb + N]
+    a, b = rows_in(M, K, torch.int8, K, oa)[0], rows_in(N, K, torch.int8, K, ob)[0]
+    a.copy_(i8((M, K), M, 112))
+    b.copy_(i8((N, K), N, 113))
+    c, buf = rows_in(M, N, dtype, N, oc, 7)
+    B.moe_matmul_i8(a, sa, b, sb, c=c)
+    want = matmul_ref(a, sa, b, sb, dtype)
+    assert torch.equal(c.cpu(), want)
+    B.moe_matmul_i8(a, sa, b, sb, c=c, accumulate=True)
+    twice = matmul_ref(a, sa, b, sb, dtype, want)
+    assert torch.equal(c.cpu(), twice)
+    c.fill_(7)
+    assert (buf == 7).all()
