@@ -7,7 +7,7 @@
         --counters DIR1/run_counter_collection.csv ... --command "..."
 
 `run` makes PASSES passes of each case that perf/operators.py lists and of the products in MORE, on two
-inputs in turn; first as they come (small inputs are in a cache then), then each after a fill of 1 GiB that leaves
+inputs in turn; first as they come (small inputs are in a cache then), then each after 1 GiB was read, which leaves
 none of them there. `table` writes profiles/kernels_ops.md: the library's launches alone, medians, and the
 counters per launch (--counters: one pass of the cases in COUNTED, after a copy of known size).
 """
@@ -72,7 +72,8 @@ def run(counters):
     if counters:
         src = torch.zeros(CALIB_BYTES, dtype=torch.uint8, device="cuda")
         torch.empty_like(src).copy_(src)
-    flush = torch.empty(0 if counters else 1 << 30, dtype=torch.uint8, device="cuda")
+    other = torch.zeros(16 if counters else 1 << 30, dtype=torch.uint8, device="cuda")
+    sums = torch.empty(1024, dtype=torch.int32, device="cuda")
     for case in cases():
         if counters and case["name"] not in COUNTED:
             continue
@@ -80,16 +81,16 @@ def run(counters):
         for cold in (False,) if counters else (False, True):
             for i in range(1 if counters else PASSES):
                 if cold:
-                    flush.fill_(i)
+                    B.moe_stream_read(other, sums, 1024)   # a fill would leave lines to write back
                 one(case, states[i % 2])
         torch.cuda.synchronize()
         print(case["name"], flush=True)
 
 
 def launches(trace_csv):
-    """The library's launches of a kernel trace in order: (kernel, workgroups, threads, us)."""
+    """The operators' launches of a kernel trace in order: (kernel, workgroups, threads, us)."""
     with open(trace_csv, newline="") as f:
-        rows = [r for r in csv.DictReader(f) if "moe::k_" in r["Kernel_Name"]]
+        rows = [r for r in csv.DictReader(f) if "moe::k_" in r["Kernel_Name"] and "k_stream_read" not in r["Kernel_Name"]]
     rows.sort(key=lambda r: int(r["Start_Timestamp"]))
     return [(re.sub(r"moe::|^void |\(.*", "", r["Kernel_Name"]), int(r["Grid_Size_X"]) // int(r["Workgroup_Size_X"]),
              int(r["Workgroup_Size_X"]), (int(r["End_Timestamp"]) - int(r["Start_Timestamp"])) / 1e3) for r in rows]
@@ -101,7 +102,7 @@ def table(trace_csv, counter_csvs, command):
         raise ValueError(f"{len(runs)} launches, not {2 * PASSES} of each of {len(cases())} cases")
     lines = ["# Kernel trace of the operators around the layer", "", "Commands (repo root, one MI355X):", "", f"    {command}", "",
              f"The library's launches alone, median and least of the last {PASSES - 2} of {PASSES}: as they come (small inputs are in a "
-             "cache), and cold, each after a fill of 1 GiB. GB/s and T(FL)OP/s go by the cold median and by the bytes and operations that the "
+             "cache), and cold, each after 1 GiB was read. GB/s and T(FL)OP/s go by the cold median and by the bytes and operations that the "
              "case cannot do without.", "",
              "| case | kernel | workgroups × threads | median µs | least µs | cold µs | GB/s | T(FL)OP/s |", "|---|---|---|---|---|---|---|---|"]
     for i, case in enumerate(cases()):

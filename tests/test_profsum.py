@@ -72,7 +72,7 @@ def test_ops_table(tmp_path, monkeypatch):
             dur = 4000 + 100 * i if p < opsprof.PASSES else 8000 + 100 * i
             if p in (0, 1, opsprof.PASSES):          # the first two of each kind do not count
                 dur = 90000
-            rows += [["at::native::fill(x)", at - 500, at - 400, 256, 2560],
+            rows += [["moe::k_stream_read(x)", at - 500, at - 400, 256, 2560],
                      [f"void moe::k_case{i}<moe::bf16_t, 4>(moe::Args)", at, at + dur, 128, 128 * (i + 1)]]
             at += 100000
     hdr = ["Kernel_Name", "Start_Timestamp", "End_Timestamp", "Workgroup_Size_X", "Grid_Size_X"]
