@@ -1452,9 +1452,10 @@ bool overlap(const Rows& a, const Rows& b) {
   const Rows &x = (uintptr_t)a.p <= (uintptr_t)b.p ? a : b, &y = &x == &a ? b : a;   // x starts first
   const uint64_t gap = (uintptr_t)y.p - (uintptr_t)x.p;
   if (gap >= (uint64_t)((x.rows - 1) * x.step + x.len)) return false;
-  if (x.step != y.step) return true;
-  const int64_t shift = (int64_t)(gap % (uint64_t)x.step);   // of y's columns
-  return shift < x.len || shift + y.len > x.step;
+  if (x.rows > 1 && y.rows > 1 && x.step != y.step) return true;
+  const int64_t step = x.rows > 1 ? x.step : y.step;      // one row has the other's
+  const int64_t shift = (int64_t)(gap % (uint64_t)step);   // of y's columns
+  return shift < x.len || shift + y.len > step;
 }
 
 // A row call's type and workgroup: by the row length alone, so that a row's sums have one order. Two pieces a

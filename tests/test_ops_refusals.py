@@ -170,3 +170,14 @@ def test_one_row_of_any_stride_overlaps_by_its_bytes(q, want):
 def test_route_factor_has_to_be_finite(factor):
     """A masked token's weights are 0, which no infinite factor leaves."""
     assert B.lib().moe_route_scores(None, *dict(ROUTE, factor=factor).values()) == ARG
+
+
+@pytest.mark.parametrize("c,want", [(P3 + 64, HIP), (P3 + 192, HIP), (P3 + 62, ARG), (P3 + 194, ARG), (P3 + 256, ARG), (P3 + 31 * 256 + 64, HIP),
+                                    (P3 - 64, HIP), (P3 - 62, ARG)])
+@pytest.mark.skipif(torch.cuda.is_available(), reason="would launch kernels on pointers that are fakes")
+def test_one_row_of_results_between_the_rows_of_an_input(c, want):
+    """Rows of 64 bytes, 256 apart, and one row of C of 64 bytes, whatever its stride."""
+    for ldc in (32, 128, 1000):
+        assert B.lib().moe_matmul_i8(None, *dict(MATMUL, M=1, ldb=256, c=c, ldc=ldc).values()) == want
+    args = dict(NORM, rows=1, res=None, res_out=P, ldro=100, y=None, q=None, scale=None)   # in place, its one row
+    assert B.lib().moe_add_rmsnorm(None, *args.values()) == HIP
