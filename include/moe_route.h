@@ -320,9 +320,9 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * dense half that every token takes) in 8-bit integers. Each call takes one token or thousands.
  *
  * Conventions beside those at the top: row strides (ld*) count elements and are at least the row
- * length and at most MOE_MAX_SPAN / rows; any such stride and any row alignment an element type allows is
- * accepted (16-byte aligned rows are fastest). Row elements past the row length and rows past the last are neither read nor
- * written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
+ * length and at most MOE_MAX_SPAN / rows; any such stride and any row alignment an element type
+ * allows is accepted (16-byte aligned rows are fastest). Row elements past the row length and rows
+ * past the last are neither read nor written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
  * NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
  * as their outputs do not. Outputs may not overlap inputs or each other unless a comment says so (rows of
  * one buffer side by side, of one stride, do not). Results do not depend on the number of rows of the
@@ -378,8 +378,8 @@ int moe_route_scores(void* stream, int dtype, const void* logits, int64_t ld, in
                      float factor, int32_t* ids, float* w);
 
 /* SwiGLU into i8 rows, beside moe_swiglu_q8_1: h = float32(g / (1 + exp(-g)) * u), evaluated in 64 bits
- * (within 2^-50 of its size) and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in `dtype` of strides ldg
- * and ldu (the two halves of one product's rows: u = g + n, both strides that product's).
+ * (within 2^-50 of its size) and rounded once, per row of n; q, scale = i8 rows of h. g and u: rows in
+ * `dtype` of strides ldg and ldu (the two halves of one product's rows: u = g + n, both strides that product's).
  * Errors: MOE_E_ARG (null or misaligned pointer, bad type or stride, overlap), MOE_E_SHAPE (n not in
  * 1..MOE_MAX_ROW, rows > MOE_MAX_ROWS). */
 int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const void* u, int64_t ldu, int rows,
