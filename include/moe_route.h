@@ -109,6 +109,9 @@ typedef enum {
 #define MOE_ERR_ALIGN 32u    /* a weight pointer not 2-byte aligned: that group skipped */
 #define MOE_ERR_WAIT 64u     /* moe_layer_step: a workgroup gave up waiting for the others (its
                                 down tiles were not written); see moe_layer_step */
+/* Of the calls on a moe_window, into *window->err: */
+#define MOE_ERR_WINDOW 128u  /* a sequence's rows, window or context out of range: it was left out */
+#define MOE_ERR_PAGE 256u    /* a page out of [0, n_pages): its keys were left out */
 
 /* One MoE layer's experts. Host struct, read during the call only. */
 typedef struct moe_layer {
@@ -332,7 +335,7 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * the q8_1 rule with the row as the block: d = max|y| / 127 (float32), q = clamp(round-half-away(
  * y / d), +-127) with the float32 quotient; d = 0 gives zero codes; a row holding an infinity or a
  * NaN gives d = NaN and zero codes. The value a code stands for is q * d. */
-typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3 } moe_dtype;   /* element types of rows */
+typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3, MOE_I8 = 4 } moe_dtype;   /* element types of rows; MOE_I8: of a cache alone */
 #define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
 #define MOE_MAX_ROWS 4194303      /* max rows of those and tokens of moe_route_scores (a launch's threads) */
 #define MOE_MAX_SPAN (1ll << 50)  /* max rows x stride of one operand, elements: more than any memory */
@@ -397,6 +400,108 @@ int moe_swiglu_i8(void* stream, int dtype, const void* g, int64_t ldg, const voi
  * of 256 x 256 values of C, ragged ones counted whole: 5 * 10^11 values). */
 int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, const int8_t* b, int64_t ldb,
                   const float* sb, int M, int N, int K, int c_dtype, void* C, int64_t ldc, int accumulate);
+
+/* ---- The attention half beside the layer, for windows of tokens (a decode step's one token, a tree of drafted tokens to
+ * verify, a prompt) of many sequences at once, over a paged cache of keys and values; and the scores of the answers.
+ *
+ * Conventions beside those above: what differs from sequence to sequence is read on the device, so a captured call
+ * follows its lengths, pages, positions and masks. Offsets into the cache are 64-bit. The calls that take a workspace
+ * need nothing in it beforehand and leave nothing for the next; calls that overlap need one each. A call of no tokens
+ * or no sequences does nothing and succeeds. Problems that only the device sees are OR-ed into *window->err:
+ * MOE_ERR_WINDOW: a sequence whose rows are not in ascending order within [0, n_tokens), whose window is longer than
+ * max_window (attention only) or whose context is negative or does not fit its pages: the sequence is left out, its
+ * rows as they were. MOE_ERR_PAGE: a page out of [0, n_pages): its keys are not written, and nobody sees them. */
+
+/* A layer's cache. Row (page p, head h, slot i) of k and of v starts p * page_stride + h * head_stride + i *
+ * slot_stride elements from k and v and holds head_dim elements; strides are positive multiples of 16 of either nesting order, and
+ * rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k and v are 16-byte aligned.
+ * dtype MOE_BF16, MOE_F16, or MOE_I8: i8 rows, one scale a row at [(p * n_kv + h) * page_size + i] of k_scale and v_scale
+ * (NULL for the others). page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple of 16 up to 256; n_kv up to
+ * MOE_MAX_HEADS. Host struct holding device pointers. */
+#define MOE_MAX_PAGE 65536
+#define MOE_MAX_HEADS 1024
+#define MOE_MAX_SEQS 4096
+#define MOE_MAX_WINDOW 64         /* tokens of one sequence in moe_window_attention */
+typedef struct moe_kv_cache {
+  int32_t dtype, n_pages, page_size, n_kv, head_dim;
+  int64_t page_stride, head_stride, slot_stride;
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+} moe_kv_cache;
+
+/* The tokens of one call. Sequence s has rows row_start[s] .. row_start[s + 1] - 1 of the call's n_tokens rows (rows of
+ * no sequence, such as padding behind the last, are neither read nor written) and ctx_len[s] keys before them in its
+ * pages: key i is slot i % page_size of page pages[s * ld_pages + i / page_size], and the window's token j is key
+ * ctx_len[s] + j. Pages may be shared between sequences where nothing is written to them. max_pages <= ld_pages columns are
+ * read at most, max_pages * page_size < 2^31. max_window: the most tokens of a sequence. pos (NULL: the token's key
+ * index): rotary position of each row. seen (NULL: token j sees tokens 0 .. j): bit i of seen[row] set = the row's
+ * token sees token i of its window (its own bit too); bits past the window count nothing; every token sees the
+ * whole context. Host struct holding device pointers. */
+typedef struct moe_window {
+  int32_t n_seqs, n_tokens, max_window, max_pages;
+  int64_t ld_pages;
+  const int32_t* row_start;      /* [n_seqs + 1] */
+  const int32_t* ctx_len;        /* [n_seqs] */
+  const int32_t* pages;          /* [n_seqs][ld_pages] */
+  const int32_t* pos;            /* [n_tokens] or NULL */
+  const uint64_t* seen;          /* [n_tokens] or NULL */
+  uint32_t* err;
+} moe_window;
+
+/* Norm and rotation of the window's queries and keys, and its keys and values into the cache. Per row and head, in 64 bits:
+ *   x = x * w / sqrt(mean(x^2) + eps)  over the head_dim values of a query or key (q_weight, k_weight [head_dim] in
+ *   w_dtype; NULL: no norm);
+ *   its first n_rot values in pairs, (i, i + n_rot / 2) for MOE_ROPE_HALF or (2 i, 2 i + 1) for MOE_ROPE_PAIRS, turn by
+ *   the angle t = pos * freq[i] (the float64 product): (a, b) -> amp * (a cos t - b sin t, b cos t + a sin t);
+ *   rounded to float32 and then to o_dtype (queries, q_out) or to the cache's type (i8 rows: of the float32 row).
+ * Values are converted alone. freq float32 [n_rot / 2] (whatever scaling a long context takes is in it and in amp) may
+ * be NULL when n_rot = 0; an angle of 2^40 or more gives NaN. q [n_tokens][ldq] of n_heads heads side by side, k
+ * and v [n_tokens][ldk], [ldv] of n_kv (the parts of one product's rows, say), all `dtype`. q and q_out may both be NULL;
+ * q_out may be the very rows of q. Windows of any length; max_window is not read.
+ * Errors: MOE_E_ARG (null or misaligned pointer, bad type, stride, layout, eps or amp not finite, overlap), MOE_E_SHAPE
+ * (sizes out of the limits above, n_rot odd or past head_dim, n_heads not a multiple of n_kv). */
+typedef enum { MOE_ROPE_HALF = 1, MOE_ROPE_PAIRS = 2 } moe_rope;
+int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
+                      const void* k, int64_t ldk, const void* v, int64_t ldv, int n_heads, int w_dtype, const void* q_weight,
+                      const void* k_weight, float eps, const float* freq, int n_rot, int layout, float amp, int o_dtype,
+                      void* q_out, int64_t ldqo);
+
+/* Attention of the window's queries over the cache, the window's own keys (appended before) among them: per row and
+ * head, over the keys that the row sees,
+ *   s_i = scale * q . k_i,  out = sum exp(s_i) v_i / sum exp(s_i),  lse = log sum exp(s_i)   (lse NULL: not wanted).
+ * A row that sees nothing gets out = 0 and lse = -infinity. Keys that a row does not see, and slots past the last key, count
+ * for nothing whatever they hold (infinities and NaN too). Head h reads the cache's head h / (n_heads / n_kv).
+ * q, out [n_tokens][ldq], [ldo] in `dtype`: the cache's type, or MOE_BF16 or MOE_F16 over an i8 cache; lse float32
+ * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max), times the value's scale over an i8
+ * cache, is rounded to `dtype` in front of its product, and the sum below is of the unrounded ones.
+ * A sequence's keys are summed in runs whose length depends on its own key count and on max_window * n_heads /
+ * n_kv being above 32 or not: a token's bits depend neither on the call's other sequences nor on the other tokens of its window.
+ * workspace: moe_window_attention_bytes, 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type or
+ * stride, scale not finite, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
+ * not a multiple of n_kv), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
+size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, int n_heads);   /* host */
+int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
+                         int n_heads, float scale, void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes);
+
+/* Log probabilities under softmax(scale * logits), row by row (the tokens that a window drafted, a prompt's own, the best
+ * alternatives), beside moe_route_scores:
+ *   logp[r][j] = log p(tokens[r][j]) (-infinity for an id out of [0, n): no token);  entropy[r] = -sum p log p;
+ *   top_ids[r], top_logp[r] = the k tokens of the largest logits, largest first, ties to the lower id, and their log p.
+ * A logit of -infinity or NaN masks its token: p = 0, log p = -infinity, and it comes after every unmasked one in the order, lowest
+ * id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. scale > 0.
+ * Each output is written when its pointer is not NULL (tokens and logp, given > 0: all or none; top_ids and top_logp, k > 0:
+ * all or none; at least one output). logits [rows][ld] in `dtype`, tokens int32 [rows][given]. n <= MOE_MAX_VOCAB,
+ * given <= 64, k <= 32 and k <= n. Sums of up to 256 terms in float32, of those in 64 bits; a row's bits do not depend on the others.
+ * workspace: moe_token_logprobs_bytes, 16-byte aligned (0 bytes and NULL if that says so). Errors: MOE_E_ARG (null or
+ * misaligned pointer, bad type, stride, count or scale, overlap), MOE_E_SHAPE (rows > MOE_MAX_ROWS, n not in
+ * 1..MOE_MAX_VOCAB), MOE_E_WS. */
+#define MOE_MAX_VOCAB (1 << 22)
+size_t moe_token_logprobs_bytes(int rows, int n, int k);   /* host */
+int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, int rows, int n, float scale,
+                       const int32_t* tokens, int given, float* logp, float* entropy, int k, int32_t* top_ids,
+                       float* top_logp, void* workspace, size_t ws_bytes);
 
 /* The achievable-bandwidth reference the decode launches are measured against (not a step of the
  * method): one launch of `grid` workgroups of 256 threads reads the `bytes` at buf once with

@@ -18,7 +18,8 @@ Q8_0, NL4, CB2, CB3, Q5_1, NL4X = 1, 2, 3, 4, 5, 6
 BLOCK_BYTES = {Q8_0: 34, NL4: 18, CB2: 70, CB3: 110, Q5_1: 24, NL4X: 136}
 BLOCK_WEIGHTS = {Q8_0: 32, NL4: 32, CB2: 256, CB3: 256, Q5_1: 32, NL4X: 256}
 
-ERR_BITS = {1: "NGROUPS", 2: "ENTRIES", 4: "EXPERT", 8: "SRC", 16: "DST", 32: "ALIGN", 64: "WAIT"}
+ERR_BITS = {1: "NGROUPS", 2: "ENTRIES", 4: "EXPERT", 8: "SRC", 16: "DST", 32: "ALIGN", 64: "WAIT", 128: "WINDOW",
+            256: "PAGE"}
 
 EXPORTS = ("moe_route_topk", "moe_build_plan", "moe_quantize_q8_1", "moe_repack", "moe_gate_up",
            "moe_swiglu_q8_1", "moe_down_scatter", "moe_workspace_bytes",
@@ -27,7 +28,8 @@ EXPORTS = ("moe_route_topk", "moe_build_plan", "moe_quantize_q8_1", "moe_repack"
            "moe_workspace_layout", "moe_prefill_plan", "moe_prefill_gate_up", "moe_prefill_swiglu_q8_1",
            "moe_prefill_down", "moe_prefill_scatter",
            "moe_add_rmsnorm", "moe_route_scores", "moe_swiglu_i8", "moe_matmul_i8",
-           "moe_stream_read", "moe_status_string", "moe_last_error")
+           "moe_window_append", "moe_window_attention_bytes", "moe_window_attention", "moe_token_logprobs_bytes",
+           "moe_token_logprobs", "moe_stream_read", "moe_status_string", "moe_last_error")
 
 _lib = None
 _P = ctypes.c_void_p
@@ -47,6 +49,18 @@ class MoePlan(ctypes.Structure):
     _fields_ = [("cap_groups", ctypes.c_int32), ("cap_entries", ctypes.c_int32),
                 ("n_groups", _P), ("grp_expert", _P), ("grp_start", _P), ("ent_src", _P),
                 ("ent_dst", _P), ("ent_w", _P), ("err", _P)]
+
+
+class MoeKvCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_kv", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_stride", _L), ("head_stride", _L),
+                ("slot_stride", _L), ("k", _P), ("v", _P), ("k_scale", _P), ("v_scale", _P)]
+
+
+class MoeWindow(ctypes.Structure):
+    _fields_ = [("n_seqs", ctypes.c_int32), ("n_tokens", ctypes.c_int32), ("max_window", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("ld_pages", _L), ("row_start", _P), ("ctx_len", _P), ("pages", _P),
+                ("pos", _P), ("seen", _P), ("err", _P)]
 
 
 def lib():
@@ -94,6 +108,14 @@ def lib():
         L.moe_route_scores.argtypes = [_P, _I, _P, _L, _I, _I, _I, _I, _P, _I, _I, _I, _I, _F, _P, _P]
         L.moe_swiglu_i8.argtypes = [_P, _I, _P, _L, _P, _L, _I, _I, _P, _L, _P]
         L.moe_matmul_i8.argtypes = [_P, _P, _L, _P, _P, _L, _P, _I, _I, _I, _I, _P, _L, _I]
+        both = [ctypes.POINTER(MoeKvCache), ctypes.POINTER(MoeWindow)]
+        L.moe_window_append.argtypes = [_P, *both, _I, _P, _L, _P, _L, _P, _L, _I, _I, _P, _P, _F, _P, _I, _I, _F, _I, _P, _L]
+        L.moe_window_attention_bytes.argtypes = [*both, _I]
+        L.moe_window_attention_bytes.restype = ctypes.c_size_t
+        L.moe_window_attention.argtypes = [_P, *both, _I, _P, _L, _I, _F, _P, _L, _P, _P, ctypes.c_size_t]
+        L.moe_token_logprobs_bytes.argtypes = [_I, _I, _I]
+        L.moe_token_logprobs_bytes.restype = ctypes.c_size_t
+        L.moe_token_logprobs.argtypes = [_P, _I, _P, _L, _I, _I, _F, _P, _I, _P, _P, _I, _P, _P, _P, ctypes.c_size_t]
         _lib = L
     return _lib
 
@@ -395,6 +417,7 @@ _DTYPE = {torch.float32: F32, torch.bfloat16: BF16, torch.float16: F16}
 
 
 _FLOATS, _INT8, _F32ONLY, _BYTES, _INT32 = tuple(_DTYPE), (torch.int8,), (torch.float32,), (torch.uint8,), (torch.int32,)
+_HALVES = (torch.bfloat16, torch.float16)
 
 
 # These calls can be a few microseconds long: the checks below ask each tensor for as little as they can,
@@ -419,6 +442,14 @@ def _on(stream, f, *args):
         raise ValueError(f"{f.__name__}: the stream is of GPU {stream.device_index}, the tensors are on {device}")
     with torch.cuda.stream(stream):
         return f(*args)
+
+
+def _on_cache(stream, f, cache, *args):
+    """f(cache, *args), and what it allocates, on `stream`."""
+    if stream.device_index != cache.device:
+        raise ValueError(f"{f.__name__}: the stream is of GPU {stream.device_index}, the cache is on {cache.device}")
+    with torch.cuda.stream(stream):
+        return f(cache, *args)
 
 
 def _gpu(what, name, t):
@@ -570,6 +601,199 @@ def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, s
     _call(what, dev, a.data_ptr(), lda, sa.data_ptr(), b.data_ptr(), ldb, sb.data_ptr(), M, N, K, _DTYPE[dtype],
           c.data_ptr(), ldc, 1 if accumulate else 0)
     return c
+
+
+# ------------------------------------------------------------------ windows over a cache ------
+
+I8 = 4                                   # moe_kv_cache.dtype of int8 rows
+ROPE_HALF, ROPE_PAIRS = 1, 2             # moe_rope
+_CACHE_DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.int8: I8}
+
+
+class KVCache:
+    """A layer's paged cache: k and v [n_pages, n_kv, page_size, head_dim] (bfloat16, float16 or int8; any strides of
+    the first three, the same for both; a cache of another order is passed as its permuted view), and for int8 rows the
+    scales k_scale and v_scale, contiguous float32 [n_pages, n_kv, page_size]."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        what = "KVCache"
+        self.device = _gpu(what, "k", k)
+        if k.dim() != 4 or k.dtype not in _CACHE_DTYPE:
+            raise ValueError(f"{what}: k is {k.dtype} {tuple(k.shape)}, not a cache [pages, heads, slots, head_dim]")
+        if v.shape != k.shape or v.dtype is not k.dtype or v.get_device() != self.device or v.stride() != k.stride():
+            raise ValueError(f"{what}: v is {v.dtype} {tuple(v.shape)} of strides {v.stride()}, not as k")
+        if k.stride(3) != 1 or max(k.shape) >> 31:
+            raise ValueError(f"{what}: strides {k.stride()} of {tuple(k.shape)}")
+        if (k_scale is None) == (k.dtype is torch.int8) or (v_scale is None) == (k.dtype is torch.int8):
+            raise ValueError(f"{what}: scales come with int8 rows, and they with scales")
+        if k_scale is not None:
+            _packed(what, "k_scale", k_scale, k.shape[:3], torch.float32, self.device)
+            _packed(what, "v_scale", v_scale, k.shape[:3], torch.float32, self.device)
+        self.k, self.v, self.k_scale, self.v_scale, self.dtype = k, v, k_scale, v_scale, k.dtype
+        self.n_pages, self.n_kv, self.page_size, self.head_dim = k.shape
+        self.struct = MoeKvCache(_CACHE_DTYPE[k.dtype], self.n_pages, self.page_size, self.n_kv, self.head_dim, *k.stride()[:3],
+                                 k.data_ptr(), v.data_ptr(), k_scale.data_ptr() if k_scale is not None else None,
+                                 v_scale.data_ptr() if v_scale is not None else None)
+        self.ref = ctypes.byref(self.struct)
+
+    @classmethod
+    def empty(cls, n_pages, page_size, n_kv, head_dim, dtype, device="cuda"):
+        """A new cache of zeros, a head's slots of a page side by side."""
+        k, v = (torch.zeros((n_pages, n_kv, page_size, head_dim), dtype=dtype, device=device) for _ in range(2))
+        if dtype is not torch.int8:
+            return cls(k, v)
+        return cls(k, v, *(torch.zeros((n_pages, n_kv, page_size), dtype=torch.float32, device=device) for _ in range(2)))
+
+
+class Window:
+    """The tokens of one call: row_start int32 [n_seqs + 1], ctx_len int32 [n_seqs], pages int32 [n_seqs, max_pages] (any
+    row stride), the number of rows, the most tokens of one sequence (as many as there are rows, if not given),
+    pos int32 [n_tokens] (rotary positions, if not the keys' indices) and seen int64 [n_tokens] (the tokens of its
+    window that each sees, as bits, if not itself and those before it). The tensors are read when a call runs."""
+
+    def __init__(self, row_start, ctx_len, pages, n_tokens, max_window=None, pos=None, seen=None):
+        what = "Window"
+        self.device, n = _gpu(what, "row_start", row_start), ctx_len.shape[0]
+        _packed(what, "row_start", row_start, (n + 1,), torch.int32, self.device)
+        _packed(what, "ctx_len", ctx_len, (n,), torch.int32, self.device)
+        ld = _rows(what, "pages", pages, None, _INT32, self.device)
+        if pages.shape[0] != n or not 0 <= n_tokens < 1 << 31:
+            raise ValueError(f"{what}: pages of {pages.shape[0]} sequences, not {n}, or {n_tokens} rows")
+        if pos is not None:
+            _packed(what, "pos", pos, (n_tokens,), torch.int32, self.device)
+        if seen is not None:
+            _packed(what, "seen", seen, (n_tokens,), torch.int64, self.device)
+        max_window = max(1, n_tokens) if max_window is None else max_window
+        if not 0 < max_window < 1 << 31:
+            raise ValueError(f"{what}: max_window {max_window}")
+        self.row_start, self.ctx_len, self.pages, self.pos, self.seen = row_start, ctx_len, pages, pos, seen
+        self.n_seqs, self.n_tokens, self.max_window = n, n_tokens, max_window
+        self.err = torch.zeros(1, dtype=torch.int32, device=row_start.device)
+        self.struct = MoeWindow(n, n_tokens, max_window, pages.shape[1], ld, row_start.data_ptr(), ctx_len.data_ptr(),
+                                pages.data_ptr(), pos.data_ptr() if pos is not None else None,
+                                seen.data_ptr() if seen is not None else None, self.err.data_ptr())
+        self.ref = ctypes.byref(self.struct)
+
+    def errors(self) -> int:
+        """The device's error word (sticky; ERR_BITS names the bits)."""
+        return int(self.err.item())
+
+
+def _over_cache(what, cache, window):
+    if window.device != cache.device:
+        raise ValueError(f"{what}: the window is on GPU {window.device}, the cache on {cache.device}")
+    return cache.device
+
+
+def moe_window_append(cache: KVCache, window: Window, q, k, v, freq=None, layout=ROPE_HALF, amp=1.0, q_weight=None,
+                      k_weight=None, eps=1e-6, q_out=None, stream=None):
+    """The window's keys and values (rows k, v [n_tokens, n_kv * head_dim]) into the cache, keys normed (k_weight) and
+    rotated (freq float32 [n_rot / 2]); its queries (rows q [n_tokens, n_heads * head_dim] or None) normed and rotated
+    into q_out, which is returned (new rows of q's type if None; it may be q)."""
+    what = "moe_window_append"
+    if stream is not None:
+        return _on_cache(stream, moe_window_append, cache, window, q, k, v, freq, layout, amp, q_weight, k_weight, eps, q_out)
+    dev, n, d = _over_cache(what, cache, window), window.n_tokens, cache.head_dim
+    kv = (n, cache.n_kv * d)
+    ldk, ldv = _rows(what, "k", k, kv, _FLOATS, dev), _rows(what, "v", v, kv, (k.dtype,), dev)
+    ldq = ldo = n_heads = o_type = n_rot = w_type = 0
+    if q is not None:
+        ldq, wide = _rows(what, "q", q, None, (k.dtype,), dev), q.shape[1]
+        n_heads = wide // d
+        if q.shape[0] != n or wide % d:
+            raise ValueError(f"{what}: q has shape {tuple(q.shape)}, not {n} rows of heads of {d}")
+        if q_out is None:
+            q_out, ldo = q.new_empty((n, wide)), wide
+        else:
+            ldo = _rows(what, "q_out", q_out, q.shape, _FLOATS, dev)
+        o_type = _DTYPE[q_out.dtype]
+    elif q_out is not None or q_weight is not None:
+        raise ValueError(f"{what}: q_out and q_weight without q")
+    if freq is not None:
+        n_rot = 2 * freq.shape[0]
+        _packed(what, "freq", freq, (n_rot // 2,), torch.float32, dev)
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            if w.dtype not in _DTYPE or (w_type and _DTYPE[w.dtype] != w_type):
+                raise ValueError(f"{what}: {name} is {w.dtype}")
+            w_type = _DTYPE[w.dtype]
+            _packed(what, name, w, (d,), w.dtype, dev)
+    _call(what, dev, cache.ref, window.ref, _DTYPE[k.dtype], q.data_ptr() if q is not None else 0, ldq, k.data_ptr(), ldk,
+          v.data_ptr(), ldv, n_heads, w_type, q_weight.data_ptr() if q_weight is not None else 0,
+          k_weight.data_ptr() if k_weight is not None else 0, eps, freq.data_ptr() if n_rot else 0, n_rot, layout, amp, o_type,
+          q_out.data_ptr() if q is not None else 0, ldo)
+    return q_out
+
+
+def window_workspace(cache: KVCache, window: Window, n_heads):
+    """A workspace for moe_window_attention of n_heads heads (calls that overlap need one each)."""
+    n = lib().moe_window_attention_bytes(cache.ref, window.ref, n_heads)
+    return torch.empty(max(n, 16), dtype=torch.uint8, device=cache.k.device)
+
+
+def moe_window_attention(cache: KVCache, window: Window, q, scale, out=None, lse=None, ws=None, stream=None):
+    """Attention of the window's queries (rows q [n_tokens, n_heads * head_dim]) over the cache, into out (rows like q,
+    new if None), which is returned, and lse (float32 [n_tokens, n_heads], if given). ws: window_workspace's."""
+    what = "moe_window_attention"
+    if stream is not None:
+        return _on_cache(stream, moe_window_attention, cache, window, q, scale, out, lse, ws)
+    dev, n, d = _over_cache(what, cache, window), window.n_tokens, cache.head_dim
+    ldq, size = _rows(what, "q", q, None, _HALVES, dev), q.shape
+    wide = size[1]
+    n_heads = wide // d
+    if size[0] != n or wide % d:
+        raise ValueError(f"{what}: q has shape {tuple(size)}, not {n} rows of heads of {d}")
+    if out is None:
+        out, ldo = q.new_empty((n, wide)), wide
+    else:
+        ldo = _rows(what, "out", out, size, (q.dtype,), dev)
+    if lse is not None:
+        _packed(what, "lse", lse, (n, n_heads), torch.float32, dev)
+    if ws is None:
+        ws = window_workspace(cache, window, n_heads)
+    elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{what}: ws is {ws.dtype} on {ws.device}, not contiguous bytes on the call's GPU")
+    _call(what, dev, cache.ref, window.ref, _DTYPE[q.dtype], q.data_ptr(), ldq, n_heads, scale, out.data_ptr(), ldo,
+          lse.data_ptr() if lse is not None else 0, ws.data_ptr(), ws.numel())
+    return out
+
+
+def logprobs_workspace(rows, n, k, device="cuda"):
+    """A workspace for moe_token_logprobs (calls that overlap need one each)."""
+    return torch.empty(max(lib().moe_token_logprobs_bytes(rows, n, k), 16), dtype=torch.uint8, device=device)
+
+
+def moe_token_logprobs(logits, tokens=None, k=0, entropy=False, scale=1.0, ws=None, stream=None):
+    """(logp, entropy, top_ids, top_logp) of logits rows [rows, n] under softmax(scale * logits): log probabilities float32
+    [rows, given] of tokens (int32 [rows, given]), entropies [rows], and the k best tokens (int32 [rows, k]) with their log
+    probabilities; None for what is not asked for. ws: logprobs_workspace's."""
+    what = "moe_token_logprobs"
+    if stream is not None:
+        return _on(stream, moe_token_logprobs, logits, tokens, k, entropy, scale, ws)
+    dev = _gpu(what, "logits", logits)
+    ld = _rows(what, "logits", logits, None, _FLOATS, dev)
+    rows, n = logits.shape
+    given, logp, h, ids, top = 0, None, None, None, None
+    if tokens is not None:
+        if tokens.dim() != 2:
+            raise ValueError(f"{what}: tokens has shape {tuple(tokens.shape)}, not rows")
+        given = tokens.shape[1]
+        _packed(what, "tokens", tokens, (rows, given), torch.int32, dev)
+        logp = logits.new_empty((rows, given), dtype=torch.float32)
+    if entropy:
+        h = logits.new_empty((rows,), dtype=torch.float32)
+    if not 0 <= k <= min(32, n) or given > 64:
+        raise ValueError(f"{what}: {k} alternatives, {given} tokens a row, of {n}")
+    if k:
+        ids, top = logits.new_empty((rows, k), dtype=torch.int32), logits.new_empty((rows, k), dtype=torch.float32)
+    if ws is None:
+        ws = logprobs_workspace(rows, n, k, logits.device)
+    elif ws.dtype is not torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"{what}: ws is {ws.dtype} on {ws.device}, not contiguous bytes on the call's GPU")
+    _call(what, dev, _DTYPE[logits.dtype], logits.data_ptr(), ld, rows, n, scale, tokens.data_ptr() if given else 0, given,
+          logp.data_ptr() if given else 0, h.data_ptr() if entropy else 0, k, ids.data_ptr() if k else 0,
+          top.data_ptr() if k else 0, ws.data_ptr(), ws.numel())
+    return logp, h, ids, top
 
 
 # ------------------------------------------------------------------ bandwidth reference -------

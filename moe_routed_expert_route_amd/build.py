@@ -7,7 +7,7 @@ import tempfile
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route.hip", "moe_ops.hip")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("moe_route.hip", "moe_ops.hip", "moe_window.hip")]
 LIB = os.path.join(HERE, "libmoe_route.so")
 
 HIPCC_FLAGS = [

@@ -22,8 +22,8 @@ import statistics
 
 from . import profsum
 
-SOURCES = ("moe_routed_expert_route_amd/csrc/moe_ops.hip", "moe_routed_expert_route_amd/csrc/moe_device.hpp",
-           "moe_routed_expert_route_amd/build.py", "perf/operators.py")
+SOURCES = ("moe_routed_expert_route_amd/csrc/moe_ops.hip", "moe_routed_expert_route_amd/csrc/moe_rows.hpp",
+           "moe_routed_expert_route_amd/csrc/moe_device.hpp", "moe_routed_expert_route_amd/build.py", "perf/operators.py")
 PASSES = 10
 COUNTED = ("norm 8192x4096 bf16", "swiglu 4096x5461 bf16", "matmul 8192x8192x4096")
 # a prompt of 512 tokens through the shared expert: gate and up stacked, and down added into the layer's Y
