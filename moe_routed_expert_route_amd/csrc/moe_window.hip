@@ -250,75 +250,603 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
 }
 
 // ------------------------------------------------------------------ attention ---------------
+//
+// The keys of a sequence are cut into runs (run_of), a workgroup takes one run of one cache head for a tile of rows (the
+// window's tokens times the query heads that share the cache head), and k_attend_join adds the runs of a row up. A wave takes
+// 64 of every 256 keys, 32 at a time. All products are transposed: scores are K . Q^T, so that a lane has four neighbouring keys
+// of one row and the row's factors are the lane's own, and K's rows go from memory straight into the matrix instruction's
+// lanes; the exponentials are already where V^T . P^T takes them (which key is which place of the sum over keys is free, as
+// long as V agrees), and a lane loads the same eight neighbouring values of eight keys, from which a byte permutation
+// makes the eight rows of V^T. No LDS until the waves join.
 
 struct AttendArgs {
   CacheArgs c;
   WindowArgs w;
   const void* q;
   void* out;
-  float* lse;
+  float *lse, *part, *part_ml;   // of runs: [row][head][max_runs] head_dim values, and (maximum, sum)
   int64_t ldq, ldo;
-  int n_heads;
+  int n_heads, max_runs, wide;
   float scale;
 };
 
-// A wave for each row and head: 64 keys at a time, one a lane.
-template <typename T, typename K>
-__global__ __launch_bounds__(64) void k_attend_rows(AttendArgs a) {
-  __shared__ float s_q[256], s_p[64];
-  const int row = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads, lane = threadIdx.x, d = a.c.d;
-  const int h = head / (a.n_heads / a.c.n_kv);
-  if (blockIdx.x == 0) check_seqs(a.w, a.w.max_window, 64);
-  const Seq q = seq_of(a.w, row, a.w.max_window);
-  if (q.tokens == 0) return;
-  const int j = row - q.start, keys = q.ctx + q.tokens;
-  const uint64_t seen = a.w.seen ? a.w.seen[row] : ~0ull >> (63 - j);
-  for (int i = lane; i < d; i += 64) s_q[i] = to_f(((const T*)a.q)[row * a.ldq + (int64_t)head * d + i]);
-  __syncthreads();
-  float top = -__builtin_inff(), sum = 0.0f, acc[4] = {};
-  for (int base = 0; base < keys; base += 64) {
-    const int key = base + lane;
-    bool sees = key < keys && (key < q.ctx || (seen >> (key - q.ctx) & 1));
-    int64_t at = 0, sc = 0;
-    if (sees) {
-      const int page = a.w.pages[q.s * a.w.ld_pages + key / a.c.page_size], slot = key % a.c.page_size;
-      sees = page >= 0 && page < a.c.n_pages;
-      if (!sees) atomicOr(a.w.err, MOE_ERR_PAGE);
-      at = page * a.c.page + h * a.c.head + slot * a.c.slot;
-      sc = ((int64_t)page * a.c.n_kv + h) * a.c.page_size + slot;
+// Keys of a run, by the sequence's own length: short enough to spread one long sequence over the card, long enough that the
+// runs' results (4 bytes a value, written and read) stay small beside the cache's rows.
+__host__ __device__ __forceinline__ int run_of(int keys, int wide) {
+  return wide ? max(1024, ((keys >> 5) + 256) & ~255) : max(256, ((keys >> 6) + 256) & ~255);
+}
+__host__ __device__ __forceinline__ int runs_of(int keys, int wide) {
+  const int run = run_of(keys, wide);
+  return (int)(((int64_t)keys + run - 1) / run);
+}
+constexpr int kMaxRuns = 64;   // runs_of of any count
+
+template <typename T>
+struct Mat;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+template <>
+struct Mat<bf16_t> {
+  static constexpr float kBoost = 0.0f;
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    typedef __bf16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, v2{(__bf16)a, (__bf16)b});
+  }
+  static __device__ __forceinline__ uint32_t odd(uint32_t x) {   // of two values, bit 0 / bit 16: not finite
+    return ((x & 0x00007F80u) == 0x00007F80u ? 1u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x10000u : 0u);
+  }
+};
+template <>
+struct Mat<f16_t> {
+  static constexpr float kBoost = 14.0f;   // weights up to 2^14, so that small ones stay normal numbers
+  static __device__ __forceinline__ f32x4 mma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float a, float b) {
+    typedef _Float16 v2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, v2{(_Float16)a, (_Float16)b});
+  }
+  static __device__ __forceinline__ uint32_t odd(uint32_t x) {
+    return ((x & 0x00007C00u) == 0x00007C00u ? 1u : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 0x10000u : 0u);
+  }
+};
+
+// Over the four lanes of a row (lane, and 16, 32, 48 on).
+__device__ __forceinline__ float max4(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+  a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+}
+__device__ __forceinline__ float sum4(float v) {
+  auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  v = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+  a = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, v), __builtin_bit_cast(uint32_t, v), false, false);
+  return __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+}
+
+// 32 keys of a head as they are loaded: of keys 16 t + lane % 16 the values that the matrix instruction takes from this lane, and
+// of keys 16 t + 4 (lane / 16) + i this lane's neighbouring values.
+template <bool I8, int HD>
+struct Keys {
+  static constexpr int KL = I8 ? HD / 64 : HD / 32, VD = I8 ? HD / 64 : HD / 32;
+  u32x4 k[2][KL];
+  uint32_t v[8][VD];
+  f32x4 ks[2], vs[2];
+};
+
+constexpr uint32_t kNowhere = 0x80000000u;   // an offset past any buffer: the load gives 0 and touches nothing
+
+// HD: 64, 128 or 256, the least that holds head_dim. NT: a wave's tiles of 16 rows. WIDE: the waves share the keys and
+// have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. AHEAD: the next keys are
+// loaded before these are used.
+template <typename T, bool I8, int HD, int NT, bool WIDE, bool AHEAD>
+__global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
+  using M = Mat<T>;
+  using KV = Keys<I8, HD>;
+  constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1), KS = HD / 32, E0 = HD < 128 ? 4 : 8, NH = HD < 128 ? 1 : HD / 128, DT = E0 * NH;
+  constexpr int SIZE = I8 ? 1 : 2, STRIDE = HD + 4;
+  __shared__ float s_m[4][WIDE ? 1 : ROWS], s_l[4][WIDE ? 1 : ROWS], s_o[4][WIDE ? 1 : 16 * STRIDE], s_p[I8 ? 1 : 4][I8 ? 1 : 32 * 16];
+  __shared__ int s_wave[4];
+  extern __shared__ int s_end[];   // [n_seqs]: items of the sequences up to this one
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quad = lane >> 4;
+  const int G = a.n_heads / a.c.n_kv, d = a.c.d;
+  int total = 0;
+  for (int i0 = 0; i0 < a.w.n_seqs; i0 += 256) {
+    const int i = i0 + tid;
+    int n = 0;
+    if (i < a.w.n_seqs) {
+      const int start = a.w.row_start[i], end = a.w.row_start[i + 1], ctx = a.w.ctx_len[i];
+      if (!seq_ok(a.w, start, end, ctx, a.w.max_window)) {
+        if (blockIdx.x == 0) atomicOr(a.w.err, MOE_ERR_WINDOW);
+      } else if (end > start) {
+        n = ((end - start) * G + ROWS - 1) / ROWS * runs_of(ctx + end - start, a.wide) * a.c.n_kv;
+      }
     }
-    float s = -__builtin_inff(), vs = 0.0f;
-    if (sees) {
-      const K* k = (const K*)a.c.k + at;
-      float dot = 0.0f;
-      for (int i = 0; i < d; ++i) dot = __builtin_fmaf(s_q[i], (float)to_f(k[i]), dot);
-      if constexpr (sizeof(K) == 1) dot *= a.c.ks[sc], vs = a.c.vs[sc];
-      s = dot * a.scale;
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) {
+      const int up = __shfl_up(n, o);
+      if (lane >= o) n += up;
     }
-    float most = s;
-    for (int o = 32; o; o /= 2) most = __builtin_fmaxf(most, __shfl_xor(most, o));
-    const float now = __builtin_fmaxf(top, most), ref = now == -__builtin_inff() ? 0.0f : now;
-    const float p = sees ? expf(s - ref) : 0.0f, keep = expf(top - ref);
-    top = now;
-    float ps = p;
-    for (int o = 32; o; o /= 2) ps += __shfl_xor(ps, o);
-    sum = sum * keep + ps;
-    s_p[lane] = sizeof(K) == 1 ? p * vs : p;
-    const uint64_t live = __ballot(sees);
+    if (lane == 63) s_wave[wave] = n;
     __syncthreads();
-    for (int x = 0; x < 4; ++x) acc[x] *= keep;
-    for (int i = 0; i < 64; ++i) {
-      if (!(live >> i & 1)) continue;
-      const int64_t from = __shfl(at, i);
-      for (int x = 0; x < 4; ++x)
-        if (x * 64 + lane < d) acc[x] = __builtin_fmaf(s_p[i], (float)to_f(((const K*)a.c.v)[from + x * 64 + lane]), acc[x]);
-    }
+    for (int w = 0; w < wave; ++w) n += s_wave[w];
+    if (i < a.w.n_seqs) s_end[i] = total + n;
+    total += s_wave[0] + s_wave[1] + s_wave[2] + s_wave[3];
     __syncthreads();
   }
-  for (int x = 0; x < 4; ++x)
-    if (x * 64 + lane < d)
-      ((T*)a.out)[row * a.ldo + (int64_t)head * d + x * 64 + lane] = from_f<T>(sum == 0.0f ? 0.0f : acc[x] / sum);
-  if (a.lse && lane == 0) a.lse[(int64_t)row * a.n_heads + head] = sum == 0.0f ? -__builtin_inff() : top + logf(sum);
+  total = __builtin_amdgcn_readfirstlane(total);
+  // neighbouring items, the tiles of one run among them, on one die
+  const int first = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+  const float c = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * 1.44269504088896340736f;
+  const int64_t slot_bytes = a.c.slot * SIZE;
+  for (int item = first; item < total; item += gridDim.x) {
+    int s = 0;
+    for (int lo = 0, n = a.w.n_seqs; n > 0;) {   // the first sequence whose end is past the item
+      const int mid = n >> 1;
+      if (s_end[lo + mid] <= item) lo += mid + 1, n -= mid + 1;
+      else n = mid;
+      s = lo;
+    }
+    s = __builtin_amdgcn_readfirstlane(s);
+    int rest = item - __builtin_amdgcn_readfirstlane(s > 0 ? s_end[s - 1] : 0);
+    const int start = __builtin_amdgcn_readfirstlane(a.w.row_start[s]);
+    const int tokens = __builtin_amdgcn_readfirstlane(a.w.row_start[s + 1]) - start;
+    const int ctx = __builtin_amdgcn_readfirstlane(a.w.ctx_len[s]), keys = ctx + tokens, rows = tokens * G;
+    const int tiles = (rows + ROWS - 1) / ROWS, run = run_of(keys, a.wide), runs = runs_of(keys, a.wide);
+    const int tile = rest % tiles;
+    rest /= tiles;
+    const int part = rest % runs, head = rest / runs;   // of the cache
+    const int key0 = part * run, len = min(run, keys - key0);
+    const int steps = WIDE ? (len + 31) >> 5 : 2 * (len >> 8) + min(2, max(0, (len & 255) - 64 * wave + 31) >> 5);
+    auto key_of = [&](int step) { return WIDE ? key0 + step * 32 : key0 + (step >> 1) * 256 + wave * 64 + (step & 1) * 32; };
+
+    // rows: this lane's row of each tile of 16, its token's mask, and its part of Q^T
+    uint64_t seen[NT];
+    u32x4 q[NT][KS];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      const int r = tile * ROWS + 16 * ((WIDE ? wave * NT : 0) + t) + col, j = r / G;
+      const bool row = r < rows;
+      const int64_t at = start + (row ? j : 0);
+      uint64_t mask = ~0ull >> (63 - (row ? j : 0));
+      if (a.w.seen) mask = a.w.seen[at];
+      seen[t] = row ? mask & (~0ull >> (64 - tokens)) : 0;
+      const T* x = (const T*)a.q + at * a.ldq + (int64_t)(head * G + r % G) * d;
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+        const int i = I8 ? (k >> 1) * 64 + quad * 16 + (k & 1) * 8 : k * 32 + quad * 8;
+        q[t][k] = u32x4{0, 0, 0, 0};
+        if (row && i < d && a.scale != 0.0f) __builtin_memcpy(&q[t][k], x + i, 16);
+        if (a.scale < 0.0f) q[t][k] ^= 0x80008000u;
+      }
+    }
+    float m[NT], l[NT];
+    int e_ref = -127;   // of an i8 cache's scales: weights are times scale / 2^e_ref
+    f32x4 acc[NT][DT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      m[t] = -__builtin_inff();
+      l[t] = 0.0f;
+#pragma unroll
+      for (int x = 0; x < DT; ++x) acc[t][x] = f32x4{0, 0, 0, 0};
+    }
+
+    int page_of = -1, slot_of = 0;   // lane i: of tile 16 i of the wave's keys from the batch on
+    const uint8_t* const k_head = a.c.k + head * a.c.head * SIZE;
+    const uint8_t* const v_head = a.c.v + head * a.c.head * SIZE;
+    auto load = [&](KV& kv, int step, bool (&live)[2]) {
+      const int key = key_of(step);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int at = 2 * (step & 31) + t;
+        const int page = __builtin_amdgcn_readlane(page_of, at), slot = __builtin_amdgcn_readlane(slot_of, at);
+        live[t] = step < steps && page >= 0;
+        const int64_t off = live[t] ? (page * a.c.page + slot * a.c.slot) * SIZE : 0;
+        const int records = live[t] ? 0x7FFFFFFF : 0;
+        const auto kr = __builtin_amdgcn_make_buffer_rsrc((void*)(k_head + off), 0, records, 0x00027000);
+        const auto vr = __builtin_amdgcn_make_buffer_rsrc((void*)(v_head + off), 0, records, 0x00027000);
+#pragma unroll
+        for (int u = 0; u < KV::KL; ++u) {
+          const uint32_t byte = u * 64 + quad * 16;
+          kv.k[t][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                                     kr, byte < (uint32_t)(d * SIZE) ? (uint32_t)(col * slot_bytes) + byte : kNowhere, 0, 0));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool in = key + 16 * t + 4 * quad + i < keys;   // a slot past the last key may hold anything
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const int e = h * 128 + col * E0;
+            const uint32_t o = in && e < d ? (uint32_t)((4 * quad + i) * slot_bytes) + (uint32_t)(e * SIZE) : kNowhere;
+            constexpr int W = E0 * SIZE / 4;
+            uint32_t* to = &kv.v[4 * t + i][h * W];
+            if constexpr (W == 4) {
+              const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, o, 0, 0));
+              to[0] = x[0], to[1] = x[1], to[2] = x[2], to[3] = x[3];
+            } else if constexpr (W == 2) {
+              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, o, 0, 0));
+              to[0] = x[0], to[1] = x[1];
+            } else {
+              to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, o, 0, 0);
+            }
+          }
+        }
+        if constexpr (I8) {
+          const int64_t so = live[t] ? ((int64_t)page * a.c.n_kv + head) * a.c.page_size + slot : 0;
+          const auto ksr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.ks + so), 0, records, 0x00027000);
+          const auto vsr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.vs + so), 0, records, 0x00027000);
+          kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ksr, quad * 16, 0, 0));
+          kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(vsr, quad * 16, 0, 0));
+        }
+      }
+    };
+
+    auto use = [&](KV& kv, int step, const bool (&live)[2]) {
+      const int key = key_of(step);
+      const bool check = key + 32 > ctx || !live[0] || !live[1];
+      f32x4 p[2][NT];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) p[t][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+          u32x4 f;
+          if constexpr (I8) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t b = kv.k[t][k >> 1][2 * (k & 1) + (x >> 1)] >> (16 * (x & 1));
+              f[x] = M::pack((float)(int8_t)b, (float)(int8_t)(b >> 8));
+            }
+          } else {
+            f = kv.k[t][k];
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) p[t][n] = M::mma(f, q[n][k], p[t][n]);
+        }
+        if constexpr (I8) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[t][n][i] *= kv.ks[t][i];
+        }
+      }
+      if (check) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rel = key + 16 * t + 4 * quad + i - ctx;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+              const bool sees = live[t] && (rel < 0 || (rel < 64 && (seen[n] >> (rel & 63) & 1)));
+              p[t][n][i] = sees ? p[t][n][i] : -__builtin_inff();
+            }
+            if constexpr (I8)
+              if (rel >= tokens) kv.vs[t][i] = 0.0f;
+          }
+      }
+      float top[NT];
+      bool grows = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        float x = m[n];
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x = __builtin_fmaxf(x, p[t][n][i]);
+        top[n] = max4(x);
+        grows |= top[n] > m[n];
+      }
+      int e = e_ref;
+      float unit = 1.0f;
+      if constexpr (I8 && M::kBoost > 0.0f) {
+        float most = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) most = __builtin_fmaxf(most, kv.vs[t][i] < __builtin_inff() ? kv.vs[t][i] : 0.0f);
+        e = max(e, (int)(__builtin_bit_cast(uint32_t, max4(most)) >> 23) - 127);
+        e = __builtin_amdgcn_readfirstlane(e);
+        grows |= e > e_ref;
+        unit = __builtin_ldexpf(1.0f, -e);
+      }
+      if (__ballot(grows)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float ref = top[n] == -__builtin_inff() ? 0.0f : top[n];
+          const float keep = __builtin_amdgcn_exp2f((m[n] - ref) * c);
+          l[n] *= keep;
+          const float keep_o = I8 && M::kBoost > 0.0f ? __builtin_ldexpf(keep, e_ref - e) : keep;
+#pragma unroll
+          for (int x = 0; x < DT; ++x) acc[n][x] *= keep_o;
+          m[n] = top[n];
+        }
+        e_ref = e;
+      }
+      u32x4 w[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float mc = (m[n] == -__builtin_inff() ? 0.0f : m[n]) * c - M::kBoost;
+        float sum = 0.0f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) p[t][n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(p[t][n][i], c, -mc));
+          sum += (p[t][n][0] + p[t][n][1]) + (p[t][n][2] + p[t][n][3]);
+          f32x4 y = p[t][n];
+          if constexpr (I8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[i] = check && y[i] == 0.0f ? 0.0f : y[i] * (kv.vs[t][i] * unit);
+          }
+          w[n][2 * t] = M::pack(y[0], y[1]);
+          w[n][2 * t + 1] = M::pack(y[2], y[3]);
+        }
+        l[n] += sum;
+      }
+      // A value of a drafted token that is not finite must not reach rows that do not see it (0 times it is NaN): it
+      // is taken out here and added to the others below.
+      bool odd = false;
+      if constexpr (!I8) {
+        if (key + 32 > ctx) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < KV::VD; ++y) {
+              const uint32_t o = M::odd(kv.v[x][y]);
+              any |= o;
+              kv.v[x][y] &= ~(o * 0xFFFFu);
+            }
+          odd = __ballot(any != 0) != 0;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int e8 = 0; e8 < E0; ++e8) {
+          u32x4 f;
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            if constexpr (I8) {
+              constexpr int W = E0 / 4;
+              const uint32_t lo = kv.v[2 * y][h * W + e8 / 4] >> (8 * (e8 & 3)), hi = kv.v[2 * y + 1][h * W + e8 / 4] >> (8 * (e8 & 3));
+              f[y] = M::pack((float)(int8_t)lo, (float)(int8_t)hi);
+            } else {
+              constexpr int W = E0 / 2;
+              f[y] = __builtin_amdgcn_perm(kv.v[2 * y + 1][h * W + e8 / 2], kv.v[2 * y][h * W + e8 / 2], e8 & 1 ? 0x07060302u : 0x05040100u);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) acc[n][h * E0 + e8] = M::mma(f, w[n], acc[n][h * E0 + e8]);
+        }
+      if constexpr (!I8) {
+        if (odd) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) s_p[wave][(16 * t + 4 * quad + i) * 16 + col] = p[t][n][i];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll 1
+            for (int k = 0; k < 32 && key + k < keys; ++k) {
+              const int at = 2 * (step & 31) + (k >> 4);
+              const int page = __builtin_amdgcn_readlane(page_of, at), slot = __builtin_amdgcn_readlane(slot_of, at);
+              if (page < 0) continue;
+              const float pk = s_p[wave][k * 16 + col];
+              const T* v = (const T*)v_head + page * a.c.page + (slot + (k & 15)) * a.c.slot;
+#pragma unroll
+              for (int x = 0; x < DT; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const int at_d = x / E0 * 128 + (4 * quad + i) * E0 + x % E0;
+                  const float f = at_d < d ? to_f(v[at_d]) : 0.0f;
+                  if (!(__builtin_fabsf(f) < __builtin_inff()) && pk != 0.0f) acc[n][x][i] += pk * f;
+                }
+            }
+            __builtin_amdgcn_wave_barrier();
+          }
+        }
+      }
+    };
+
+    for (int batch = 0; batch < steps; batch += 32) {
+      {
+        const int key = key_of(batch + (lane >> 1)) + 16 * (lane & 1);
+        page_of = -1;
+        if (key < key0 + len) {
+          const int page = a.w.pages[s * a.w.ld_pages + key / a.c.page_size];
+          slot_of = key % a.c.page_size;
+          if (page >= 0 && page < a.c.n_pages) page_of = page;
+          else atomicOr(a.w.err, MOE_ERR_PAGE);
+        }
+      }
+      const int last = min(batch + 32, steps);
+      if constexpr (AHEAD) {
+        KV x, y;
+        bool lx[2], ly[2];
+        load(x, batch, lx);
+        for (int i = batch; i < last; i += 2) {
+          load(y, i + 1 < last ? i + 1 : steps, ly);
+          use(x, i, lx);
+          if (i + 1 >= last) break;
+          load(x, i + 2 < last ? i + 2 : steps, lx);
+          use(y, i + 1, ly);
+        }
+      } else {
+        for (int i = batch; i < last; ++i) {
+          KV x;
+          bool lx[2];
+          load(x, i, lx);
+          use(x, i, lx);
+        }
+      }
+    }
+
+    if constexpr (WIDE) {   // a lane has neighbouring values of its rows
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float sum = sum4(l[n]);
+        const int r = tile * ROWS + 16 * (wave * NT + n) + col;
+        if (r >= rows) continue;
+        const float best = m[n] == -__builtin_inff() ? 0.0f : m[n], unit = I8 && M::kBoost > 0.0f ? __builtin_ldexpf(1.0f, e_ref) : 1.0f;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const int64_t row = start + r / G;
+        const int qh = head * G + r % G;
+        const int64_t idx = (row * a.n_heads + qh) * a.max_runs + part;
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = h * 128 + (4 * quad + i) * E0;
+            if (at >= d) continue;
+            float o[E0];
+#pragma unroll
+            for (int x = 0; x < E0; ++x) o[x] = acc[n][h * E0 + x][i] * unit;
+            if (runs == 1) {
+              T y[E0];
+#pragma unroll
+              for (int x = 0; x < E0; ++x) y[x] = from_f<T>(sum == 0.0f ? 0.0f : o[x] * inv);
+              __builtin_memcpy((T*)a.out + row * a.ldo + (int64_t)qh * d + at, y, sizeof y);
+            } else {
+              __builtin_memcpy(a.part + idx * d + at, o, sizeof o);
+            }
+          }
+        if (quad == 0 && runs == 1 && a.lse)
+          a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - M::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
+        if (quad == 0 && runs > 1) {
+          a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - M::kBoost;
+          a.part_ml[2 * idx + 1] = sum;
+        }
+      }
+      continue;
+    }
+    if constexpr (!WIDE) {
+    // the waves' results, in their order
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const float sum = sum4(l[n]);
+      if (quad == 0) {
+        s_m[wave][16 * n + col] = m[n];
+        s_l[wave][16 * n + col] = sum;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      auto best_of = [&](int r) {
+        const float x = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
+        return x == -__builtin_inff() ? 0.0f : x;
+      };
+      float f = __builtin_amdgcn_exp2f((m[n] - best_of(16 * n + col)) * c);
+      if constexpr (I8 && M::kBoost > 0.0f) f = __builtin_ldexpf(f, e_ref);
+#pragma unroll
+      for (int h = 0; h < NH; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int e4 = 0; e4 < E0; e4 += 4) {
+            f32x4 y;
+#pragma unroll
+            for (int x = 0; x < 4; ++x) y[x] = acc[n][h * E0 + e4 + x][i] * f;
+            *(f32x4*)&s_o[wave][col * STRIDE + h * 128 + (4 * quad + i) * E0 + e4] = y;
+          }
+      __syncthreads();
+      const int rr = tid >> 4, at = (tid & 15) * (HD / 16), r = tile * ROWS + 16 * n + rr;
+      if (r < rows && at < d) {
+        const float best = best_of(16 * n + rr);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w) sum += s_l[w][16 * n + rr] * __builtin_amdgcn_exp2f((s_m[w][16 * n + rr] - best) * c);
+        const int64_t row = start + r / G;
+        const int qh = head * G + r % G;
+        float o[HD / 16];
+#pragma unroll
+        for (int x = 0; x < HD / 16; x += 4) {
+          f32x4 y = *(const f32x4*)&s_o[0][rr * STRIDE + at + x];
+#pragma unroll
+          for (int w = 1; w < 4; ++w) y += *(const f32x4*)&s_o[w][rr * STRIDE + at + x];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[x + i] = y[i];
+        }
+        if (runs == 1) {
+          T* out = (T*)a.out + row * a.ldo + (int64_t)qh * d + at;
+          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+          T y[HD / 16];
+#pragma unroll
+          for (int x = 0; x < HD / 16; ++x) y[x] = from_f<T>(sum == 0.0f ? 0.0f : o[x] * inv);
+          __builtin_memcpy(out, y, sizeof y);
+          if (a.lse && at == 0)
+            a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - M::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
+        } else {
+          const int64_t idx = (row * a.n_heads + qh) * a.max_runs + part;
+          __builtin_memcpy(a.part + idx * d + at, o, sizeof o);
+          if (at == 0) {
+            a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - M::kBoost;
+            a.part_ml[2 * idx + 1] = sum;
+          }
+        }
+      }
+      __syncthreads();
+    }
+    }
+  }
+}
+
+// The runs of a row and head: a workgroup each; lanes side by side take neighbouring values and the groups of lanes every
+// eighth run (of head_dim 128), always in the same order.
+template <typename T>
+__global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
+  __shared__ float s_w[kMaxRuns];
+  __shared__ f32x4 s_o[256];
+  const int row = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads, tid = threadIdx.x, d = a.c.d;
+  const Seq q = seq_of(a.w, row, a.w.max_window);
+  if (q.tokens == 0) return;
+  const int runs = runs_of(q.ctx + q.tokens, a.wide);
+  if (runs == 1) return;
+  const int64_t idx = (int64_t)blockIdx.x * a.max_runs;
+  const int lane = tid & 63;
+  float best = -__builtin_inff(), l = 0.0f;
+  if (lane < runs) best = a.part_ml[2 * (idx + lane)], l = a.part_ml[2 * (idx + lane) + 1];
+  const float m = best;
+#pragma unroll
+  for (int o = 32; o; o /= 2) best = __builtin_fmaxf(best, __shfl_xor(best, o));
+  const float w = lane < runs ? __builtin_amdgcn_exp2f(m - (best == -__builtin_inff() ? 0.0f : best)) : 0.0f;
+  float sum = l * w;
+#pragma unroll
+  for (int o = 32; o; o /= 2) sum += __shfl_xor(sum, o);
+  if (tid < kMaxRuns) s_w[tid] = w;
+  __syncthreads();
+  const int wide = d <= 64 ? 16 : d <= 128 ? 32 : 64, at = (tid % wide) * 4, first = tid / wide, groups = 256 / wide;
+  f32x4 o = {0, 0, 0, 0};
+  if (at < d) {
+    const float* p = a.part + idx * d + at;
+#pragma unroll 4
+    for (int r = first; r < runs; r += groups) {
+      const f32x4 x = *(const f32x4*)(p + (int64_t)r * d);
+      const float f = s_w[r];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
+    }
+  }
+  s_o[tid] = o;
+  __syncthreads();
+  if (tid < wide && at < d) {
+    for (int g = 1; g < groups; ++g) o += s_o[g * wide + tid];
+    T* out = (T*)a.out + row * a.ldo + (int64_t)head * d + at;
+    T y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = from_f<T>(sum == 0.0f ? 0.0f : o[i] / sum);
+    __builtin_memcpy(out, y, sizeof y);
+    if (a.lse && at == 0)
+      a.lse[(int64_t)row * a.n_heads + head] = sum == 0.0f ? -__builtin_inff() : (best + __builtin_log2f(sum)) * 0.69314718055994530942f;
+  }
 }
 
 // ------------------------------------------------------------------ log probabilities -------
@@ -446,6 +974,7 @@ int check_cache(const moe_kv_cache* c) {
   if (c->n_pages < 1 || c->page_size < 16 || c->page_size > MOE_MAX_PAGE || c->page_size % 16 || c->n_kv < 1 ||
       c->n_kv > MOE_MAX_HEADS || c->head_dim < 16 || c->head_dim > 256 || c->head_dim % 16)
     return MOE_E_SHAPE;
+  if (c->page_size > 1 && c->slot_stride > 1 << 24) return MOE_E_SHAPE;   // 16 rows within 32 bits of bytes
   if (!c->k || !c->v || !aligned(c->k, 16) || !aligned(c->v, 16) || !cache_extent(*c).ok) return MOE_E_ARG;
   if (c->dtype == MOE_I8) {
     if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return MOE_E_ARG;
@@ -500,6 +1029,48 @@ CacheArgs cache_args(const moe_kv_cache& c) {
 WindowArgs window_args(const moe_window& w, const moe_kv_cache& c) {
   return WindowArgs{w.row_start, w.ctx_len, w.pages, w.pos, w.seen, w.err, w.ld_pages, w.n_seqs, w.n_tokens, w.max_window,
                     w.max_pages * c.page_size};
+}
+
+// Windows of more than 32 rows a cache head take longer runs: their runs' results weigh more, and their tiles fill the card.
+int wide_rule(const moe_kv_cache& c, const moe_window& w, int n_heads) { return w.max_window * (n_heads / c.n_kv) > 32; }
+int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
+  const int wide = wide_rule(c, w, n_heads), least = wide ? 1024 : 256;   // keys of a run
+  return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, wide ? 32 : kMaxRuns);
+}
+
+template <typename T, bool I8, int HD, int NT, bool WIDE>
+int launch_attend(hipStream_t st, const AttendArgs& a) {
+  constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1);
+  const int64_t tiles = ((int64_t)a.w.max_window * (a.n_heads / a.c.n_kv) + ROWS - 1) / ROWS;
+  const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;
+  if (items > 0x7FFFFFFF) return MOE_E_SHAPE;
+  const int grid = (int)std::min<int64_t>(512, (items + 7) & ~7ll);
+  hipLaunchKernelGGL((k_attend<T, I8, HD, NT, WIDE, NT == 1 && HD < 256>), dim3(grid), dim3(256), 4 * a.w.n_seqs, st, a);
+  if (const int rc = launched("moe_window_attention")) return rc;
+  if (a.max_runs > 1) {
+    hipLaunchKernelGGL(k_attend_join<T>, dim3((unsigned)(a.w.n_tokens * a.n_heads)), dim3(256), 0, st, a);
+    return launched("moe_window_attention");
+  }
+  return MOE_OK;
+}
+template <typename T>
+int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
+  const int rows = a.w.max_window * (a.n_heads / a.c.n_kv);
+  if ((int64_t)a.w.n_tokens * a.n_heads * 256 > kLaunchThreads) return MOE_E_SHAPE;
+  auto tiles = [&](auto i, auto hd) {
+    constexpr bool I8 = decltype(i)::value;
+    constexpr int HD = decltype(hd)::value;
+    constexpr int MOST = HD == 256 ? 1 : 2;   // tiles of 16 rows that a wave has registers for
+    if (a.wide) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, MOST, true>(st, a);
+    return rows <= 16 ? launch_attend<T, I8, HD, 1, false>(st, a) : launch_attend<T, I8, HD, MOST, false>(st, a);
+  };
+  auto width = [&](auto i) {
+    using std::integral_constant;
+    if (a.c.d <= 64) return tiles(i, integral_constant<int, 64>{});
+    if (a.c.d <= 128) return tiles(i, integral_constant<int, 128>{});
+    return tiles(i, integral_constant<int, 256>{});
+  };
+  return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
 }  // namespace moe
@@ -563,7 +1134,8 @@ size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, in
   if (check_cache(C) || check_window(W, *C) || n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv ||
       W->max_window > MOE_MAX_WINDOW)
     return 0;
-  return 16;
+  const size_t runs = max_runs(*C, *W, n_heads);
+  return runs == 1 ? 16 : ((size_t)W->n_tokens * n_heads * runs * (C->head_dim + 2) * 4 + 15) & ~(size_t)15;
 }
 
 int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
@@ -594,13 +1166,12 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return MOE_E_ARG;
   }
-  const AttendArgs a{cache_args(*C), window_args(*W, *C), q, out, lse, ldq, ldo, n_heads, scale};
-  const int64_t blocks = (int64_t)n * n_heads;
-  if (blocks * 64 > kLaunchThreads) return MOE_E_SHAPE;
-  auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64), 0, (hipStream_t)stream, a); };
-  if (dtype == MOE_BF16) C->dtype == MOE_I8 ? go(k_attend_rows<bf16_t, int8_t>) : go(k_attend_rows<bf16_t, bf16_t>);
-  else C->dtype == MOE_I8 ? go(k_attend_rows<f16_t, int8_t>) : go(k_attend_rows<f16_t, f16_t>);
-  return launched("moe_window_attention");
+  const int runs = max_runs(*C, *W, n_heads);
+  AttendArgs a{cache_args(*C), window_args(*W, *C), q, out, lse, (float*)workspace, nullptr, ldq, ldo, n_heads, runs,
+               wide_rule(*C, *W, n_heads), scale};
+  a.part_ml = a.part + (int64_t)n * n_heads * runs * C->head_dim;
+  return dtype == MOE_BF16 ? run_attend<bf16_t>((hipStream_t)stream, a, C->dtype == MOE_I8)
+                           : run_attend<f16_t>((hipStream_t)stream, a, C->dtype == MOE_I8);
 }
 
 size_t moe_token_logprobs_bytes(int rows, int n, int k) {
