@@ -493,8 +493,8 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
  * id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. scale > 0.
  * Each output is written when its pointer is not NULL (tokens and logp, given > 0: all or none; top_ids and top_logp, k > 0:
  * all or none; at least one output). logits [rows][ld] in `dtype`, tokens int32 [rows][given]. n <= MOE_MAX_VOCAB,
- * given <= 64, k <= 32 and k <= n. Sums of up to 256 terms in float32, of those in 64 bits; a row's bits do not depend on the others.
- * workspace: moe_token_logprobs_bytes, 16-byte aligned (0 bytes and NULL if that says so). Errors: MOE_E_ARG (null or
+ * given <= 64, k <= 32 and k <= n. Sums of up to 2^14 terms in float32 (up to 64 one after the other), of those in 64 bits; a row's bits do not depend on the others.
+ * workspace: moe_token_logprobs_bytes (0 for sizes that the call refuses), 16-byte aligned. Errors: MOE_E_ARG (null or
  * misaligned pointer, bad type, stride, count or scale, overlap), MOE_E_SHAPE (rows > MOE_MAX_ROWS, n not in
  * 1..MOE_MAX_VOCAB), MOE_E_WS. */
 #define MOE_MAX_VOCAB (1 << 22)

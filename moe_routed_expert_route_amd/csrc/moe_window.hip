@@ -850,83 +850,284 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 }
 
 // ------------------------------------------------------------------ log probabilities -------
+//
+// A row is cut into pieces of 256 lanes times EL values (by the row's length alone, so that its sums have one order).
+// k_scores takes a piece into registers, reads it once, and leaves its maximum, its sums of e = exp(z) and of e z, and the best
+// tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The
+// pieces' bound for the best: the k-th largest of the 256 lanes' maxima (of its first 16 bits); k lanes have a value of at
+// least that, and few values are above it.
 
 struct ScoreArgs {
   const void* logits;
   const int32_t* tokens;
   float *logp, *entropy, *top_logp;
   int32_t* top_ids;
+  float* stats;       // [row][piece] maximum, sum of e, sum of e z, and how many best
+  uint64_t* best;     // [row][piece][kKept] their keys
   int64_t ld;
-  int n, given, k, dtype;
+  int n, given, k, pieces;
   float scale;
 };
 
+constexpr int kKept = 64;     // best tokens that a piece hands on
+constexpr int kListed = 512;  // and those it can choose them from
+
 __device__ __forceinline__ float masked_logit(float x) {   // NaN is -infinity, infinity the largest number
-  x = x == x ? x : -__builtin_inff();
-  return __builtin_fminf(x, 0x1.fffffep127f);
+  return __builtin_fminf(__builtin_fmaxf(x, -__builtin_inff()), 0x1.fffffep127f);
+}
+// Ordered as the values are, -0 as 0; kMasked and below: -infinity.
+constexpr uint32_t kMasked = 0x007FFFFFu;
+__device__ __forceinline__ uint32_t order_of(float x) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, x + 0.0f);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float value_of(uint32_t order) {
+  return __builtin_bit_cast(float, order >> 31 ? order ^ 0x80000000u : ~order);
+}
+// Larger values first, then lower ids.
+__device__ __forceinline__ uint64_t key_of(float x, int id) { return (uint64_t)order_of(masked_logit(x)) << 32 | (uint32_t)~id; }
+
+__device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
+#pragma unroll
+  for (int o = 32; o; o /= 2) {
+    const uint64_t u = (uint64_t)__shfl_xor((unsigned long long)v, o);
+    v = u > v ? u : v;
+  }
+  return v;
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+#pragma unroll
+  for (int o = 32; o; o /= 2) v += __shfl_xor(v, o);
+  return v;
 }
 
-// A workgroup a row, which goes over it once for the maximum, once for the sums and once for each of the k best.
-template <typename T>
-__global__ __launch_bounds__(256) void k_logprobs_rows(ScoreArgs a) {
-  __shared__ double s_red[3][4];
+// The k best of `list` (n keys that differ, n <= 64 PER) into out, largest first, 0 where there are none left; by one wave.
+template <int PER, typename F>
+__device__ __forceinline__ void choose(const uint64_t* list, int n, int k, F out) {
+  const int lane = threadIdx.x & 63;
+  uint64_t v[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = i * 64 + lane < n ? list[i * 64 + lane] : 0;
+  for (int c = 0; c < k; ++c) {
+    uint64_t mine = v[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) mine = v[i] > mine ? v[i] : mine;
+    const uint64_t top = wave_max64(mine);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) v[i] = v[i] == top ? 0 : v[i];
+    out(c, top);
+  }
+}
+
+// z = x c - r in units of log 2, with c the float32 unit and r its reference: the float32 product top c, whose rounding
+// the join makes good, or the product itself where that is large.
+constexpr float kFused = 0x1p20f;
+__device__ __forceinline__ float unit_of(float scale) { return scale * 1.44269504088896340736f; }
+__device__ __forceinline__ double reference(float top, float c) {
+  const float tc = top * c;
+  return __builtin_fabsf(tc) < kFused ? (double)tc : (double)top * (double)c;
+}
+
+template <typename T, int EL>
+__global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
+  constexpr int PIECES = EL / 8;
+  __shared__ uint32_t s_top[256];
+  __shared__ uint64_t s_list[kListed];
+  __shared__ float s_sum[2][4];
   __shared__ uint64_t s_key[4];
-  const int64_t row = blockIdx.x;
+  __shared__ int s_count;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
+  const int64_t row = blockIdx.x / a.pieces;
+  const int piece = blockIdx.x % a.pieces, from = piece * (256 * EL);
   const T* x = (const T*)a.logits + row * a.ld;
-  const int wave = threadIdx.x >> 6;
-  // larger logits first, then lower ids
-  auto key_of = [&](int i) {
-    const uint32_t b = __builtin_bit_cast(uint32_t, masked_logit(to_f(x[i])) + 0.0f);
-    return (uint64_t)(b >> 31 ? ~b : b | 0x80000000u) << 32 | (uint32_t)~i;
-  };
-  double log_sum = 0.0, mean = 0.0;
-  float top = 0.0f;
-  bool none = true;
-  uint64_t bound = ~0ull;
-  for (int c = 0; c < (a.k > 0 ? a.k : 1); ++c) {
-    uint64_t best = 0;
-    for (int i = threadIdx.x; i < a.n; i += 256) {
-      const uint64_t key = key_of(i);
-      if (key < bound && key > best) best = key;
+  T raw[PIECES][8];
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p) {
+    const int i = from + p * 2048 + tid * 8;
+    if (i + 8 <= a.n) {
+      __builtin_memcpy(raw[p], x + i, sizeof raw[p]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) raw[p][e] = i + e < a.n ? x[i + e] : from_f<T>(-__builtin_inff());
     }
-    for (int o = 32; o; o /= 2) best = max(best, (uint64_t)__shfl_xor((unsigned long long)best, o));
-    if ((threadIdx.x & 63) == 0) s_key[wave] = best;
-    __syncthreads();
-    best = max(max(s_key[0], s_key[1]), max(s_key[2], s_key[3]));
-    bound = best;
-    const int id = (int)~(uint32_t)best;
-    const float v = masked_logit(to_f(x[id]));
-    if (c == 0) {
-      none = v == -__builtin_inff();
-      top = none ? 0.0f : v;
-      double sum = 0.0, dot = 0.0;
-      for (int i = threadIdx.x; i < a.n; i += 256) {
-        const double z = ((double)masked_logit(to_f(x[i])) - (double)top) * (double)a.scale;
-        const double e = exp64(z);
-        sum += e;
-        if (e > 0.0) dot = __builtin_fma(e, z, dot);
+  }
+  if (tid == 0) s_count = 0;
+  float mine = -__builtin_inff();
+#pragma unroll
+  for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine = __builtin_fmaxf(mine, to_f(raw[p][e]));
+  mine = __builtin_fminf(mine, 0x1.fffffep127f);
+  const uint32_t my_order = order_of(mine);
+  s_top[tid] = my_order;
+  __syncthreads();
+  uint32_t tops[4], most = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    tops[i] = s_top[i * 64 + lane];
+    most = max(most, tops[i]);
+  }
+  most = wave_max(most);
+  const bool none = most <= kMasked;
+  const float top = none ? 0.0f : value_of(most);
+
+  // below -200 (masked tokens too) z counts as that, and e is 0
+  const float c = unit_of(a.scale), tc = top * c;
+  float sum = 0.0f, dot = 0.0f;
+  if (__builtin_fabsf(tc) < kFused) {
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = __builtin_fmaxf(__builtin_fmaf(to_f(raw[p][e]), c, -tc), -200.0f);
+        const float y = __builtin_amdgcn_exp2f(z);
+        sum += y;
+        dot = __builtin_fmaf(y, z, dot);
       }
-      sum = wave_sum(sum);
-      dot = wave_sum(dot);
-      if ((threadIdx.x & 63) == 0) s_red[0][wave] = sum, s_red[1][wave] = dot;
-      __syncthreads();
-      sum = s_red[0][0] + s_red[0][1] + s_red[0][2] + s_red[0][3];
-      dot = s_red[1][0] + s_red[1][1] + s_red[1][2] + s_red[1][3];
-      log_sum = none ? 0.0 : log(sum);
-      mean = none ? 0.0 : dot / sum;
+  } else {   // the rounding of tc counts, or it is out of range: the difference first
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float z = __builtin_fmaxf((masked_logit(to_f(raw[p][e])) - top) * c, -200.0f);
+        const float y = __builtin_amdgcn_exp2f(z);
+        sum += y;
+        dot = __builtin_fmaf(y, z, dot);
+      }
+  }
+  sum = wave_sum_f(sum);
+  dot = wave_sum_f(dot);
+  if (lane == 0) s_sum[0][wave] = sum, s_sum[1][wave] = dot;
+
+  uint32_t bound = kMasked >> 16;
+  if (a.k > 0 && !none) {
+    uint32_t t = 0;
+#pragma unroll
+    for (int b = 15; b >= 0; --b) {
+      const uint32_t next = (t | 1u << b) << 16;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(tops[i] >= next));
+      t = n >= a.k ? t | 1u << b : t;
     }
-    if (threadIdx.x == 0 && a.k > 0) {
-      a.top_ids[row * a.k + c] = id;
-      a.top_logp[row * a.k + c] = (float)(((double)v - (double)top) * (double)a.scale - log_sum);
+    bound = max(t, (kMasked >> 16) + 1);
+    for (uint64_t hot = __ballot(my_order >> 16 >= bound); hot; hot &= hot - 1) {
+      const int h = __builtin_ctzll(hot), i = from + (lane >> 3) * 2048 + (wave * 64 + h) * 8 + (lane & 7);
+      if (lane < EL && i < a.n) {
+        const uint64_t key = key_of(to_f(x[i]), i);
+        if (key >> 48 >= bound) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kListed) s_list[at] = key;
+        }
+      }
+    }
+  }
+  __syncthreads();
+  float* stats = a.stats + (int64_t)blockIdx.x * 4;
+  uint64_t* best = a.best + (int64_t)blockIdx.x * kKept;
+  const int count = s_count;
+  if (tid == 0) {
+    stats[0] = none ? -__builtin_inff() : top;
+    stats[1] = none ? 0.0f : (s_sum[0][0] + s_sum[0][1]) + (s_sum[0][2] + s_sum[0][3]);
+    stats[2] = none ? 0.0f : (s_sum[1][0] + s_sum[1][1]) + (s_sum[1][2] + s_sum[1][3]);
+    stats[3] = __builtin_bit_cast(float, count <= kKept ? count : a.k);
+  }
+  if (count <= kKept) {
+    if (tid < count) best[tid] = s_list[tid];
+  } else if (count <= kListed) {
+    if (wave == 0) choose<kListed / 64>(s_list, count, a.k, [&](int i, uint64_t key) {
+      if (lane == 0) best[i] = key;
+    });
+  } else {   // many equal values: one after the other
+    uint64_t last = ~0ull;
+    for (int i = 0; i < a.k; ++i) {
+      uint64_t next = 0;
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint64_t key = key_of(to_f(raw[p][e]), from + p * 2048 + tid * 8 + e);
+          if (key < last && key > next) next = key;
+        }
+      next = wave_max64(next);
+      if (lane == 0) s_key[wave] = next;
+      __syncthreads();
+      last = max(max(s_key[0], s_key[1]), max(s_key[2], s_key[3]));
+      __syncthreads();
+      if (tid == 0) best[i] = last;
+    }
+  }
+}
+
+// A wave a row.
+template <typename T>
+__global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
+  __shared__ uint64_t s_list[kListed];
+  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x;
+  const T* x = (const T*)a.logits + row * a.ld;
+  const float* stats = a.stats + row * a.pieces * 4;
+  const float c = unit_of(a.scale);
+  float top = -__builtin_inff();
+  for (int p = lane; p < a.pieces; p += 64) top = __builtin_fmaxf(top, stats[4 * p]);
+#pragma unroll
+  for (int o = 32; o; o /= 2) top = __builtin_fmaxf(top, __shfl_xor(top, o));
+  const bool none = top == -__builtin_inff();
+  const double ref = none ? 0.0 : reference(top, c), ln2 = 0.6931471805599453;
+  double sum = 0.0, dot = 0.0;
+  for (int p = lane; p < a.pieces; p += 64) {
+    const float m = stats[4 * p];
+    if (m == -__builtin_inff()) continue;
+    const double z = reference(m, c) - ref, f = exp64(z * ln2), s = (double)stats[4 * p + 1];
+    sum = __builtin_fma(s, f, sum);
+    dot = __builtin_fma(f, __builtin_fma(s, f > 0.0 ? z : 0.0, (double)stats[4 * p + 2]), dot);
+  }
+  sum = wave_sum(sum);
+  dot = wave_sum(dot);
+  const double log_sum = none ? 0.0 : log(sum), base = none ? 0.0 : (double)top;
+  const double rest = ((base * (double)c) - ref) * ln2 - log_sum;
+  auto logp_of = [&](float v) { return (float)(((double)v - base) * (double)a.scale + rest); };
+  if (lane == 0 && a.entropy) a.entropy[row] = none ? 0.0f : (float)(log_sum - dot / sum * ln2);
+  if (lane < a.given) {
+    const int id = a.tokens[row * a.given + lane];
+    a.logp[row * a.given + lane] = logp_of(id >= 0 && id < a.n ? masked_logit(to_f(x[id])) : -__builtin_inff());
+  }
+  if (a.k == 0) return;
+  // the pieces' best, as many pieces at a time as the list holds
+  int have = 0;
+  for (int p = 0; p < a.pieces;) {
+    for (; p < a.pieces; ++p) {
+      const int count = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, stats[4 * p + 3]));
+      if (have + count > kListed) break;
+      if (lane < count) s_list[have + lane] = a.best[(row * a.pieces + p) * kKept + lane];
+      have += count;
     }
     __syncthreads();
+    uint64_t mine = 0;   // of the k best, lane by lane
+    auto take = [&](int i, uint64_t key) { mine = lane == i ? key : mine; };
+    if (have <= 64) choose<1>(s_list, have, a.k, take);
+    else if (have <= 128) choose<2>(s_list, have, a.k, take);
+    else choose<kListed / 64>(s_list, have, a.k, take);
+    __syncthreads();
+    if (lane < a.k) s_list[lane] = mine;
+    have = __popcll(__ballot(lane < a.k && mine != 0));
+    __syncthreads();
   }
-  if ((int)threadIdx.x < a.given) {
-    const int id = a.tokens[row * a.given + threadIdx.x];
-    const float v = id >= 0 && id < a.n ? masked_logit(to_f(x[id])) : -__builtin_inff();
-    a.logp[row * a.given + threadIdx.x] = (float)(((double)v - (double)top) * (double)a.scale - log_sum);
+  if (lane < have) {
+    const uint64_t key = s_list[lane];
+    a.top_ids[row * a.k + lane] = (int)~(uint32_t)key;
+    a.top_logp[row * a.k + lane] = logp_of(value_of((uint32_t)(key >> 32)));
   }
-  if (threadIdx.x == 0 && a.entropy) a.entropy[row] = (float)(log_sum - mean);
+  for (int i = 0; have < a.k && i < a.n; i += 64) {   // then masked tokens, lowest id first
+    const bool masked = i + lane < a.n && order_of(masked_logit(to_f(x[i + lane < a.n ? i + lane : 0]))) <= kMasked;
+    const uint64_t all = __ballot(masked);
+    const int at = have + __popcll(all & ((1ull << lane) - 1));
+    if (masked && at < a.k) {
+      a.top_ids[row * a.k + at] = i + lane;
+      a.top_logp[row * a.k + at] = -__builtin_inff();
+    }
+    have += __popcll(all);
+  }
 }
 
 // ------------------------------------------------------------------ host checks -------------
@@ -1073,6 +1274,9 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
+constexpr int kScoreEl = 32;
+int pieces_of(int n) { return (n + 256 * kScoreEl - 1) / (256 * kScoreEl); }
+
 }  // namespace moe
 
 using namespace moe;
@@ -1175,8 +1379,8 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
 }
 
 size_t moe_token_logprobs_bytes(int rows, int n, int k) {
-  if (rows < 0 || rows > MOE_MAX_ROWS || n < 1 || n > MOE_MAX_VOCAB || k < 0 || k > 32 || k > n) return 0;
-  return 0;
+  if (rows < 1 || rows > MOE_MAX_ROWS || n < 1 || n > MOE_MAX_VOCAB || k < 0 || k > 32 || k > n) return 0;
+  return (size_t)rows * pieces_of(n) * (16 + (k ? 8 * kKept : 0));
 }
 
 int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, int rows, int n, float scale,
@@ -1194,19 +1398,25 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
       !aligned(top_ids, 4) || !aligned(top_logp, 4))
     return MOE_E_ARG;
   const size_t need = moe_token_logprobs_bytes(rows, n, k);
-  if (need && (!workspace || ws_bytes < need || !aligned(workspace, 16))) return MOE_E_WS;
+  if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return MOE_E_WS;
   const Rows in[] = {rows_of(logits, rows, n, ld, type_size(dtype)), rows_of(tokens, 1, (int64_t)rows * given, 0, 4)};
   const Rows outs[] = {rows_of(logp, 1, (int64_t)rows * given, 0, 4), rows_of(entropy, 1, rows, 0, 4),
                        rows_of(top_ids, 1, (int64_t)rows * k, 0, 4), rows_of(top_logp, 1, (int64_t)rows * k, 0, 4),
-                       rows_of(workspace, need ? 1 : 0, (int64_t)need, 0, 1)};
+                       rows_of(workspace, 1, (int64_t)need, 0, 1)};
   for (int i = 0; i < 5; ++i) {
     if (over(outs[i], in)) return MOE_E_ARG;
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return MOE_E_ARG;
   }
-  const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, ld, n, given, k, dtype, scale};
+  const int pieces = pieces_of(n);
+  const int64_t blocks = (int64_t)rows * pieces;
+  if (blocks * 256 > kLaunchThreads) return MOE_E_SHAPE;
+  float* const stats = (float*)workspace;
+  const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, stats, (uint64_t*)(stats + 4 * blocks), ld, n, given, k, pieces, scale};
   with_type(dtype, [&](auto t) {
-    hipLaunchKernelGGL(k_logprobs_rows<decltype(t)>, dim3(rows), dim3(256), 0, (hipStream_t)stream, a);
+    using T = decltype(t);
+    hipLaunchKernelGGL((k_scores<T, kScoreEl>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    hipLaunchKernelGGL(k_scores_join<T>, dim3(rows), dim3(64), 0, (hipStream_t)stream, a);
   });
   return launched("moe_token_logprobs");
 }
