@@ -854,7 +854,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 // A row is cut into pieces of 256 lanes times EL values (by the row's length alone, so that its sums have one order).
 // k_scores takes a piece into registers, reads it once, and leaves its maximum, its sums of e = exp(z) and of e z, and the best
 // tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The
-// pieces' bound for the best: the k-th largest of the 256 lanes' maxima (of its first 16 bits); k lanes have a value of at
+// pieces' bound for the best: the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at
 // least that, and few values are above it.
 
 struct ScoreArgs {
@@ -887,13 +887,20 @@ __device__ __forceinline__ float value_of(uint32_t order) {
 // Larger values first, then lower ids.
 __device__ __forceinline__ uint64_t key_of(float x, int id) { return (uint64_t)order_of(masked_logit(x)) << 32 | (uint32_t)~id; }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint64_t dpp_max64(uint64_t v) {
+  const uint64_t u = (uint64_t)dpp0<CTRL, ROWS>((uint32_t)v) | (uint64_t)dpp0<CTRL, ROWS>((uint32_t)(v >> 32)) << 32;
+  return u > v ? u : v;
+}
 __device__ __forceinline__ uint64_t wave_max64(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o; o /= 2) {
-    const uint64_t u = (uint64_t)__shfl_xor((unsigned long long)v, o);
-    v = u > v ? u : v;
-  }
-  return v;
+  v = dpp_max64<0x111, 0xF>(v);
+  v = dpp_max64<0x112, 0xF>(v);
+  v = dpp_max64<0x114, 0xF>(v);
+  v = dpp_max64<0x118, 0xF>(v);
+  v = dpp_max64<0x142, 0xA>(v);
+  v = dpp_max64<0x143, 0xC>(v);
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)v, 63) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(v >> 32), 63) << 32;
 }
 __device__ __forceinline__ float wave_sum_f(float v) {
 #pragma unroll
@@ -928,6 +935,22 @@ __device__ __forceinline__ double reference(float top, float c) {
   return __builtin_fabsf(tc) < kFused ? (double)tc : (double)top * (double)c;
 }
 
+// Eight neighbouring values as they are in memory.
+template <typename T>
+struct Eight {
+  static constexpr int W = sizeof(T) * 2;
+  uint32_t w[W];
+  __device__ __forceinline__ float at(int e) const {
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
+    else return to_f(__builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e & 1)))));
+  }
+  // What follows converts anew rather than keep a register for each value.
+  __device__ __forceinline__ void forget() {
+#pragma unroll
+    for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+  }
+};
+
 template <typename T, int EL>
 __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   constexpr int PIECES = EL / 8;
@@ -940,15 +963,17 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   const int64_t row = blockIdx.x / a.pieces;
   const int piece = blockIdx.x % a.pieces, from = piece * (256 * EL);
   const T* x = (const T*)a.logits + row * a.ld;
-  T raw[PIECES][8];
+  Eight<T> raw[PIECES];
 #pragma unroll
   for (int p = 0; p < PIECES; ++p) {
     const int i = from + p * 2048 + tid * 8;
     if (i + 8 <= a.n) {
-      __builtin_memcpy(raw[p], x + i, sizeof raw[p]);
+      __builtin_memcpy(raw[p].w, x + i, sizeof raw[p].w);
     } else {
+      T v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) raw[p][e] = i + e < a.n ? x[i + e] : from_f<T>(-__builtin_inff());
+      for (int e = 0; e < 8; ++e) v[e] = i + e < a.n ? x[i + e] : from_f<T>(-__builtin_inff());
+      __builtin_memcpy(raw[p].w, v, sizeof v);
     }
   }
   if (tid == 0) s_count = 0;
@@ -956,18 +981,13 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
 #pragma unroll
   for (int p = 0; p < PIECES; ++p)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) mine = __builtin_fmaxf(mine, to_f(raw[p][e]));
+    for (int e = 0; e < 8; ++e) mine = __builtin_fmaxf(mine, raw[p].at(e));
   mine = __builtin_fminf(mine, 0x1.fffffep127f);
   const uint32_t my_order = order_of(mine);
   s_top[tid] = my_order;
   __syncthreads();
-  uint32_t tops[4], most = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    tops[i] = s_top[i * 64 + lane];
-    most = max(most, tops[i]);
-  }
-  most = wave_max(most);
+  const uint32_t four = max(max(s_top[lane], s_top[64 + lane]), max(s_top[128 + lane], s_top[192 + lane]));
+  const uint32_t most = wave_max(four);
   const bool none = most <= kMasked;
   const float top = none ? 0.0f : value_of(most);
 
@@ -976,24 +996,28 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   float sum = 0.0f, dot = 0.0f;
   if (__builtin_fabsf(tc) < kFused) {
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p)
+    for (int p = 0; p < PIECES; ++p) {
+      raw[p].forget();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = __builtin_fmaxf(__builtin_fmaf(to_f(raw[p][e]), c, -tc), -200.0f);
+        const float z = __builtin_fmaxf(__builtin_fmaf(raw[p].at(e), c, -tc), -200.0f);
         const float y = __builtin_amdgcn_exp2f(z);
         sum += y;
         dot = __builtin_fmaf(y, z, dot);
       }
+    }
   } else {   // the rounding of tc counts, or it is out of range: the difference first
 #pragma unroll
-    for (int p = 0; p < PIECES; ++p)
+    for (int p = 0; p < PIECES; ++p) {
+      raw[p].forget();
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float z = __builtin_fmaxf((masked_logit(to_f(raw[p][e])) - top) * c, -200.0f);
+        const float z = __builtin_fmaxf((masked_logit(raw[p].at(e)) - top) * c, -200.0f);
         const float y = __builtin_amdgcn_exp2f(z);
         sum += y;
         dot = __builtin_fmaf(y, z, dot);
       }
+    }
   }
   sum = wave_sum_f(sum);
   dot = wave_sum_f(dot);
@@ -1005,16 +1029,24 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
 #pragma unroll
     for (int b = 15; b >= 0; --b) {
       const uint32_t next = (t | 1u << b) << 16;
-      int n = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) n += __popcll(__ballot(tops[i] >= next));
-      t = n >= a.k ? t | 1u << b : t;
+      if (__popcll(__ballot(four >= next)) >= a.k) t |= 1u << b;
     }
     bound = max(t, (kMasked >> 16) + 1);
-    for (uint64_t hot = __ballot(my_order >> 16 >= bound); hot; hot &= hot - 1) {
-      const int h = __builtin_ctzll(hot), i = from + (lane >> 3) * 2048 + (wave * 64 + h) * 8 + (lane & 7);
-      if (lane < EL && i < a.n) {
-        const uint64_t key = key_of(to_f(x[i]), i);
+    // the values of the lanes that have some, a lane's by the wave, four lanes at a time
+    for (uint64_t hot = __ballot(my_order >> 16 >= bound); hot;) {
+      float v[4];
+      int id[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int h = hot ? __builtin_ctzll(hot) : 0;
+        id[j] = from + (lane >> 3) * 2048 + (wave * 64 + h) * 8 + (lane & 7);
+        const bool in = hot && lane < EL && id[j] < a.n;
+        v[j] = in ? to_f(x[id[j]]) : -__builtin_inff();
+        hot &= hot - 1;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t key = key_of(v[j], id[j]);
         if (key >> 48 >= bound) {
           const int at = atomicAdd(&s_count, 1);
           if (at < kListed) s_list[at] = key;
@@ -1042,13 +1074,10 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
     uint64_t last = ~0ull;
     for (int i = 0; i < a.k; ++i) {
       uint64_t next = 0;
-#pragma unroll
-      for (int p = 0; p < PIECES; ++p)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t key = key_of(to_f(raw[p][e]), from + p * 2048 + tid * 8 + e);
-          if (key < last && key > next) next = key;
-        }
+      for (int at = from + tid; at < min(a.n, from + 256 * EL); at += 256) {
+        const uint64_t key = key_of(to_f(x[at]), at);
+        if (key < last && key > next) next = key;
+      }
       next = wave_max64(next);
       if (lane == 0) s_key[wave] = next;
       __syncthreads();
@@ -1062,7 +1091,7 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
 // A wave a row.
 template <typename T>
 __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
-  __shared__ uint64_t s_list[kListed];
+  __shared__ uint64_t s_list[kListed + 64];
   const int64_t row = blockIdx.x;
   const int lane = threadIdx.x;
   const T* x = (const T*)a.logits + row * a.ld;
@@ -1093,26 +1122,42 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
     a.logp[row * a.given + lane] = logp_of(id >= 0 && id < a.n ? masked_logit(to_f(x[id])) : -__builtin_inff());
   }
   if (a.k == 0) return;
-  // the pieces' best, as many pieces at a time as the list holds
+  // the pieces' best, eight pieces at a time
   int have = 0;
-  for (int p = 0; p < a.pieces;) {
-    for (; p < a.pieces; ++p) {
-      const int count = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, stats[4 * p + 3]));
-      if (have + count > kListed) break;
-      if (lane < count) s_list[have + lane] = a.best[(row * a.pieces + p) * kKept + lane];
-      have += count;
-    }
-    __syncthreads();
-    uint64_t mine = 0;   // of the k best, lane by lane
+  uint64_t mine = 0;   // of the k best, lane by lane
+  auto choose_from = [&]() {
+    mine = 0;
     auto take = [&](int i, uint64_t key) { mine = lane == i ? key : mine; };
+    __syncthreads();
     if (have <= 64) choose<1>(s_list, have, a.k, take);
     else if (have <= 128) choose<2>(s_list, have, a.k, take);
-    else choose<kListed / 64>(s_list, have, a.k, take);
+    else if (have <= 256) choose<4>(s_list, have, a.k, take);
+    else choose<(kListed + 64) / 64>(s_list, have, a.k, take);
     __syncthreads();
     if (lane < a.k) s_list[lane] = mine;
     have = __popcll(__ballot(lane < a.k && mine != 0));
-    __syncthreads();
+  };
+  for (int p0 = 0; p0 < a.pieces; p0 += 64) {
+    const int counts = p0 + lane < a.pieces ? __builtin_bit_cast(int, stats[4 * (p0 + lane) + 3]) : 0;
+    const uint64_t* best = a.best + (row * a.pieces + p0) * kKept;
+    for (int p = 0; p < 64 && p0 + p < a.pieces; p += 8) {
+      uint64_t key[8];
+      int count[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        count[i] = __builtin_amdgcn_readlane(counts, p + i);
+        key[i] = lane < count[i] ? best[(p + i) * kKept + lane] : 0;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (have + count[i] > kListed + 64) choose_from();
+        if (lane < count[i]) s_list[have + lane] = key[i];
+        have += count[i];
+      }
+    }
   }
+  choose_from();
+  __syncthreads();
   if (lane < have) {
     const uint64_t key = s_list[lane];
     a.top_ids[row * a.k + lane] = (int)~(uint32_t)key;
@@ -1274,8 +1319,8 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
-constexpr int kScoreEl = 32;
-int pieces_of(int n) { return (n + 256 * kScoreEl - 1) / (256 * kScoreEl); }
+constexpr int kShortRow = 65536;
+int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 16383) / 16384; }
 
 }  // namespace moe
 
@@ -1415,7 +1460,8 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
   const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, stats, (uint64_t*)(stats + 4 * blocks), ld, n, given, k, pieces, scale};
   with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    hipLaunchKernelGGL((k_scores<T, kScoreEl>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    if (n <= kShortRow) hipLaunchKernelGGL((k_scores<T, 32>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    else hipLaunchKernelGGL((k_scores<T, 64>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
     hipLaunchKernelGGL(k_scores_join<T>, dim3(rows), dim3(64), 0, (hipStream_t)stream, a);
   });
   return launched("moe_token_logprobs");
