@@ -34,18 +34,22 @@ __device__ __forceinline__ bool seq_ok(const WindowArgs& w, int start, int end, 
   return start >= 0 && start <= end && end <= w.n_tokens && end - start <= most && ctx >= 0 && ctx <= w.max_keys - (end - start);
 }
 // The sequence that a row is of (the last that starts at or before it: one without tokens is passed over); tokens = 0:
-// none, or one that is left out. Uniform over the wave: a lane looks at one start in 64.
+// none, or one that is left out. Uniform over the wave: a lane looks at one sequence in 64, all it needs at once.
 __device__ __forceinline__ Seq seq_of(const WindowArgs& w, int row, int most) {
-  int n = 0;
+  Seq q{0, 0, 0, 0};
   for (int i = 0; i < w.n_seqs; i += 64) {
-    const int at = i + (int)(threadIdx.x & 63);
-    n += __popcll(__ballot(at < w.n_seqs && w.row_start[at < w.n_seqs ? at : 0] <= row));
+    const int at = min(i + (int)(threadIdx.x & 63), w.n_seqs - 1);
+    const int start = w.row_start[at], end = w.row_start[at + 1], ctx = w.ctx_len[at];
+    const int n = __popcll(__ballot(start <= row && i + (int)(threadIdx.x & 63) < w.n_seqs));
+    if (n == 0) continue;   // of an ascending list: the ones before have it
+    q.s = i + n - 1;
+    q.start = __builtin_amdgcn_readlane(start, n - 1);
+    q.tokens = __builtin_amdgcn_readlane(end, n - 1);   // the end, so far
+    q.ctx = __builtin_amdgcn_readlane(ctx, n - 1);
   }
-  n = __builtin_amdgcn_readfirstlane(n);
-  if (n == 0) return Seq{0, 0, 0, 0};
-  const int start = w.row_start[n - 1], end = w.row_start[n], ctx = w.ctx_len[n - 1];
-  if (row >= end || !seq_ok(w, start, end, ctx, most)) return Seq{0, 0, 0, 0};
-  return Seq{n - 1, start, end - start, ctx};
+  if (row >= q.tokens || !seq_ok(w, q.start, q.tokens, q.ctx, most)) return Seq{0, 0, 0, 0};
+  q.tokens -= q.start;
+  return q;
 }
 // One workgroup of a launch looks at every sequence.
 __device__ __forceinline__ void check_seqs(const WindowArgs& w, int most, int threads) {
@@ -266,17 +270,14 @@ struct AttendArgs {
   void* out;
   float *lse, *part, *part_ml;   // of runs: [row][head][max_runs] head_dim values, and (maximum, sum)
   int64_t ldq, ldo;
-  int n_heads, max_runs, wide;
+  int n_heads, max_runs, least_run;
   float scale;
 };
 
-// Keys of a run, by the sequence's own length: short enough to spread one long sequence over the card, long enough that the
-// runs' results (4 bytes a value, written and read) stay small beside the cache's rows.
-__host__ __device__ __forceinline__ int run_of(int keys, int wide) {
-  return wide ? max(1024, ((keys >> 5) + 256) & ~255) : max(256, ((keys >> 6) + 256) & ~255);
-}
-__host__ __device__ __forceinline__ int runs_of(int keys, int wide) {
-  const int run = run_of(keys, wide);
+// Keys of a run: `least` (by the call's sizes), or what makes kMaxRuns of the sequence's keys.
+__host__ __device__ __forceinline__ int run_of(int keys, int least) { return max(least, ((keys >> 6) + 256) & ~255); }
+__host__ __device__ __forceinline__ int runs_of(int keys, int least) {
+  const int run = run_of(keys, least);
   return (int)(((int64_t)keys + run - 1) / run);
 }
 constexpr int kMaxRuns = 64;   // runs_of of any count
@@ -342,9 +343,9 @@ struct Keys {
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset past any buffer: the load gives 0 and touches nothing
 
 // HD: 64, 128 or 256, the least that holds head_dim. NT: a wave's tiles of 16 rows. WIDE: the waves share the keys and
-// have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. AHEAD: the next keys are
-// loaded before these are used.
-template <typename T, bool I8, int HD, int NT, bool WIDE, bool AHEAD>
+// have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. AHEAD: the next keys
+// (1), and their values too (2), are loaded before these are used (0: there are no registers for that).
+template <typename T, bool I8, int HD, int NT, bool WIDE, int AHEAD>
 __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
   using M = Mat<T>;
   using KV = Keys<I8, HD>;
@@ -355,49 +356,71 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
   extern __shared__ int s_end[];   // [n_seqs]: items of the sequences up to this one
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quad = lane >> 4;
   const int G = a.n_heads / a.c.n_kv, d = a.c.d;
-  int total = 0;
-  for (int i0 = 0; i0 < a.w.n_seqs; i0 += 256) {
-    const int i = i0 + tid;
-    int n = 0;
-    if (i < a.w.n_seqs) {
-      const int start = a.w.row_start[i], end = a.w.row_start[i + 1], ctx = a.w.ctx_len[i];
-      if (!seq_ok(a.w, start, end, ctx, a.w.max_window)) {
-        if (blockIdx.x == 0) atomicOr(a.w.err, MOE_ERR_WINDOW);
-      } else if (end > start) {
-        n = ((end - start) * G + ROWS - 1) / ROWS * runs_of(ctx + end - start, a.wide) * a.c.n_kv;
-      }
+  auto items_of = [&](int i, int start, int end, int ctx) {
+    if (!seq_ok(a.w, start, end, ctx, a.w.max_window)) {
+      if (blockIdx.x == 0) atomicOr(a.w.err, MOE_ERR_WINDOW);
+      return 0;
     }
+    return end > start ? ((end - start) * G + ROWS - 1) / ROWS * runs_of(ctx + end - start, a.least_run) * a.c.n_kv : 0;
+  };
+  auto scan = [&](int n) {
 #pragma unroll
     for (int o = 1; o < 64; o *= 2) {
       const int up = __shfl_up(n, o);
       if (lane >= o) n += up;
     }
-    if (lane == 63) s_wave[wave] = n;
-    __syncthreads();
-    for (int w = 0; w < wave; ++w) n += s_wave[w];
-    if (i < a.w.n_seqs) s_end[i] = total + n;
-    total += s_wave[0] + s_wave[1] + s_wave[2] + s_wave[3];
-    __syncthreads();
+    return n;
+  };
+  // items of the sequences up to each: in the lanes of every wave, or, of more than 64, in LDS
+  int total = 0, my_start = 0, my_end = 0, my_ctx = 0, my_items = 0;
+  const bool few = a.w.n_seqs <= 64;
+  if (few) {
+    int n = 0;
+    if (lane < a.w.n_seqs) {
+      my_start = a.w.row_start[lane], my_end = a.w.row_start[lane + 1], my_ctx = a.w.ctx_len[lane];
+      n = items_of(lane, my_start, my_end, my_ctx);
+    }
+    my_items = scan(n);
+    total = __builtin_amdgcn_readlane(my_items, 63);
+  } else {
+    for (int i0 = 0; i0 < a.w.n_seqs; i0 += 256) {
+      const int i = i0 + tid;
+      int n = scan(i < a.w.n_seqs ? items_of(i, a.w.row_start[i], a.w.row_start[i + 1], a.w.ctx_len[i]) : 0);
+      if (lane == 63) s_wave[wave] = n;
+      __syncthreads();
+      for (int w = 0; w < wave; ++w) n += s_wave[w];
+      if (i < a.w.n_seqs) s_end[i] = total + n;
+      total += s_wave[0] + s_wave[1] + s_wave[2] + s_wave[3];
+      __syncthreads();
+    }
+    total = __builtin_amdgcn_readfirstlane(total);
   }
-  total = __builtin_amdgcn_readfirstlane(total);
   // neighbouring items, the tiles of one run among them, on one die
   const int first = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
   const float c = a.scale == 0.0f ? 1.0f : __builtin_fabsf(a.scale) * 1.44269504088896340736f;
   const int64_t slot_bytes = a.c.slot * SIZE;
   for (int item = first; item < total; item += gridDim.x) {
-    int s = 0;
-    for (int lo = 0, n = a.w.n_seqs; n > 0;) {   // the first sequence whose end is past the item
-      const int mid = n >> 1;
-      if (s_end[lo + mid] <= item) lo += mid + 1, n -= mid + 1;
-      else n = mid;
-      s = lo;
+    int s = 0, rest, start, tokens, ctx;
+    if (few) {
+      s = __popcll(__ballot(my_items <= item));   // the first whose end is past the item
+      rest = item - (s > 0 ? __builtin_amdgcn_readlane(my_items, s - 1) : 0);
+      start = __builtin_amdgcn_readlane(my_start, s);
+      tokens = __builtin_amdgcn_readlane(my_end, s) - start;
+      ctx = __builtin_amdgcn_readlane(my_ctx, s);
+    } else {
+      for (int n = a.w.n_seqs; n > 0;) {
+        const int mid = n >> 1;
+        if (s_end[s + mid] <= item) s += mid + 1, n -= mid + 1;
+        else n = mid;
+      }
+      s = __builtin_amdgcn_readfirstlane(s);
+      rest = item - __builtin_amdgcn_readfirstlane(s > 0 ? s_end[s - 1] : 0);
+      start = __builtin_amdgcn_readfirstlane(a.w.row_start[s]);
+      tokens = __builtin_amdgcn_readfirstlane(a.w.row_start[s + 1]) - start;
+      ctx = __builtin_amdgcn_readfirstlane(a.w.ctx_len[s]);
     }
-    s = __builtin_amdgcn_readfirstlane(s);
-    int rest = item - __builtin_amdgcn_readfirstlane(s > 0 ? s_end[s - 1] : 0);
-    const int start = __builtin_amdgcn_readfirstlane(a.w.row_start[s]);
-    const int tokens = __builtin_amdgcn_readfirstlane(a.w.row_start[s + 1]) - start;
-    const int ctx = __builtin_amdgcn_readfirstlane(a.w.ctx_len[s]), keys = ctx + tokens, rows = tokens * G;
-    const int tiles = (rows + ROWS - 1) / ROWS, run = run_of(keys, a.wide), runs = runs_of(keys, a.wide);
+    const int keys = ctx + tokens, rows = tokens * G;
+    const int tiles = (rows + ROWS - 1) / ROWS, run = run_of(keys, a.least_run), runs = runs_of(keys, a.least_run);
     const int tile = rest % tiles;
     rest /= tiles;
     const int part = rest % runs, head = rest / runs;   // of the cache
@@ -439,7 +462,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
     int page_of = -1, slot_of = 0;   // lane i: of tile 16 i of the wave's keys from the batch on
     const uint8_t* const k_head = a.c.k + head * a.c.head * SIZE;
     const uint8_t* const v_head = a.c.v + head * a.c.head * SIZE;
-    auto load = [&](KV& kv, int step, bool (&live)[2]) {
+    auto load = [&](KV& kv, int step, bool (&live)[2], bool want_k, bool want_v) {
       const int key = key_of(step);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -451,13 +474,13 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
         const auto kr = __builtin_amdgcn_make_buffer_rsrc((void*)(k_head + off), 0, records, 0x00027000);
         const auto vr = __builtin_amdgcn_make_buffer_rsrc((void*)(v_head + off), 0, records, 0x00027000);
 #pragma unroll
-        for (int u = 0; u < KV::KL; ++u) {
+        for (int u = 0; want_k && u < KV::KL; ++u) {
           const uint32_t byte = u * 64 + quad * 16;
           kv.k[t][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
                                                      kr, byte < (uint32_t)(d * SIZE) ? (uint32_t)(col * slot_bytes) + byte : kNowhere, 0, 0));
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; want_v && i < 4; ++i) {
           const bool in = key + 16 * t + 4 * quad + i < keys;   // a slot past the last key may hold anything
 #pragma unroll
           for (int h = 0; h < NH; ++h) {
@@ -480,8 +503,8 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
           const int64_t so = live[t] ? ((int64_t)page * a.c.n_kv + head) * a.c.page_size + slot : 0;
           const auto ksr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.ks + so), 0, records, 0x00027000);
           const auto vsr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.vs + so), 0, records, 0x00027000);
-          kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ksr, quad * 16, 0, 0));
-          kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(vsr, quad * 16, 0, 0));
+          if (want_k) kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ksr, quad * 16, 0, 0));
+          if (want_v) kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(vsr, quad * 16, 0, 0));
         }
       }
     };
@@ -668,23 +691,23 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
         }
       }
       const int last = min(batch + 32, steps);
-      if constexpr (AHEAD) {
-        KV x, y;
-        bool lx[2], ly[2];
-        load(x, batch, lx);
-        for (int i = batch; i < last; i += 2) {
-          load(y, i + 1 < last ? i + 1 : steps, ly);
+      KV x, y;
+      bool lx[2], ly[2];
+      if constexpr (AHEAD == 0) {
+        for (int i = batch; i < last; ++i) {
+          load(x, i, lx, true, true);
           use(x, i, lx);
-          if (i + 1 >= last) break;
-          load(x, i + 2 < last ? i + 2 : steps, lx);
-          use(y, i + 1, ly);
         }
       } else {
-        for (int i = batch; i < last; ++i) {
-          KV x;
-          bool lx[2];
-          load(x, i, lx);
+        load(x, batch, lx, true, AHEAD == 2);
+        for (int i = batch; i < last; i += 2) {
+          if constexpr (AHEAD == 1) load(x, i, lx, false, true);
+          load(y, i + 1 < last ? i + 1 : steps, ly, true, AHEAD == 2);
           use(x, i, lx);
+          if (i + 1 >= last) break;
+          if constexpr (AHEAD == 1) load(y, i + 1, ly, false, true);
+          load(x, i + 2 < last ? i + 2 : steps, lx, true, AHEAD == 2);
+          use(y, i + 1, ly);
         }
       }
     }
@@ -808,7 +831,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   const int row = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads, tid = threadIdx.x, d = a.c.d;
   const Seq q = seq_of(a.w, row, a.w.max_window);
   if (q.tokens == 0) return;
-  const int runs = runs_of(q.ctx + q.tokens, a.wide);
+  const int runs = runs_of(q.ctx + q.tokens, a.least_run);
   if (runs == 1) return;
   const int64_t idx = (int64_t)blockIdx.x * a.max_runs;
   const int lane = tid & 63;
@@ -944,6 +967,10 @@ struct Eight {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
     else return to_f(__builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e & 1)))));
   }
+  static __device__ __forceinline__ uint32_t none() {   // -infinity, one or two of them
+    const uint32_t v = sizeof(T) == 4 ? 0xFF800000u : (uint32_t)__builtin_bit_cast(uint16_t, from_f<std::conditional_t<sizeof(T) == 4, bf16_t, T>>(-__builtin_inff()));
+    return sizeof(T) == 4 ? v : v | v << 16;
+  }
   // What follows converts anew rather than keep a register for each value.
   __device__ __forceinline__ void forget() {
 #pragma unroll
@@ -964,16 +991,30 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   const int piece = blockIdx.x % a.pieces, from = piece * (256 * EL);
   const T* x = (const T*)a.logits + row * a.ld;
   Eight<T> raw[PIECES];
+  if (from + 256 * EL <= a.n) {
 #pragma unroll
-  for (int p = 0; p < PIECES; ++p) {
-    const int i = from + p * 2048 + tid * 8;
-    if (i + 8 <= a.n) {
-      __builtin_memcpy(raw[p].w, x + i, sizeof raw[p].w);
-    } else {
-      T v[8];
+    for (int p = 0; p < PIECES; ++p) __builtin_memcpy(raw[p].w, x + from + p * 2048 + tid * 8, sizeof raw[p].w);
+  } else {   // the row's end: eight values that it cuts are loaded one by one, and past it all are -infinity
+    const int cut = a.n & ~7;
+    Eight<T> last;
+    T v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = i + e < a.n ? x[i + e] : from_f<T>(-__builtin_inff());
-      __builtin_memcpy(raw[p].w, v, sizeof v);
+    for (int e = 0; e < 8; ++e) v[e] = from_f<T>(-__builtin_inff());
+    if (((cut - from) / 8 & 255) == tid) {
+#pragma unroll
+      for (int e = 0; e < 7; ++e)
+        if (cut + e < a.n) v[e] = x[cut + e];
+    }
+    __builtin_memcpy(last.w, v, sizeof v);
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      const int i = from + p * 2048 + tid * 8;
+      if (i < cut) {
+        __builtin_memcpy(raw[p].w, x + i, sizeof raw[p].w);
+      } else {
+#pragma unroll
+        for (int w = 0; w < Eight<T>::W; ++w) raw[p].w[w] = i == cut ? last.w[w] : Eight<T>::none();
+      }
     }
   }
   if (tid == 0) s_count = 0;
@@ -1085,8 +1126,7 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
       __syncthreads();
       if (tid == 0) best[i] = last;
     }
-  }
-}
+  }}
 
 // A wave a row.
 template <typename T>
@@ -1277,11 +1317,16 @@ WindowArgs window_args(const moe_window& w, const moe_kv_cache& c) {
                     w.max_pages * c.page_size};
 }
 
-// Windows of more than 32 rows a cache head take longer runs: their runs' results weigh more, and their tiles fill the card.
-int wide_rule(const moe_kv_cache& c, const moe_window& w, int n_heads) { return w.max_window * (n_heads / c.n_kv) > 32; }
+// Rows that share a cache head, at most.
+int most_rows(const moe_kv_cache& c, const moe_window& w, int n_heads) { return w.max_window * (n_heads / c.n_kv); }
+// The least keys of a run, by how many sequences, cache heads and tiles of rows there are to spread over the card.
+int least_run(const moe_kv_cache& c, const moe_window& w, int n_heads) {
+  const int64_t units = (int64_t)w.n_seqs * c.n_kv * ((most_rows(c, w, n_heads) + 127) / 128);
+  return units <= 32 ? 256 : units <= 128 ? 512 : 1024;
+}
 int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
-  const int wide = wide_rule(c, w, n_heads), least = wide ? 1024 : 256;   // keys of a run
-  return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, wide ? 32 : kMaxRuns);
+  const int least = least_run(c, w, n_heads);
+  return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, kMaxRuns);
 }
 
 template <typename T, bool I8, int HD, int NT, bool WIDE>
@@ -1291,7 +1336,7 @@ int launch_attend(hipStream_t st, const AttendArgs& a) {
   const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;
   if (items > 0x7FFFFFFF) return MOE_E_SHAPE;
   const int grid = (int)std::min<int64_t>(512, (items + 7) & ~7ll);
-  hipLaunchKernelGGL((k_attend<T, I8, HD, NT, WIDE, NT == 1 && HD < 256>), dim3(grid), dim3(256), 4 * a.w.n_seqs, st, a);
+  hipLaunchKernelGGL((k_attend<T, I8, HD, NT, WIDE, HD == 256 ? 0 : NT == 1 ? 2 : 1>), dim3(grid), dim3(256), 4 * a.w.n_seqs, st, a);
   if (const int rc = launched("moe_window_attention")) return rc;
   if (a.max_runs > 1) {
     hipLaunchKernelGGL(k_attend_join<T>, dim3((unsigned)(a.w.n_tokens * a.n_heads)), dim3(256), 0, st, a);
@@ -1307,7 +1352,7 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
     constexpr bool I8 = decltype(i)::value;
     constexpr int HD = decltype(hd)::value;
     constexpr int MOST = HD == 256 ? 1 : 2;   // tiles of 16 rows that a wave has registers for
-    if (a.wide) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, MOST, true>(st, a);
+    if (rows > 32) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, MOST, true>(st, a);
     return rows <= 16 ? launch_attend<T, I8, HD, 1, false>(st, a) : launch_attend<T, I8, HD, MOST, false>(st, a);
   };
   auto width = [&](auto i) {
@@ -1319,8 +1364,8 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
-constexpr int kShortRow = 65536;
-int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 16383) / 16384; }
+constexpr int kShortRow = 65536, kLongEl = 64;
+int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 256 * kLongEl - 1) / (256 * kLongEl); }
 
 }  // namespace moe
 
@@ -1417,7 +1462,7 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
   }
   const int runs = max_runs(*C, *W, n_heads);
   AttendArgs a{cache_args(*C), window_args(*W, *C), q, out, lse, (float*)workspace, nullptr, ldq, ldo, n_heads, runs,
-               wide_rule(*C, *W, n_heads), scale};
+               least_run(*C, *W, n_heads), scale};
   a.part_ml = a.part + (int64_t)n * n_heads * runs * C->head_dim;
   return dtype == MOE_BF16 ? run_attend<bf16_t>((hipStream_t)stream, a, C->dtype == MOE_I8)
                            : run_attend<f16_t>((hipStream_t)stream, a, C->dtype == MOE_I8);
@@ -1461,7 +1506,7 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
   with_type(dtype, [&](auto t) {
     using T = decltype(t);
     if (n <= kShortRow) hipLaunchKernelGGL((k_scores<T, 32>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
-    else hipLaunchKernelGGL((k_scores<T, 64>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    else hipLaunchKernelGGL((k_scores<T, kLongEl>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
     hipLaunchKernelGGL(k_scores_join<T>, dim3(rows), dim3(64), 0, (hipStream_t)stream, a);
   });
   return launched("moe_token_logprobs");
