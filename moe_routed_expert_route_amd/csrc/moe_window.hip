@@ -282,6 +282,14 @@ __host__ __device__ __forceinline__ int runs_of(int keys, int least) {
 }
 constexpr int kMaxRuns = 64;   // runs_of of any count
 
+// s_waitcnt vmcnt(n), the other counters left alone (n < 64; vmcnt in bits 3:0 and 15:14)
+#define MOE_VM(n) (((n) & 15) | (((n) >> 4) << 14) | (7 << 4) | (15 << 8))
+// Every LDS access of the wave has finished, then the workgroup meets; loads stay on their way.
+__device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
+
+#define PVB(e) (((e) & 1) == 1)
+#define QKB __builtin_amdgcn_sched_barrier(0)
+#define SMB __builtin_amdgcn_sched_barrier(0)
 template <typename T>
 struct Mat;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -297,6 +305,7 @@ struct Mat<bf16_t> {
     typedef __bf16 v2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, v2{(__bf16)a, (__bf16)b});
   }
+  static constexpr uint32_t kOne = 0x3F80u;
   static __device__ __forceinline__ uint32_t odd(uint32_t x) {   // of two values, bit 0 / bit 16: not finite
     return ((x & 0x00007F80u) == 0x00007F80u ? 1u : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0x10000u : 0u);
   }
@@ -311,6 +320,7 @@ struct Mat<f16_t> {
     typedef _Float16 v2 __attribute__((ext_vector_type(2)));
     return __builtin_bit_cast(uint32_t, v2{(_Float16)a, (_Float16)b});
   }
+  static constexpr uint32_t kOne = 0x3C00u;
   static __device__ __forceinline__ uint32_t odd(uint32_t x) {
     return ((x & 0x00007C00u) == 0x00007C00u ? 1u : 0u) | ((x & 0x7C000000u) == 0x7C000000u ? 0x10000u : 0u);
   }
@@ -342,18 +352,24 @@ struct Keys {
 
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset past any buffer: the load gives 0 and touches nothing
 
-// HD: 64, 128 or 256, the least that holds head_dim. NT: a wave's tiles of 16 rows. WIDE: the waves share the keys and
-// have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. AHEAD: the next keys
-// (1), and their values too (2), are loaded before these are used (0: there are no registers for that).
-template <typename T, bool I8, int HD, int NT, bool WIDE, int AHEAD>
-__global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
+// HD: 64, 128 or 256, the least that holds head_dim. NT: a wave's tiles of 16 rows. WIDE: the waves share the keys, which
+// then go through LDS (a ring of stages of 32 keys, loaded straight into it), and have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. The next
+// keys are loaded as soon as these are multiplied, the next values as soon as these are.
+constexpr int ring_bytes(int hd, bool i8) { return 64 * hd * (i8 ? 1 : 2) * (hd * (i8 ? 1 : 2) > 256 ? 2 : 3); }   // three stages, or two large ones
+constexpr int kAttendWaves(int hd, int nt) { return 2; }   // of a SIMD
+template <typename T, bool I8, int HD, int NT, bool WIDE>
+__global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs a) {
   using M = Mat<T>;
   using KV = Keys<I8, HD>;
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1), KS = HD / 32, E0 = HD < 128 ? 4 : 8, NH = HD < 128 ? 1 : HD / 128, DT = E0 * NH;
   constexpr int SIZE = I8 ? 1 : 2, STRIDE = HD + 4;
-  __shared__ float s_m[4][WIDE ? 1 : ROWS], s_l[4][WIDE ? 1 : ROWS], s_o[4][WIDE ? 1 : 16 * STRIDE], s_p[I8 ? 1 : 4][I8 ? 1 : 32 * 16];
+  __shared__ float s_m[4][WIDE ? 1 : ROWS], s_l[4][WIDE ? 1 : ROWS], s_o[4][WIDE ? 1 : 16 * STRIDE];
   __shared__ int s_wave[4];
-  extern __shared__ int s_end[];   // [n_seqs]: items of the sequences up to this one
+  // the ring: rows of 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that neighbouring lanes meet other banks
+  constexpr int CR = HD * SIZE / 16, HALF = 32 * HD * SIZE, STAGE = 2 * HALF, STAGES = ring_bytes(HD, I8) / STAGE;
+  constexpr int RPI = 64 / CR, NI = 32 / RPI, PER = NI / 2;   // rows a load instruction has, loads of K, loads a wave makes
+  extern __shared__ __align__(16) uint8_t s_ring[];            // static, the compiler would have reads wait for the loads on their way
+  int* const s_end = (int*)(s_ring + (WIDE ? STAGES * STAGE : 0));   // [n_seqs]: items of the sequences up to this one
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quad = lane >> 4;
   const int G = a.n_heads / a.c.n_kv, d = a.c.d;
   auto items_of = [&](int i, int start, int end, int ctx) {
@@ -394,6 +410,13 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
       __syncthreads();
     }
     total = __builtin_amdgcn_readfirstlane(total);
+  }
+  auto swizzle = [](int r) { return CR == 4 ? r >> 1 & 3 : r & (CR < 16 ? CR - 1 : 15); };
+  if constexpr (WIDE) {
+    if (d < HD) {   // places that no load reaches
+      for (int i = tid; i < STAGES * STAGE / 16; i += 256) ((u32x4*)s_ring)[i] = u32x4{0, 0, 0, 0};
+      __syncthreads();
+    }
   }
   // neighbouring items, the tiles of one run among them, on one die
   const int first = (blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
@@ -459,57 +482,135 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
       for (int x = 0; x < DT; ++x) acc[t][x] = f32x4{0, 0, 0, 0};
     }
 
-    int page_of = -1, slot_of = 0;   // lane i: of tile 16 i of the wave's keys from the batch on
-    const uint8_t* const k_head = a.c.k + head * a.c.head * SIZE;
-    const uint8_t* const v_head = a.c.v + head * a.c.head * SIZE;
-    auto load = [&](KV& kv, int step, bool (&live)[2], bool want_k, bool want_v) {
-      const int key = key_of(step);
+    // Lane i: where tile i of 16 keys (of the wave's from the batch on) is, in bytes from the head's first page, and its scales;
+    // `there`: the tiles that are.
+    uint32_t at_lo = 0, at_hi = 0, sc_lo = 0, sc_hi = 0;
+    uint64_t there = 0;
+    auto pages = [&](int batch) {
+      const int key = key_of(batch + (lane >> 1)) + 16 * (lane & 1);
+      int page = -1, slot = 0;
+      if (key < key0 + len) {
+        page = a.w.pages[s * a.w.ld_pages + key / a.c.page_size];
+        slot = key % a.c.page_size;
+        if (page < 0 || page >= a.c.n_pages) {
+          atomicOr(a.w.err, MOE_ERR_PAGE);
+          page = -1;
+        }
+      }
+      there = __ballot(page >= 0);
+      const int64_t at = page >= 0 ? (page * a.c.page + slot * a.c.slot) * SIZE : 0;
+      at_lo = (uint32_t)at, at_hi = (uint32_t)(at >> 32);
+      if constexpr (I8) {
+        const int64_t sc = page >= 0 ? (((int64_t)page * a.c.n_kv + head) * a.c.page_size + slot) * 4 : 0;
+        sc_lo = (uint32_t)sc, sc_hi = (uint32_t)(sc >> 32);
+      }
+    };
+    const uint64_t k_head = (uint64_t)(a.c.k + head * a.c.head * SIZE), v_head = (uint64_t)(a.c.v + head * a.c.head * SIZE);
+    auto lane64 = [](uint32_t lo, uint32_t hi, int i) {
+      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, i) | (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
+    };
+    auto buffer = [](uint64_t at, bool live) { return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, live ? 0x7FFFFFFF : 0, 0x00027000); };
+    auto scales = [&](KV& kv, int step, bool k, bool v) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int at = 2 * (step & 31) + t;
-        const int page = __builtin_amdgcn_readlane(page_of, at), slot = __builtin_amdgcn_readlane(slot_of, at);
-        live[t] = step < steps && page >= 0;
-        const int64_t off = live[t] ? (page * a.c.page + slot * a.c.slot) * SIZE : 0;
-        const int records = live[t] ? 0x7FFFFFFF : 0;
-        const auto kr = __builtin_amdgcn_make_buffer_rsrc((void*)(k_head + off), 0, records, 0x00027000);
-        const auto vr = __builtin_amdgcn_make_buffer_rsrc((void*)(v_head + off), 0, records, 0x00027000);
-#pragma unroll
-        for (int u = 0; want_k && u < KV::KL; ++u) {
-          const uint32_t byte = u * 64 + quad * 16;
-          kv.k[t][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                                     kr, byte < (uint32_t)(d * SIZE) ? (uint32_t)(col * slot_bytes) + byte : kNowhere, 0, 0));
-        }
-#pragma unroll
-        for (int i = 0; want_v && i < 4; ++i) {
-          const bool in = key + 16 * t + 4 * quad + i < keys;   // a slot past the last key may hold anything
-#pragma unroll
-          for (int h = 0; h < NH; ++h) {
-            const int e = h * 128 + col * E0;
-            const uint32_t o = in && e < d ? (uint32_t)((4 * quad + i) * slot_bytes) + (uint32_t)(e * SIZE) : kNowhere;
-            constexpr int W = E0 * SIZE / 4;
-            uint32_t* to = &kv.v[4 * t + i][h * W];
-            if constexpr (W == 4) {
-              const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, o, 0, 0));
-              to[0] = x[0], to[1] = x[1], to[2] = x[2], to[3] = x[3];
-            } else if constexpr (W == 2) {
-              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, o, 0, 0));
-              to[0] = x[0], to[1] = x[1];
-            } else {
-              to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, o, 0, 0);
-            }
-          }
-        }
-        if constexpr (I8) {
-          const int64_t so = live[t] ? ((int64_t)page * a.c.n_kv + head) * a.c.page_size + slot : 0;
-          const auto ksr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.ks + so), 0, records, 0x00027000);
-          const auto vsr = __builtin_amdgcn_make_buffer_rsrc((void*)(a.c.vs + so), 0, records, 0x00027000);
-          if (want_k) kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(ksr, quad * 16, 0, 0));
-          if (want_v) kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(vsr, quad * 16, 0, 0));
-        }
+        const int i = 2 * (step & 31) + t;
+        const bool live = step < steps && (there >> i & 1);
+        const uint64_t at = lane64(sc_lo, sc_hi, i);
+        if (k) kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer((uint64_t)a.c.ks + at, live), quad * 16, 0, 0));
+        if (v) kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer((uint64_t)a.c.vs + at, live), quad * 16, 0, 0));
       }
     };
 
-    auto use = [&](KV& kv, int step, const bool (&live)[2]) {
+    // Keys straight into registers. Lane offsets; of what is past head_dim, nowhere.
+    uint32_t k_off[KV::KL], v_off[NH];
+#pragma unroll
+    for (int u = 0; u < KV::KL; ++u) {
+      const uint32_t byte = u * 64 + quad * 16;
+      k_off[u] = byte < (uint32_t)(d * SIZE) ? (uint32_t)(col * slot_bytes) + byte : kNowhere;
+    }
+#pragma unroll
+    for (int h = 0; h < NH; ++h) {
+      const int e = h * 128 + col * E0;
+      v_off[h] = e < d ? (uint32_t)(4 * quad * slot_bytes) + (uint32_t)(e * SIZE) : kNowhere;
+    }
+    auto load = [&](KV& kv, int step, bool want_k, bool want_v) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int at = 2 * (step & 31) + t;
+        const bool live = step < steps && (there >> at & 1);
+        const uint64_t off = lane64(at_lo, at_hi, at);
+        const auto kr = buffer(k_head + off, live), vr = buffer(v_head + off, live);
+#pragma unroll
+        for (int u = 0; want_k && u < KV::KL; ++u)
+          kv.k[t][u] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(kr, k_off[u], 0, 0));
+#pragma unroll
+        for (int i = 0; want_v && i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            constexpr int W = E0 * SIZE / 4;
+            uint32_t* to = &kv.v[4 * t + i][h * W];
+            if constexpr (W == 4) {
+              const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[h], (int)(i * slot_bytes), 0));
+              to[0] = x[0], to[1] = x[1], to[2] = x[2], to[3] = x[3];
+            } else if constexpr (W == 2) {
+              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[h], (int)(i * slot_bytes), 0));
+              to[0] = x[0], to[1] = x[1];
+            } else {
+              to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, v_off[h], (int)(i * slot_bytes), 0);
+            }
+          }
+      }
+      if constexpr (I8) scales(kv, step, want_k, want_v);
+    };
+
+    // Through LDS: a wave's share of a step's rows on the way to the ring, and a step's values from there.
+    uint32_t s_off[WIDE ? PER : 1];
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int r = (wave + 4 * x) % NI * RPI + lane / CR, byte = ((lane % CR) ^ swizzle(r)) * 16;
+        s_off[x] = byte < d * SIZE ? (uint32_t)((r & 15) * slot_bytes) + byte : kNowhere;
+      }
+    }
+    uint64_t lives = 0;   // of the tiles sent: bit 2 (step % 32) + t
+    auto send = [&](int step, int slot) {
+      const int at = 2 * (step & 31);
+      lives = (lives & ~(3ull << at)) | (there & 3ull << at);
+      uint8_t* const stage = s_ring + slot * STAGE;
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        const int j = wave + 4 * x, of_v = j >= NI, row0 = (of_v ? j - NI : j) * RPI, i = at + (row0 >> 4);
+        const auto from = __builtin_amdgcn_make_buffer_rsrc((void*)((of_v ? v_head : k_head) + lane64(at_lo, at_hi, i)), 0,
+                                                            there >> i & 1 ? 0x7FFFFFFF : 0, 0x00027000);
+        if (s_off[x] != kNowhere)
+          __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (MOE_LDS void*)(stage + of_v * HALF + row0 * (HD * SIZE)), 16, (int)s_off[x], 0, 0, 0);
+      }
+    };
+    auto read = [&](KV& kv, int slot) {
+      int col = lane & 15, quad = lane >> 4;   // offsets made anew each time: kept, they cost registers that the loop has not
+      asm volatile("" : "+v"(col), "+v"(quad));
+      const uint8_t* const stage = s_ring + slot * STAGE;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int u = 0; u < KV::KL; ++u)
+          kv.k[t][u] = *(const u32x4*)(stage + (16 * t + col) * (HD * SIZE) + ((u * 4 + quad) ^ swizzle(col)) * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int h = 0; h < NH; ++h) {
+            const int byte = (h * 128 + col * E0) * SIZE, r = 4 * quad + i;
+            constexpr int W = E0 * SIZE / 4;
+            using Words = std::conditional_t<W == 4, u32x4, std::conditional_t<W == 2, u32x2, uint32_t>>;
+            const Words x = *(const Words*)(stage + HALF + (16 * t + r) * (HD * SIZE) + ((byte >> 4) ^ swizzle(r)) * 16 + (byte & 15));
+            __builtin_memcpy(&kv.v[4 * t + i][h * W], &x, 4 * W);
+          }
+      }
+    };
+
+    bool odd = false;   // whether a value of a window's key is not finite
+    // One step; `next` is called when the keys (true) and then the values (false) are used up.
+    auto use = [&](KV& kv, int step, const bool (&live)[2], auto next) {
       const int key = key_of(step);
       const bool check = key + 32 > ctx || !live[0] || !live[1];
       f32x4 p[2][NT];
@@ -539,12 +640,18 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
             for (int i = 0; i < 4; ++i) p[t][n][i] *= kv.ks[t][i];
         }
       }
+      QKB;
+      next(true);
       if (check) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int rel = key + 16 * t + 4 * quad + i - ctx;
+            if (rel >= tokens || !live[t]) {   // a slot past the last key may hold anything
+#pragma unroll
+              for (int y = 0; y < KV::VD; ++y) kv.v[4 * t + i][y] = 0;
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
               const bool sees = live[t] && (rel < 0 || (rel < 64 && (seen[n] >> (rel & 63) & 1)));
@@ -553,6 +660,20 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
             if constexpr (I8)
               if (rel >= tokens) kv.vs[t][i] = 0.0f;
           }
+        // A value of a drafted token that is not finite must not reach rows that do not see it (0 times it is NaN): it
+        // counts as 0 here, and add_odd adds it to the rows that do.
+        if constexpr (!I8) {
+          uint32_t any = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x)
+#pragma unroll
+            for (int y = 0; y < KV::VD; ++y) {
+              const uint32_t o = key + 16 * (x >> 2) + 4 * quad + (x & 3) >= ctx ? M::odd(kv.v[x][y]) : 0;
+              any |= o;
+              kv.v[x][y] &= ~(o * 0xFFFFu);
+            }
+          odd |= __ballot(any != 0) != 0;
+        }
       }
       float top[NT];
       bool grows = false;
@@ -612,23 +733,6 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
         }
         l[n] += sum;
       }
-      // A value of a drafted token that is not finite must not reach rows that do not see it (0 times it is NaN): it
-      // is taken out here and added to the others below.
-      bool odd = false;
-      if constexpr (!I8) {
-        if (key + 32 > ctx) {
-          uint32_t any = 0;
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-#pragma unroll
-            for (int y = 0; y < KV::VD; ++y) {
-              const uint32_t o = M::odd(kv.v[x][y]);
-              any |= o;
-              kv.v[x][y] &= ~(o * 0xFFFFu);
-            }
-          odd = __ballot(any != 0) != 0;
-        }
-      }
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -647,70 +751,75 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[n][h * E0 + e8] = M::mma(f, w[n], acc[n][h * E0 + e8]);
+          if (PVB(e8)) __builtin_amdgcn_sched_barrier(0);
         }
+      next(false);
+    };
+    auto add_odd = [&]() {
       if constexpr (!I8) {
-        if (odd) {
+        for (int step = 0; step < steps; ++step)
+          for (int k = 0; k < 32; ++k) {
+            const int key = key_of(step) + k;
+            if (key < ctx || key >= keys) continue;
+            const int page = a.w.pages[s * a.w.ld_pages + key / a.c.page_size];
+            if (page < 0 || page >= a.c.n_pages) continue;
+            const T* v = (const T*)v_head + page * a.c.page + key % a.c.page_size * a.c.slot;
 #pragma unroll
-          for (int n = 0; n < NT; ++n) {
+            for (int x = 0; x < DT; ++x)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
+              for (int i = 0; i < 4; ++i) {
+                const int e = x / E0 * 128 + (4 * quad + i) * E0 + x % E0;
+                const float f = to_f(v[e < d ? e : 0]);
+                const bool counts = (e < d) & !(__builtin_fabsf(f) < __builtin_inff());
 #pragma unroll
-              for (int i = 0; i < 4; ++i) s_p[wave][(16 * t + 4 * quad + i) * 16 + col] = p[t][n][i];
-            __builtin_amdgcn_wave_barrier();
-#pragma unroll 1
-            for (int k = 0; k < 32 && key + k < keys; ++k) {
-              const int at = 2 * (step & 31) + (k >> 4);
-              const int page = __builtin_amdgcn_readlane(page_of, at), slot = __builtin_amdgcn_readlane(slot_of, at);
-              if (page < 0) continue;
-              const float pk = s_p[wave][k * 16 + col];
-              const T* v = (const T*)v_head + page * a.c.page + (slot + (k & 15)) * a.c.slot;
-#pragma unroll
-              for (int x = 0; x < DT; ++x)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int at_d = x / E0 * 128 + (4 * quad + i) * E0 + x % E0;
-                  const float f = at_d < d ? to_f(v[at_d]) : 0.0f;
-                  if (!(__builtin_fabsf(f) < __builtin_inff()) && pk != 0.0f) acc[n][x][i] += pk * f;
-                }
-            }
-            __builtin_amdgcn_wave_barrier();
+                for (int n = 0; n < NT; ++n) acc[n][x][i] += counts & (bool)(seen[n] >> (key - ctx) & 1) ? f : 0.0f;
+              }
           }
-        }
       }
     };
 
-    for (int batch = 0; batch < steps; batch += 32) {
-      {
-        const int key = key_of(batch + (lane >> 1)) + 16 * (lane & 1);
-        page_of = -1;
-        if (key < key0 + len) {
-          const int page = a.w.pages[s * a.w.ld_pages + key / a.c.page_size];
-          slot_of = key % a.c.page_size;
-          if (page >= 0 && page < a.c.n_pages) page_of = page;
-          else atomicOr(a.w.err, MOE_ERR_PAGE);
+    if constexpr (WIDE) {
+      KV x, ahead;
+      bool live[2];
+      pages(0);
+#pragma unroll
+      for (int i = 0; i < STAGES - 1; ++i)
+        if (i < steps) send(i, i);
+      if constexpr (I8) scales(ahead, 0, true, true);
+      for (int i = 0, slot = 0; i < steps; ++i, slot = slot + 1 == STAGES ? 0 : slot + 1) {
+        // this step has landed: all but the loads of the steps behind it
+        if (i + STAGES - 2 < steps) __builtin_amdgcn_s_waitcnt(MOE_VM(PER * (STAGES - 2)));
+        else __builtin_amdgcn_s_waitcnt(MOE_VM(0));
+        meet();   // all waves', and the stage before it is free
+        const int next = i + STAGES - 1;
+        if constexpr (I8) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) x.ks[t] = ahead.ks[t], x.vs[t] = ahead.vs[t];
+          if (STAGES > 2 && i + 1 < steps) scales(ahead, i + 1, true, true);   // while its pages are there
         }
-      }
-      const int last = min(batch + 32, steps);
-      KV x, y;
-      bool lx[2], ly[2];
-      if constexpr (AHEAD == 0) {
-        for (int i = batch; i < last; ++i) {
-          load(x, i, lx, true, true);
-          use(x, i, lx);
+        live[0] = lives >> (2 * (i & 31)) & 1, live[1] = lives >> (2 * (i & 31) + 1) & 1;
+        if (next < steps) {
+          if ((next & 31) == 0) pages(next);
+          send(next, slot == 0 ? STAGES - 1 : slot - 1);
+          if constexpr (I8 && STAGES == 2) scales(ahead, next, true, true);
         }
-      } else {
-        load(x, batch, lx, true, AHEAD == 2);
-        for (int i = batch; i < last; i += 2) {
-          if constexpr (AHEAD == 1) load(x, i, lx, false, true);
-          load(y, i + 1 < last ? i + 1 : steps, ly, true, AHEAD == 2);
-          use(x, i, lx);
-          if (i + 1 >= last) break;
-          if constexpr (AHEAD == 1) load(y, i + 1, ly, false, true);
-          load(x, i + 2 < last ? i + 2 : steps, lx, true, AHEAD == 2);
-          use(y, i + 1, ly);
-        }
+        read(x, slot);
+        use(x, i, live, [](bool) {});
       }
     }
+    for (int batch = 0; !WIDE && batch < steps; batch += 32) {
+      pages(batch);
+      const int last = min(batch + 32, steps);
+      KV x;
+      load(x, batch, true, false);
+      __builtin_amdgcn_sched_barrier(0);   // in this order, so that the loop waits for the keys alone
+      load(x, batch, false, true);
+      for (int i = batch; i < last; ++i) {
+        const bool live[2] = {(bool)(there >> (2 * (i & 31)) & 1), (bool)(there >> (2 * (i & 31) + 1) & 1)};
+        use(x, i, live, [&](bool keys_done) { load(x, i + 1 < last ? i + 1 : steps, keys_done, !keys_done); });
+      }
+    }
+    if (odd) add_odd();
 
     if constexpr (WIDE) {   // a lane has neighbouring values of its rows
 #pragma unroll
@@ -748,6 +857,7 @@ __global__ __launch_bounds__(256, 2) void k_attend(AttendArgs a) {
           a.part_ml[2 * idx + 1] = sum;
         }
       }
+      meet();
       continue;
     }
     if constexpr (!WIDE) {
@@ -1335,8 +1445,14 @@ int launch_attend(hipStream_t st, const AttendArgs& a) {
   const int64_t tiles = ((int64_t)a.w.max_window * (a.n_heads / a.c.n_kv) + ROWS - 1) / ROWS;
   const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;
   if (items > 0x7FFFFFFF) return MOE_E_SHAPE;
-  const int grid = (int)std::min<int64_t>(512, (items + 7) & ~7ll);
-  hipLaunchKernelGGL((k_attend<T, I8, HD, NT, WIDE, HD == 256 ? 0 : NT == 1 ? 2 : 1>), dim3(grid), dim3(256), 4 * a.w.n_seqs, st, a);
+  const int grid = (int)std::min<int64_t>(256 * kAttendWaves(HD, NT), (items + 7) & ~7ll);
+  const int lds = (WIDE ? ring_bytes(HD, I8) : 0) + 4 * a.w.n_seqs;
+  const auto kern = k_attend<T, I8, HD, NT, WIDE>;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute((const void*)kern, hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return hip_fail(e, "moe_window_attention");
+  }
+  hipLaunchKernelGGL(kern, dim3(grid), dim3(256), lds, st, a);
   if (const int rc = launched("moe_window_attention")) return rc;
   if (a.max_runs > 1) {
     hipLaunchKernelGGL(k_attend_join<T>, dim3((unsigned)(a.w.n_tokens * a.n_heads)), dim3(256), 0, st, a);
