@@ -143,12 +143,52 @@ __device__ __forceinline__ void load4(const void* p, int dtype, int at, int n, f
 }
 
 // A head's row is with LG neighbouring lanes, eight values each: four pairs (of MOE_ROPE_HALF: four values and their
-// four partners), or eight values that do not turn.
+// four partners), or eight values that do not turn. A workgroup takes `units` heads of a token, the next head's values on
+// their way while it works on one. The first are asked for before the token's sequence is known. Everything is in 64 bits
+// (full rate here), which a dozen instructions a value leave hidden behind the bytes.
 template <typename T, int LG>
 __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
   constexpr int GROUPS = 256 / LG;
   __shared__ double s_turn[128][2];
-  const int row = blockIdx.x, l = threadIdx.x % LG, d = a.c.d;
+  const int row = blockIdx.x, l = threadIdx.x % LG, d = a.c.d, half = a.n_rot / 2;
+  const int last = min((int)(blockIdx.y + 1) * a.units, a.n_heads + 2 * a.c.n_kv);
+  struct Part {   // this lane's values of a head: n0 from at0 on, n1 from at1 on
+    int at0, at1, n0, n1;
+    bool turns, halves;
+  };
+  auto part_of = [&](bool is_v) {
+    const int rot = is_v ? 0 : a.n_rot, turning = (rot + 7) / 8;
+    Part p;
+    p.turns = l < turning, p.halves = p.turns && a.layout == MOE_ROPE_HALF;
+    p.at0 = p.halves ? 4 * l : p.turns ? 8 * l : rot + 8 * (l - turning);
+    p.at1 = p.halves ? half + 4 * l : p.at0 + 4;
+    const int end = p.turns ? rot : d;
+    p.n0 = (p.halves ? half : end) - p.at0, p.n1 = end - p.at1;
+    return p;
+  };
+  const Part turning = part_of(false), plain = part_of(true);
+  T raw[2][4];
+  auto load = [&](int u) {
+    if (u >= last) return;
+    const bool is_q = u < a.n_heads, is_v = u >= a.n_heads + a.c.n_kv;
+    const int h = is_q ? u : is_v ? u - a.n_heads - a.c.n_kv : u - a.n_heads;
+    const T* x = is_q ? (const T*)a.q + row * a.ldq : is_v ? (const T*)a.v + row * a.ldv : (const T*)a.k + row * a.ldk;
+    const Part p = is_v ? plain : turning;
+    load4(x + (int64_t)h * d + p.at0, p.n0, raw[0]);
+    load4(x + (int64_t)h * d + p.at1, p.n1, raw[1]);
+  };
+  int u = blockIdx.y * a.units + (int)threadIdx.x / LG;
+  load(u);
+  // the weights of this lane's values
+  float qw[8], kw[8];
+  if (a.q_weight) {
+    load4(a.q_weight, a.w_dtype, turning.at0, turning.n0, qw);
+    load4(a.q_weight, a.w_dtype, turning.at1, turning.n1, qw + 4);
+  }
+  if (a.k_weight) {
+    load4(a.k_weight, a.w_dtype, turning.at0, turning.n0, kw);
+    load4(a.k_weight, a.w_dtype, turning.at1, turning.n1, kw + 4);
+  }
   if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a.w, 0x7FFFFFFF, 256);
   const Seq q = seq_of(a.w, row, 0x7FFFFFFF);
   if (q.tokens == 0) return;
@@ -156,7 +196,6 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
   const int page = a.w.pages[q.s * a.w.ld_pages + key / a.c.page_size];
   const bool page_ok = page >= 0 && page < a.c.n_pages;
   if (!page_ok && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.w.err, MOE_ERR_PAGE);
-  const int half = a.n_rot / 2;
   if ((int)threadIdx.x < half) {
     double c, s;
     turn64((double)(a.w.pos ? a.w.pos[row] : key) * (double)a.freq[threadIdx.x], c, s);
@@ -164,48 +203,45 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     s_turn[threadIdx.x][1] = (double)a.amp * s;
   }
   __syncthreads();
-  const int first = blockIdx.y * a.units, last = min(first + a.units, a.n_heads + 2 * a.c.n_kv);
-  for (int u = first + (int)threadIdx.x / LG; u < last; u += GROUPS) {
+  double turn_c[4], turn_s[4];   // of this lane's pairs; past the last (1, 0)
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const bool in = 4 * l + e < half;
+    turn_c[e] = in ? s_turn[4 * l + e][0] : 1.0;
+    turn_s[e] = in ? s_turn[4 * l + e][1] : 0.0;
+  }
+  for (; u < last; u += GROUPS) {
     const bool is_q = u < a.n_heads, is_v = u >= a.n_heads + a.c.n_kv;
-    const int h = is_q ? u : (u - a.n_heads) % a.c.n_kv;
-    const T* x = is_q ? (const T*)a.q + row * a.ldq : is_v ? (const T*)a.v + row * a.ldv : (const T*)a.k + row * a.ldk;
-    x += (int64_t)h * d;
-    // this lane's values: n0 from at0 on, n1 from at1 on
-    const int rot = is_v ? 0 : a.n_rot, turning = (rot + 7) / 8;
-    const bool turns = l < turning, halves = turns && a.layout == MOE_ROPE_HALF;
-    const int at0 = halves ? 4 * l : turns ? 8 * l : rot + 8 * (l - turning);
-    const int at1 = halves ? half + 4 * l : at0 + 4, end = turns ? rot : d;
-    const int n0 = (halves ? half : end) - at0, n1 = end - at1;
-    T raw[2][4];
-    load4(x + at0, n0, raw[0]);
-    load4(x + at1, n1, raw[1]);
+    const int h = is_q ? u : is_v ? u - a.n_heads - a.c.n_kv : u - a.n_heads;
+    const Part p = is_v ? plain : turning;
     double y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (double)to_f(raw[e / 4][e % 4]);
-    const void* weight = is_q ? a.q_weight : is_v ? nullptr : a.k_weight;
-    if (weight) {
+    load(u + GROUPS);
+    if (is_q ? a.q_weight != nullptr : !is_v && a.k_weight) {
       double sum = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = __builtin_fma(y[e], y[e], sum);
 #pragma unroll
       for (int o = LG / 2; o; o /= 2) sum += __shfl_xor(sum, o);
       const double rinv = 1.0 / __builtin_sqrt(sum / d + (double)a.eps);
-      float w[8];
-      load4(weight, a.w_dtype, at0, n0, w);
-      load4(weight, a.w_dtype, at1, n1, w + 4);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = y[e] * rinv * (double)w[e];
+      for (int e = 0; e < 8; ++e) y[e] = y[e] * rinv * (double)(is_q ? qw[e] : kw[e]);
     }
-    if (turns) {
+    if (p.turns) {
+      double z[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        if (4 * l + e >= half) break;
-        const double c = s_turn[4 * l + e][0], s = s_turn[4 * l + e][1];
-        double &u0 = halves ? y[e] : y[2 * e], &u1 = halves ? y[4 + e] : y[2 * e + 1];
-        const double p = u0, r = u1;
-        u0 = __builtin_fma(p, c, -(r * s));
-        u1 = __builtin_fma(r, c, p * s);
+        const double c = turn_c[e], s = turn_s[e];
+        const double p0 = p.halves ? y[e] : y[2 * e], p1 = p.halves ? y[4 + e] : y[2 * e + 1];
+        const double r0 = __builtin_fma(p0, c, -(p1 * s)), r1 = __builtin_fma(p1, c, p0 * s);
+        // by selects: an index that differs from lane to lane would put y into memory
+        y[e] = p.halves ? r0 : y[e];
+        y[4 + e] = p.halves ? r1 : y[4 + e];
+        z[2 * e] = r0, z[2 * e + 1] = r1;
       }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = p.halves ? y[e] : z[e];
     }
     float f[8];
 #pragma unroll
@@ -213,8 +249,8 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     if (is_q) {
       on_type(a.o_dtype, [&](auto t) {
         auto* o = (decltype(t)*)a.q_out + row * a.ldo + (int64_t)h * d;
-        store4(o + at0, n0, f);
-        store4(o + at1, n1, f + 4);
+        store4(o + p.at0, p.n0, f);
+        store4(o + p.at1, p.n1, f + 4);
       });
       continue;
     }
@@ -224,15 +260,15 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
       if (!page_ok) continue;
       auto put = [&](auto t) {
         auto* o = (decltype(t)*)pool + at;
-        store4(o + at0, n0, f);
-        store4(o + at1, n1, f + 4);
+        store4(o + p.at0, p.n0, f);
+        store4(o + p.at1, p.n1, f + 4);
       };
       a.c_dtype == MOE_BF16 ? put(bf16_t{}) : put(f16_t{});
       continue;
     }
     uint32_t most = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = max(most, (e < 4 ? e < n0 : e - 4 < n1) ? __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu : 0u);
+    for (int e = 0; e < 8; ++e) most = max(most, (e < 4 ? e < p.n0 : e - 4 < p.n1) ? __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu : 0u);
 #pragma unroll
     for (int o = LG / 2; o; o /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, o));
     const bool finite = most < 0x7F800000u;
@@ -242,11 +278,15 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     if (!page_ok) continue;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int n = i ? n1 : n0;
-      int8_t* o = (int8_t*)pool + at + (i ? at1 : at0);
+      const int n = i ? p.n1 : p.n0;
+      int8_t* o = (int8_t*)pool + at + (i ? p.at1 : p.at0);
+      if (n >= 4) {
+        __builtin_memcpy(o, &codes[i], 4);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (e < n) o[e] = (int8_t)(codes[i] >> (8 * e));
+        for (int e = 0; e < 3; ++e)
+          if (e < n) o[e] = (int8_t)(codes[i] >> (8 * e));
+      }
     }
     if (l == 0)
       (is_v ? a.c.vs : a.c.ks)[((int64_t)page * a.c.n_kv + h) * a.c.page_size + slot] = finite ? s.d : __builtin_nanf("");
@@ -287,9 +327,6 @@ constexpr int kMaxRuns = 64;   // runs_of of any count
 // Every LDS access of the wave has finished, then the workgroup meets; loads stay on their way.
 __device__ __forceinline__ void meet() { asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory"); }
 
-#define PVB(e) (((e) & 1) == 1)
-#define QKB __builtin_amdgcn_sched_barrier(0)
-#define SMB __builtin_amdgcn_sched_barrier(0)
 template <typename T>
 struct Mat;
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -356,14 +393,16 @@ constexpr uint32_t kNowhere = 0x80000000u;   // an offset past any buffer: the l
 // then go through LDS (a ring of stages of 32 keys, loaded straight into it), and have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. The next
 // keys are loaded as soon as these are multiplied, the next values as soon as these are.
 constexpr int ring_bytes(int hd, bool i8) { return 64 * hd * (i8 ? 1 : 2) * (hd * (i8 ? 1 : 2) > 256 ? 2 : 3); }   // three stages, or two large ones
-constexpr int kAttendWaves(int hd, int nt) { return 2; }   // of a SIMD
+constexpr int kAttendWaves(int hd) { return hd < 256 ? 2 : 1; }   // of a SIMD: what their registers leave room for
 template <typename T, bool I8, int HD, int NT, bool WIDE>
-__global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs a) {
+__global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) {
   using M = Mat<T>;
   using KV = Keys<I8, HD>;
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1), KS = HD / 32, E0 = HD < 128 ? 4 : 8, NH = HD < 128 ? 1 : HD / 128, DT = E0 * NH;
   constexpr int SIZE = I8 ? 1 : 2, STRIDE = HD + 4;
   __shared__ float s_m[4][WIDE ? 1 : ROWS], s_l[4][WIDE ? 1 : ROWS], s_o[4][WIDE ? 1 : 16 * STRIDE];
+  constexpr bool Q_LDS = !WIDE && NT == 2;
+  __shared__ u32x4 s_q[Q_LDS ? NT : 1][Q_LDS ? KS : 1][Q_LDS ? 64 : 1];
   __shared__ int s_wave[4];
   // the ring: rows of 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that neighbouring lanes meet other banks
   constexpr int CR = HD * SIZE / 16, HALF = 32 * HD * SIZE, STAGE = 2 * HALF, STAGES = ring_bytes(HD, I8) / STAGE;
@@ -453,7 +492,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
 
     // rows: this lane's row of each tile of 16, its token's mask, and its part of Q^T
     uint64_t seen[NT];
-    u32x4 q[NT][KS];
+    u32x4 q[Q_LDS ? 1 : NT][Q_LDS ? 1 : KS];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       const int r = tile * ROWS + 16 * ((WIDE ? wave * NT : 0) + t) + col, j = r / G;
@@ -466,11 +505,15 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
         const int i = I8 ? (k >> 1) * 64 + quad * 16 + (k & 1) * 8 : k * 32 + quad * 8;
-        q[t][k] = u32x4{0, 0, 0, 0};
-        if (row && i < d && a.scale != 0.0f) __builtin_memcpy(&q[t][k], x + i, 16);
-        if (a.scale < 0.0f) q[t][k] ^= 0x80008000u;
+        if (Q_LDS && (k & 3) != wave) continue;
+        u32x4 v = {0, 0, 0, 0};
+        if (row && i < d && a.scale != 0.0f) __builtin_memcpy(&v, x + i, 16);
+        if (a.scale < 0.0f) v ^= 0x80008000u;
+        if constexpr (Q_LDS) s_q[t][k][lane] = v;
+        else q[t][k] = v;
       }
     }
+    if constexpr (Q_LDS) __syncthreads();
     float m[NT], l[NT];
     int e_ref = -127;   // of an i8 cache's scales: weights are times scale / 2^e_ref
     f32x4 acc[NT][DT];
@@ -610,16 +653,29 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
 
     bool odd = false;   // whether a value of a window's key is not finite
     // One step; `next` is called when the keys (true) and then the values (false) are used up.
-    auto use = [&](KV& kv, int step, const bool (&live)[2], auto next) {
+    // Steps of the context whose pages are all there (`plain`) need no masks; a loop of their own keeps the masks' registers
+    // out of it.
+    auto plain = [&](int step, const bool (&live)[2]) { return key_of(step) + 32 <= ctx && live[0] && live[1]; };
+    auto use = [&](auto checked, KV& kv, int step, const bool (&live)[2], auto next) {
+      constexpr bool check = checked();
       const int key = key_of(step);
-      const bool check = key + 32 > ctx || !live[0] || !live[1];
       f32x4 p[2][NT];
+      int q_lane = lane;   // read each time: kept, the rows cost registers that the loop has not
+      if constexpr (Q_LDS) asm volatile("" : "+v"(q_lane));
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int n = 0; n < NT; ++n) p[t][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
+      for (int k = 0; k < KS; ++k) {
+        u32x4 qk[NT];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          if constexpr (Q_LDS) qk[n] = s_q[n][k][q_lane];
+          else qk[n] = q[n][k];
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
           u32x4 f;
           if constexpr (I8) {
 #pragma unroll
@@ -631,18 +687,19 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
             f = kv.k[t][k];
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) p[t][n] = M::mma(f, q[n][k], p[t][n]);
+          for (int n = 0; n < NT; ++n) p[t][n] = M::mma(f, qk[n], p[t][n]);
         }
-        if constexpr (I8) {
+      }
+      if constexpr (I8) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) p[t][n][i] *= kv.ks[t][i];
-        }
       }
-      QKB;
       next(true);
-      if (check) {
+      if constexpr (check) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -751,7 +808,6 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) acc[n][h * E0 + e8] = M::mma(f, w[n], acc[n][h * E0 + e8]);
-          if (PVB(e8)) __builtin_amdgcn_sched_barrier(0);
         }
       next(false);
     };
@@ -786,25 +842,38 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
       for (int i = 0; i < STAGES - 1; ++i)
         if (i < steps) send(i, i);
       if constexpr (I8) scales(ahead, 0, true, true);
-      for (int i = 0, slot = 0; i < steps; ++i, slot = slot + 1 == STAGES ? 0 : slot + 1) {
+      auto arrive = [&](int i) {
         // this step has landed: all but the loads of the steps behind it
         if (i + STAGES - 2 < steps) __builtin_amdgcn_s_waitcnt(MOE_VM(PER * (STAGES - 2)));
         else __builtin_amdgcn_s_waitcnt(MOE_VM(0));
         meet();   // all waves', and the stage before it is free
+        live[0] = lives >> (2 * (i & 31)) & 1, live[1] = lives >> (2 * (i & 31) + 1) & 1;
+      };
+      auto step = [&](auto checked, int i, int slot) {
         const int next = i + STAGES - 1;
         if constexpr (I8) {
 #pragma unroll
           for (int t = 0; t < 2; ++t) x.ks[t] = ahead.ks[t], x.vs[t] = ahead.vs[t];
           if (STAGES > 2 && i + 1 < steps) scales(ahead, i + 1, true, true);   // while its pages are there
         }
-        live[0] = lives >> (2 * (i & 31)) & 1, live[1] = lives >> (2 * (i & 31) + 1) & 1;
         if (next < steps) {
           if ((next & 31) == 0) pages(next);
           send(next, slot == 0 ? STAGES - 1 : slot - 1);
           if constexpr (I8 && STAGES == 2) scales(ahead, next, true, true);
         }
         read(x, slot);
-        use(x, i, live, [](bool) {});
+        use(checked, x, i, live, [](bool) {});
+      };
+      int i = 0, slot = 0;
+      for (; i < steps; ++i, slot = slot + 1 == STAGES ? 0 : slot + 1) {
+        arrive(i);
+        if (!plain(i, live)) break;
+        step(std::false_type{}, i, slot);
+      }
+      while (i < steps) {
+        step(std::true_type{}, i, slot);
+        ++i, slot = slot + 1 == STAGES ? 0 : slot + 1;
+        if (i < steps) arrive(i);
       }
     }
     for (int batch = 0; !WIDE && batch < steps; batch += 32) {
@@ -814,9 +883,18 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
       load(x, batch, true, false);
       __builtin_amdgcn_sched_barrier(0);   // in this order, so that the loop waits for the keys alone
       load(x, batch, false, true);
-      for (int i = batch; i < last; ++i) {
+      int i = batch;
+      auto step = [&](auto checked, const bool (&live)[2]) {
+        use(checked, x, i, live, [&](bool keys_done) { load(x, i + 1 < last ? i + 1 : steps, keys_done, !keys_done); });
+      };
+      for (; i < last; ++i) {
         const bool live[2] = {(bool)(there >> (2 * (i & 31)) & 1), (bool)(there >> (2 * (i & 31) + 1) & 1)};
-        use(x, i, live, [&](bool keys_done) { load(x, i + 1 < last ? i + 1 : steps, keys_done, !keys_done); });
+        if (!plain(i, live)) break;
+        step(std::false_type{}, live);
+      }
+      for (; i < last; ++i) {
+        const bool live[2] = {(bool)(there >> (2 * (i & 31)) & 1), (bool)(there >> (2 * (i & 31) + 1) & 1)};
+        step(std::true_type{}, live);
       }
     }
     if (odd) add_odd();
@@ -932,21 +1010,24 @@ __global__ __launch_bounds__(256, kAttendWaves(HD, NT)) void k_attend(AttendArgs
   }
 }
 
-// The runs of a row and head: a workgroup each; lanes side by side take neighbouring values and the groups of lanes every
-// eighth run (of head_dim 128), always in the same order.
-template <typename T>
+// The runs of a row and head, by W waves. Lanes side by side take four neighbouring values, and the groups of lanes every
+// 4 W / (2 W, W)-th run of head_dim up to 64 (128, 256), always in the same order.
+template <typename T, int W>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
-  __shared__ float s_w[kMaxRuns];
-  __shared__ f32x4 s_o[256];
-  const int row = blockIdx.x / a.n_heads, head = blockIdx.x % a.n_heads, tid = threadIdx.x, d = a.c.d;
-  const Seq q = seq_of(a.w, row, a.w.max_window);
-  if (q.tokens == 0) return;
-  const int runs = runs_of(q.ctx + q.tokens, a.least_run);
-  if (runs == 1) return;
-  const int64_t idx = (int64_t)blockIdx.x * a.max_runs;
-  const int lane = tid & 63;
+  __shared__ float s_w[4 / W][kMaxRuns];
+  __shared__ f32x4 s_o[W > 1 ? 256 : 1];
+  const int tid = threadIdx.x, lane = tid & 63, team = tid / (64 * W), d = a.c.d;
+  const int64_t item = (int64_t)blockIdx.x * (4 / W) + team;
+  const bool there = item < (int64_t)a.w.n_tokens * a.n_heads;
+  const int row = there ? (int)(item / a.n_heads) : 0, head = there ? (int)(item % a.n_heads) : 0;
+  const int64_t idx = there ? item * a.max_runs : 0;
+  // asked for before it is known how many there are
   float best = -__builtin_inff(), l = 0.0f;
-  if (lane < runs) best = a.part_ml[2 * (idx + lane)], l = a.part_ml[2 * (idx + lane) + 1];
+  if (lane < a.max_runs) best = a.part_ml[2 * (idx + lane)], l = a.part_ml[2 * (idx + lane) + 1];
+  const Seq q = seq_of(a.w, row, a.w.max_window);
+  const int runs = there && q.tokens > 0 ? runs_of(q.ctx + q.tokens, a.least_run) : 0;
+  if (runs <= 1) return;   // W > 1: the whole workgroup
+  if (lane >= runs) best = -__builtin_inff(), l = 0.0f;
   const float m = best;
 #pragma unroll
   for (int o = 32; o; o /= 2) best = __builtin_fmaxf(best, __shfl_xor(best, o));
@@ -954,24 +1035,32 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
   float sum = l * w;
 #pragma unroll
   for (int o = 32; o; o /= 2) sum += __shfl_xor(sum, o);
-  if (tid < kMaxRuns) s_w[tid] = w;
-  __syncthreads();
-  const int wide = d <= 64 ? 16 : d <= 128 ? 32 : 64, at = (tid % wide) * 4, first = tid / wide, groups = 256 / wide;
+  if (W == 1 || tid < 64) s_w[team][lane] = w;
+  if constexpr (W > 1) __syncthreads();
+  else __builtin_amdgcn_wave_barrier();
+  const int wide = d <= 64 ? 16 : d <= 128 ? 32 : 64, mine = tid % (64 * W), at = (mine % wide) * 4, groups = 64 * W / wide;
   f32x4 o = {0, 0, 0, 0};
   if (at < d) {
     const float* p = a.part + idx * d + at;
 #pragma unroll 4
-    for (int r = first; r < runs; r += groups) {
+    for (int r = mine / wide; r < runs; r += groups) {
       const f32x4 x = *(const f32x4*)(p + (int64_t)r * d);
-      const float f = s_w[r];
+      const float f = s_w[team][r];
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(x[i], f, o[i]);
     }
   }
-  s_o[tid] = o;
-  __syncthreads();
-  if (tid < wide && at < d) {
-    for (int g = 1; g < groups; ++g) o += s_o[g * wide + tid];
+  if constexpr (W > 1) {
+    s_o[tid] = o;
+    __syncthreads();
+    if (tid < wide)
+      for (int g = 1; g < groups; ++g) o += s_o[g * wide + tid];
+  } else {
+    for (int step = wide; step < 64; step *= 2)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] += __shfl_xor(o[i], step);
+  }
+  if (mine < wide && at < d) {
     T* out = (T*)a.out + row * a.ldo + (int64_t)head * d + at;
     T y[4];
 #pragma unroll
@@ -1439,13 +1528,15 @@ int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
   return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, kMaxRuns);
 }
 
+constexpr int kAppendFew = 512;   // tokens whose heads are spread over several workgroups
+constexpr int kJoinWide = 1024;   // rows and heads that get four waves each
 template <typename T, bool I8, int HD, int NT, bool WIDE>
 int launch_attend(hipStream_t st, const AttendArgs& a) {
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1);
   const int64_t tiles = ((int64_t)a.w.max_window * (a.n_heads / a.c.n_kv) + ROWS - 1) / ROWS;
   const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;
   if (items > 0x7FFFFFFF) return MOE_E_SHAPE;
-  const int grid = (int)std::min<int64_t>(256 * kAttendWaves(HD, NT), (items + 7) & ~7ll);
+  const int grid = (int)std::min<int64_t>(256 * kAttendWaves(HD), (items + 7) & ~7ll);
   const int lds = (WIDE ? ring_bytes(HD, I8) : 0) + 4 * a.w.n_seqs;
   const auto kern = k_attend<T, I8, HD, NT, WIDE>;
   if (lds > 64 * 1024) {
@@ -1455,7 +1546,9 @@ int launch_attend(hipStream_t st, const AttendArgs& a) {
   hipLaunchKernelGGL(kern, dim3(grid), dim3(256), lds, st, a);
   if (const int rc = launched("moe_window_attention")) return rc;
   if (a.max_runs > 1) {
-    hipLaunchKernelGGL(k_attend_join<T>, dim3((unsigned)(a.w.n_tokens * a.n_heads)), dim3(256), 0, st, a);
+    const int64_t rows = (int64_t)a.w.n_tokens * a.n_heads;
+    if (rows <= kJoinWide) hipLaunchKernelGGL((k_attend_join<T, 4>), dim3((unsigned)rows), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((k_attend_join<T, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, st, a);
     return launched("moe_window_attention");
   }
   return MOE_OK;
@@ -1467,9 +1560,8 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   auto tiles = [&](auto i, auto hd) {
     constexpr bool I8 = decltype(i)::value;
     constexpr int HD = decltype(hd)::value;
-    constexpr int MOST = HD == 256 ? 1 : 2;   // tiles of 16 rows that a wave has registers for
-    if (rows > 32) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, MOST, true>(st, a);
-    return rows <= 16 ? launch_attend<T, I8, HD, 1, false>(st, a) : launch_attend<T, I8, HD, MOST, false>(st, a);
+    if (rows > 32) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, HD == 256 && !I8 ? 1 : 2, true>(st, a);
+    return rows <= 16 ? launch_attend<T, I8, HD, 1, false>(st, a) : launch_attend<T, I8, HD, 2, false>(st, a);
   };
   auto width = [&](auto i) {
     using std::integral_constant;
@@ -1525,16 +1617,17 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
     if (over(r, spans)) return MOE_E_ARG;
   for (int i = 0; i < 5; ++i)
     if (overlap(window[i], window[5])) return MOE_E_ARG;
-  const int heads = q ? n_heads : 0, units = heads + 2 * C->n_kv;
+  const int heads = q ? n_heads : 0, all = heads + 2 * C->n_kv;
+  const int lanes = std::max((d + 7) / 8, (n_rot + 7) / 8 + (d - n_rot + 7) / 8), lg = lanes <= 8 ? 8 : lanes <= 16 ? 16 : lanes <= 32 ? 32 : 64;
+  const int units = n <= kAppendFew ? 256 / lg : all;
   const AppendArgs a{cache_args(*C), window_args(*W, *C), q, k, v, q_weight, k_weight, freq, q_out, ldq, ldk, ldv, ldqo,
                      heads, n_rot, layout, w_dtype, o_dtype, C->dtype, units, eps, amp};
-  const int lanes = std::max((d + 7) / 8, (n_rot + 7) / 8 + (d - n_rot + 7) / 8);
   with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(n), dim3(256), 0, (hipStream_t)stream, a); };
-    if (lanes <= 8) go(k_window_append<T, 8>);
-    else if (lanes <= 16) go(k_window_append<T, 16>);
-    else if (lanes <= 32) go(k_window_append<T, 32>);
+    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(n, (all + units - 1) / units), dim3(256), 0, (hipStream_t)stream, a); };
+    if (lg == 8) go(k_window_append<T, 8>);
+    else if (lg == 16) go(k_window_append<T, 16>);
+    else if (lg == 32) go(k_window_append<T, 32>);
     else go(k_window_append<T, 64>);
   });
   return launched("moe_window_append");
