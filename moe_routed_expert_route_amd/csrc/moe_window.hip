@@ -142,16 +142,60 @@ __device__ __forceinline__ void load4(const void* p, int dtype, int at, int n, f
   });
 }
 
+// Sum and maximum over LG neighbouring lanes, in all of them: halves of 8 mirrored, rows of 16 turned round, then the
+// neighbouring rows.
+template <int LG>
+__device__ __forceinline__ double lanes_sum(double v) {
+  if constexpr (LG == 8) {
+    v += dpp0<0x141, 0xF>(v);
+    v += dpp0<0x4E, 0xF>(v);
+    v += dpp0<0xB1, 0xF>(v);
+  } else {
+    v += dpp0<0x128, 0xF>(v);
+    v += dpp0<0x124, 0xF>(v);
+    v += dpp0<0x122, 0xF>(v);
+    v += dpp0<0x121, 0xF>(v);
+  }
+  if constexpr (LG >= 32) v += __shfl_xor(v, 16);
+  if constexpr (LG >= 64) v += __shfl_xor(v, 32);
+  return v;
+}
+template <int LG>
+__device__ __forceinline__ uint32_t lanes_max(uint32_t v) {
+  if constexpr (LG == 8) {
+    v = max(v, dpp0<0x141, 0xF>(v));
+    v = max(v, dpp0<0x4E, 0xF>(v));
+    v = max(v, dpp0<0xB1, 0xF>(v));
+  } else {
+    v = max(v, dpp0<0x128, 0xF>(v));
+    v = max(v, dpp0<0x124, 0xF>(v));
+    v = max(v, dpp0<0x122, 0xF>(v));
+    v = max(v, dpp0<0x121, 0xF>(v));
+  }
+  if constexpr (LG >= 32) v = max(v, (uint32_t)__shfl_xor((int)v, 16));
+  if constexpr (LG >= 64) v = max(v, (uint32_t)__shfl_xor((int)v, 32));
+  return v;
+}
+// 1 / sqrt(x) to two ulps for normal x > 0: the seed and two Newton steps; 0 for infinity, NaN for NaN.
+__device__ __forceinline__ double inverse_sqrt64(double x) {
+  const double s = __builtin_amdgcn_rsq(x);
+  const double h = 0.5 * x;
+  const double r = __builtin_fma(s, __builtin_fma(-h * s, s, 0.5), s);
+  const double y = __builtin_fma(r, __builtin_fma(-h * r, r, 0.5), r);
+  return x < __builtin_inf() ? y : s;
+}
+
 // A head's row is with LG neighbouring lanes, eight values each: four pairs (of MOE_ROPE_HALF: four values and their
-// four partners), or eight values that do not turn. A workgroup takes `units` heads of a token, the next head's values on
-// their way while it works on one. The first are asked for before the token's sequence is known. Everything is in 64 bits
-// (full rate here), which a dozen instructions a value leave hidden behind the bytes.
-template <typename T, int LG>
+// four partners), or eight values that do not turn. A workgroup takes `units` heads of a token, or all of TK tokens, which
+// it looks up side by side, a wave each; the next head's values are on their way while it works on one, the first before
+// the sequences are known. Everything is in 64 bits (full rate here).
+template <typename T, int LG, int TK>
 __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
   constexpr int GROUPS = 256 / LG;
-  __shared__ double s_turn[128][2];
-  const int row = blockIdx.x, l = threadIdx.x % LG, d = a.c.d, half = a.n_rot / 2;
-  const int last = min((int)(blockIdx.y + 1) * a.units, a.n_heads + 2 * a.c.n_kv);
+  __shared__ double s_turn[TK][128][2];
+  __shared__ int s_place[TK][4];   // key (-1: no token), page (-1: none), slot
+  const int first_row = blockIdx.x * TK, l = threadIdx.x % LG, d = a.c.d, half = a.n_rot / 2, all = a.n_heads + 2 * a.c.n_kv;
+  const int last = min((int)(blockIdx.y + 1) * a.units, all);   // of the heads (TK = 1)
   struct Part {   // this lane's values of a head: n0 from at0 on, n1 from at1 on
     int at0, at1, n0, n1;
     bool turns, halves;
@@ -168,17 +212,23 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
   };
   const Part turning = part_of(false), plain = part_of(true);
   T raw[2][4];
-  auto load = [&](int u) {
-    if (u >= last) return;
+  auto load = [&](int row, int u) {
+    if (row >= first_row + TK || row >= a.w.n_tokens || u >= last) return;
     const bool is_q = u < a.n_heads, is_v = u >= a.n_heads + a.c.n_kv;
     const int h = is_q ? u : is_v ? u - a.n_heads - a.c.n_kv : u - a.n_heads;
     const T* x = is_q ? (const T*)a.q + row * a.ldq : is_v ? (const T*)a.v + row * a.ldv : (const T*)a.k + row * a.ldk;
     const Part p = is_v ? plain : turning;
-    load4(x + (int64_t)h * d + p.at0, p.n0, raw[0]);
-    load4(x + (int64_t)h * d + p.at1, p.n1, raw[1]);
+    x += (int64_t)h * d;
+    load4(x + p.at0, p.n0, raw[0]);
+    load4(x + p.at1, p.n1, raw[1]);
   };
-  int u = blockIdx.y * a.units + (int)threadIdx.x / LG;
-  load(u);
+  int row = first_row, u = blockIdx.y * a.units + (int)threadIdx.x / LG;
+  auto next = [&](int& row, int& u) {
+    u += GROUPS;
+    while (TK > 1 && u >= all) u -= all, ++row;
+  };
+  while (TK > 1 && u >= all) u -= all, ++row;
+  load(row, u);
   // the weights of this lane's values
   float qw[8], kw[8];
   if (a.q_weight) {
@@ -190,41 +240,54 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     load4(a.k_weight, a.w_dtype, turning.at1, turning.n1, kw + 4);
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) check_seqs(a.w, 0x7FFFFFFF, 256);
-  const Seq q = seq_of(a.w, row, 0x7FFFFFFF);
-  if (q.tokens == 0) return;
-  const int key = q.ctx + row - q.start, slot = key % a.c.page_size;
-  const int page = a.w.pages[q.s * a.w.ld_pages + key / a.c.page_size];
-  const bool page_ok = page >= 0 && page < a.c.n_pages;
-  if (!page_ok && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(a.w.err, MOE_ERR_PAGE);
-  if ((int)threadIdx.x < half) {
+  const int wave = threadIdx.x >> 6;
+  int my_key = -1, my_page = -1, my_slot = 0;
+  if (TK == 1 || wave < TK) {
+    const int mine = first_row + (TK == 1 ? 0 : wave);
+    const Seq q = mine < a.w.n_tokens ? seq_of(a.w, mine, 0x7FFFFFFF) : Seq{0, 0, 0, 0};
+    if (q.tokens > 0) {
+      my_key = q.ctx + mine - q.start;
+      my_page = a.w.pages[q.s * a.w.ld_pages + my_key / a.c.page_size];
+      my_slot = my_key % a.c.page_size;
+      if (my_page < 0 || my_page >= a.c.n_pages) {
+        my_page = -1;
+        if (blockIdx.y == 0 && (threadIdx.x & 63) == 0) atomicOr(a.w.err, MOE_ERR_PAGE);
+      }
+    }
+    if (TK > 1 && (threadIdx.x & 63) == 0) s_place[wave][0] = my_key, s_place[wave][1] = my_page, s_place[wave][2] = my_slot;
+  }
+  if constexpr (TK > 1) __syncthreads();
+  else if (my_key < 0) return;
+  for (int i = threadIdx.x; i < TK * half; i += 256) {
+    const int t = TK == 1 ? 0 : i / half, p = i - t * half, key = TK == 1 ? my_key : s_place[t][0];
+    if (key < 0) continue;
     double c, s;
-    turn64((double)(a.w.pos ? a.w.pos[row] : key) * (double)a.freq[threadIdx.x], c, s);
-    s_turn[threadIdx.x][0] = (double)a.amp * c;
-    s_turn[threadIdx.x][1] = (double)a.amp * s;
+    turn64((double)(a.w.pos ? a.w.pos[first_row + t] : key) * (double)a.freq[p], c, s);
+    s_turn[t][p][0] = (double)a.amp * c;
+    s_turn[t][p][1] = (double)a.amp * s;
   }
   __syncthreads();
-  double turn_c[4], turn_s[4];   // of this lane's pairs; past the last (1, 0)
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const bool in = 4 * l + e < half;
-    turn_c[e] = in ? s_turn[4 * l + e][0] : 1.0;
-    turn_s[e] = in ? s_turn[4 * l + e][1] : 0.0;
-  }
-  for (; u < last; u += GROUPS) {
+  for (; row < first_row + TK && u < last; next(row, u)) {
     const bool is_q = u < a.n_heads, is_v = u >= a.n_heads + a.c.n_kv;
+    const int t = row - first_row;
+    const int page = TK == 1 ? my_page : s_place[t][1], slot = TK == 1 ? my_slot : s_place[t][2];
+    const bool page_ok = page >= 0;
     const int h = is_q ? u : is_v ? u - a.n_heads - a.c.n_kv : u - a.n_heads;
     const Part p = is_v ? plain : turning;
     double y[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (double)to_f(raw[e / 4][e % 4]);
-    load(u + GROUPS);
+    {
+      int r = row, v = u;
+      next(r, v);
+      load(r, v);
+    }
+    if (TK > 1 && s_place[t][0] < 0) continue;   // a row of no sequence
     if (is_q ? a.q_weight != nullptr : !is_v && a.k_weight) {
       double sum = 0.0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum = __builtin_fma(y[e], y[e], sum);
-#pragma unroll
-      for (int o = LG / 2; o; o /= 2) sum += __shfl_xor(sum, o);
-      const double rinv = 1.0 / __builtin_sqrt(sum / d + (double)a.eps);
+      const double rinv = inverse_sqrt64(__builtin_fma(lanes_sum<LG>(sum), 1.0 / d, (double)a.eps));
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = y[e] * rinv * (double)(is_q ? qw[e] : kw[e]);
     }
@@ -232,7 +295,8 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
       double z[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const double c = turn_c[e], s = turn_s[e];
+        const bool in = 4 * l + e < half;   // past the last pair zeros, which stay
+        const double c = in ? s_turn[t][4 * l + e][0] : 1.0, s = in ? s_turn[t][4 * l + e][1] : 0.0;
         const double p0 = p.halves ? y[e] : y[2 * e], p1 = p.halves ? y[4 + e] : y[2 * e + 1];
         const double r0 = __builtin_fma(p0, c, -(p1 * s)), r1 = __builtin_fma(p1, c, p0 * s);
         // by selects: an index that differs from lane to lane would put y into memory
@@ -246,11 +310,14 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     float f[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) f[e] = (float)y[e];
+    auto put = [&](auto* o, const float* f) {
+      store4(o + p.at0, p.n0, f);
+      store4(o + p.at1, p.n1, f + 4);
+    };
     if (is_q) {
       on_type(a.o_dtype, [&](auto t) {
         auto* o = (decltype(t)*)a.q_out + row * a.ldo + (int64_t)h * d;
-        store4(o + p.at0, p.n0, f);
-        store4(o + p.at1, p.n1, f + 4);
+        put(o, f);
       });
       continue;
     }
@@ -258,19 +325,13 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     uint8_t* pool = is_v ? a.c.v : a.c.k;
     if (a.c_dtype != MOE_I8) {
       if (!page_ok) continue;
-      auto put = [&](auto t) {
-        auto* o = (decltype(t)*)pool + at;
-        store4(o + p.at0, p.n0, f);
-        store4(o + p.at1, p.n1, f + 4);
-      };
-      a.c_dtype == MOE_BF16 ? put(bf16_t{}) : put(f16_t{});
+      a.c_dtype == MOE_BF16 ? put((bf16_t*)pool + at, f) : put((f16_t*)pool + at, f);
       continue;
     }
     uint32_t most = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) most = max(most, (e < 4 ? e < p.n0 : e - 4 < p.n1) ? __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu : 0u);
-#pragma unroll
-    for (int o = LG / 2; o; o /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, o));
+    most = lanes_max<LG>(most);
     const bool finite = most < 0x7F800000u;
     const QScale s = q_scale(__builtin_bit_cast(float, most));
     uint32_t codes[2] = {0, 0};
@@ -1624,11 +1685,16 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
                      heads, n_rot, layout, w_dtype, o_dtype, C->dtype, units, eps, amp};
   with_type(dtype, [&](auto t) {
     using T = decltype(t);
-    auto go = [&](auto kern) { hipLaunchKernelGGL(kern, dim3(n, (all + units - 1) / units), dim3(256), 0, (hipStream_t)stream, a); };
-    if (lg == 8) go(k_window_append<T, 8>);
-    else if (lg == 16) go(k_window_append<T, 16>);
-    else if (lg == 32) go(k_window_append<T, 32>);
-    else go(k_window_append<T, 64>);
+    auto go = [&](auto l) {
+      constexpr int LG = decltype(l)::value;
+      if (n <= kAppendFew) hipLaunchKernelGGL((k_window_append<T, LG, 1>), dim3(n, (all + units - 1) / units), dim3(256), 0, (hipStream_t)stream, a);
+      else hipLaunchKernelGGL((k_window_append<T, LG, 4>), dim3((n + 3) / 4), dim3(256), 0, (hipStream_t)stream, a);
+    };
+    using std::integral_constant;
+    if (lg == 8) go(integral_constant<int, 8>{});
+    else if (lg == 16) go(integral_constant<int, 16>{});
+    else if (lg == 32) go(integral_constant<int, 32>{});
+    else go(integral_constant<int, 64>{});
   });
   return launched("moe_window_append");
 }
