@@ -413,8 +413,9 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
  * rows as they were. MOE_ERR_PAGE: a page out of [0, n_pages): its keys are not written, and nobody sees them. */
 
 /* A layer's cache. Row (page p, head h, slot i) of k and of v starts p * page_stride + h * head_stride + i *
- * slot_stride elements from k and v and holds head_dim elements; strides are positive multiples of 16 of either nesting order, and
- * rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k and v are 16-byte aligned.
+ * slot_stride elements from k and v and holds head_dim elements; strides are positive multiples of 16, slot_stride at most
+ * 2^24, of any nesting order, and rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k and v are
+ * 16-byte aligned.
  * dtype MOE_BF16, MOE_F16, or MOE_I8: i8 rows, one scale a row at [(p * n_kv + h) * page_size + i] of k_scale and v_scale
  * (NULL for the others). page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple of 16 up to 256; n_kv up to
  * MOE_MAX_HEADS. Host struct holding device pointers. */
@@ -476,8 +477,9 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
  * q, out [n_tokens][ldq], [ldo] in `dtype`: the cache's type, or MOE_BF16 or MOE_F16 over an i8 cache; lse float32
  * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max), times the value's scale over an i8
  * cache, is rounded to `dtype` in front of its product, and the sum below is of the unrounded ones.
- * A sequence's keys are summed in runs whose length depends on its own key count and on max_window * n_heads /
- * n_kv being above 32 or not: a token's bits depend neither on the call's other sequences nor on the other tokens of its window.
+ * A value of a window's key that is not finite reaches the rows that see it, and no others. A sequence's keys are summed in
+ * runs whose length depends on its own key count and on the call's sizes (n_seqs, max_window, heads): a token's bits do not
+ * depend on what the other sequences of the call hold.
  * workspace: moe_window_attention_bytes, 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type or
  * stride, scale not finite, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
  * not a multiple of n_kv), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */

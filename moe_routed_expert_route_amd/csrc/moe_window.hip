@@ -188,7 +188,9 @@ __device__ __forceinline__ double inverse_sqrt64(double x) {
 // A head's row is with LG neighbouring lanes, eight values each: four pairs (of MOE_ROPE_HALF: four values and their
 // four partners), or eight values that do not turn. A workgroup takes `units` heads of a token, or all of TK tokens, which
 // it looks up side by side, a wave each; the next head's values are on their way while it works on one, the first before
-// the sequences are known. Everything is in 64 bits (full rate here).
+// the sequences are known. Everything is in 64 bits: sums and products at full rate, conversions at a quarter, which bound
+// 8192 tokens of 48 heads of 128 (77 us, 2.6 TB/s; without the norm 69). One token takes 5.1 us: loads that wait for each other.
+// Slower for the 8192: one token a workgroup (99 us), two to four heads on their way (82 to 98), weights kept in 64 bits (101).
 template <typename T, int LG, int TK>
 __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
   constexpr int GROUPS = 256 / LG;
@@ -362,7 +364,14 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
 // of one row and the row's factors are the lane's own, and K's rows go from memory straight into the matrix instruction's
 // lanes; the exponentials are already where V^T . P^T takes them (which key is which place of the sum over keys is free, as
 // long as V agrees), and a lane loads the same eight neighbouring values of eight keys, from which a byte permutation
-// makes the eight rows of V^T. No LDS until the waves join.
+// makes the eight rows of V^T. Without WIDE there is no LDS until the waves join.
+// Bound by the cache's bytes up to some 32 rows a cache head: 4 tokens x 8 heads over 131072 keys 55 us (4.9 TB/s) and 5 to
+// join, one token 50 us (5.3 TB/s); 64 sequences x 4 tokens of 512 to 8192 keys, int8 136 us (4.4 TB/s) and 8. One token
+// over 4096 keys takes 11 us and 4 to join: loads that wait for each other (lengths, pages, keys) and code that is new to the
+// instruction cache. Trees of 64 tokens x 8 heads over 4096 to 8100 keys 219 us (0.44 PFLOP/s) and 24: some 230 vector and
+// 170 scalar instructions beside 32 matrix instructions a step, which two waves a SIMD overlap only in part.
+// Tried and slower: keys and values of two steps in registers (145 us for the int8 batch where this takes 136), three
+// waves a SIMD (spills; 158), values read from the ring when they are needed (265 us for the trees where this takes 219).
 
 struct AttendArgs {
   CacheArgs c;
@@ -1071,7 +1080,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
   }
 }
 
-// The runs of a row and head, by W waves. Lanes side by side take four neighbouring values, and the groups of lanes every
+// The runs of a row and head, by W waves: 8192 rows 8.4 us by one each, 16.4 by four. Lanes side by side take four neighbouring values, and the groups of lanes every
 // 4 W / (2 W, W)-th run of head_dim up to 64 (128, 256), always in the same order.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
@@ -1137,15 +1146,16 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 // A row is cut into pieces of 256 lanes times EL values (by the row's length alone, so that its sums have one order).
 // k_scores takes a piece into registers, reads it once, and leaves its maximum, its sums of e = exp(z) and of e z, and the best
 // tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The
-// pieces' bound for the best: the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at
-// least that, and few values are above it.
+// pieces' bound for the best is the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at
+// least that, and few values are above it. 1024 x 131072 bf16: 53 us for k = 8 (5.0 TB/s), 48 for none, 72 for 32; the join
+// 7, 5 and 17. Slower: workgroups that go on to further pieces with the next one's values on their way (75; 55 for none).
 
 struct ScoreArgs {
   const void* logits;
   const int32_t* tokens;
   float *logp, *entropy, *top_logp;
   int32_t* top_ids;
-  float* stats;       // [row][piece] maximum, sum of e, sum of e z, and how many best
+  float* stats;       // [row][piece] maximum, sums of e and of e z without the maxima, how many best and (from bit 16) maxima
   uint64_t* best;     // [row][piece][kKept] their keys
   int64_t ld;
   int n, given, k, pieces;
@@ -1245,7 +1255,7 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   __shared__ uint64_t s_list[kListed];
   __shared__ float s_sum[2][4];
   __shared__ uint64_t s_key[4];
-  __shared__ int s_count;
+  __shared__ int s_count, s_tops;
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63;
   const int64_t row = blockIdx.x / a.pieces;
   const int piece = blockIdx.x % a.pieces, from = piece * (256 * EL);
@@ -1277,7 +1287,7 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
       }
     }
   }
-  if (tid == 0) s_count = 0;
+  if (tid == 0) s_count = s_tops = 0;
   float mine = -__builtin_inff();
 #pragma unroll
   for (int p = 0; p < PIECES; ++p)
@@ -1319,6 +1329,26 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
         dot = __builtin_fmaf(y, z, dot);
       }
     }
+  }
+  // A row that is sure of a token has a sum of 1 and little more, and that little is what its entropy hangs on: the lanes
+  // that have the maximum add up the others alone, and the join counts the maxima.
+  if (mine == top) {
+    sum = dot = 0.0f;
+    int tops = 0;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) {
+      raw[p].forget();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float v = masked_logit(raw[p].at(e));
+        const float z = __builtin_fmaxf(__builtin_fabsf(tc) < kFused ? __builtin_fmaf(v, c, -tc) : (v - top) * c, -200.0f);
+        const float y = v == top ? 0.0f : __builtin_amdgcn_exp2f(z);
+        tops += v == top;
+        sum += y;
+        dot = __builtin_fmaf(y, z, dot);
+      }
+    }
+    if (!none) atomicAdd(&s_tops, tops);
   }
   sum = wave_sum_f(sum);
   dot = wave_sum_f(dot);
@@ -1363,7 +1393,7 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
     stats[0] = none ? -__builtin_inff() : top;
     stats[1] = none ? 0.0f : (s_sum[0][0] + s_sum[0][1]) + (s_sum[0][2] + s_sum[0][3]);
     stats[2] = none ? 0.0f : (s_sum[1][0] + s_sum[1][1]) + (s_sum[1][2] + s_sum[1][3]);
-    stats[3] = __builtin_bit_cast(float, count <= kKept ? count : a.k);
+    stats[3] = __builtin_bit_cast(float, (count <= kKept ? count : a.k) | s_tops << 16);
   }
   if (count <= kKept) {
     if (tid < count) best[tid] = s_list[tid];
@@ -1407,16 +1437,18 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
   for (int p = lane; p < a.pieces; p += 64) {
     const float m = stats[4 * p];
     if (m == -__builtin_inff()) continue;
-    const double z = reference(m, c) - ref, f = exp64(z * ln2), s = (double)stats[4 * p + 1];
+    // the maxima's z, which the rounding of the reference leaves a little off 0, and their share
+    const double off = (double)m * (double)c - reference(m, c), tops = (double)(__builtin_bit_cast(int, stats[4 * p + 3]) >> 16) * exp64(off * ln2);
+    const double z = reference(m, c) - ref, f = exp64(z * ln2), s = (double)stats[4 * p + 1] + tops;
     sum = __builtin_fma(s, f, sum);
-    dot = __builtin_fma(f, __builtin_fma(s, f > 0.0 ? z : 0.0, (double)stats[4 * p + 2]), dot);
+    dot = __builtin_fma(f, __builtin_fma(s, f > 0.0 ? z : 0.0, __builtin_fma(tops, off, (double)stats[4 * p + 2])), dot);
   }
   sum = wave_sum(sum);
   dot = wave_sum(dot);
   const double log_sum = none ? 0.0 : log(sum), base = none ? 0.0 : (double)top;
   const double rest = ((base * (double)c) - ref) * ln2 - log_sum;
   auto logp_of = [&](float v) { return (float)(((double)v - base) * (double)a.scale + rest); };
-  if (lane == 0 && a.entropy) a.entropy[row] = none ? 0.0f : (float)(log_sum - dot / sum * ln2);
+  if (lane == 0 && a.entropy) a.entropy[row] = none ? 0.0f : (float)__builtin_fmax(log_sum - dot / sum * ln2, 0.0);
   if (lane < a.given) {
     const int id = a.tokens[row * a.given + lane];
     a.logp[row * a.given + lane] = logp_of(id >= 0 && id < a.n ? masked_logit(to_f(x[id])) : -__builtin_inff());
@@ -1438,7 +1470,7 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
     have = __popcll(__ballot(lane < a.k && mine != 0));
   };
   for (int p0 = 0; p0 < a.pieces; p0 += 64) {
-    const int counts = p0 + lane < a.pieces ? __builtin_bit_cast(int, stats[4 * (p0 + lane) + 3]) : 0;
+    const int counts = p0 + lane < a.pieces ? __builtin_bit_cast(int, stats[4 * (p0 + lane) + 3]) & 0xFFFF : 0;
     const uint64_t* best = a.best + (row * a.pieces + p0) * kKept;
     for (int p = 0; p < 64 && p0 + p < a.pieces; p += 8) {
       uint64_t key[8];
@@ -1579,7 +1611,9 @@ WindowArgs window_args(const moe_window& w, const moe_kv_cache& c) {
 
 // Rows that share a cache head, at most.
 int most_rows(const moe_kv_cache& c, const moe_window& w, int n_heads) { return w.max_window * (n_heads / c.n_kv); }
-// The least keys of a run, by how many sequences, cache heads and tiles of rows there are to spread over the card.
+// The least keys of a run, by how many sequences, cache heads and tiles of rows there are to spread over the card: 6
+// sequences x 2 heads of up to 1000 keys 18.5 us in runs of 256, 24.0 of 1024; 64 x 8 of up to 8192 196 us in runs of
+// 256 (their results are a quarter of the bytes), 158 of 1024, 160 of 2048.
 int least_run(const moe_kv_cache& c, const moe_window& w, int n_heads) {
   const int64_t units = (int64_t)w.n_seqs * c.n_kv * ((most_rows(c, w, n_heads) + 127) / 128);
   return units <= 32 ? 256 : units <= 128 ? 512 : 1024;
@@ -1633,6 +1667,7 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
+// Values of a lane: 32 spread short rows over more workgroups; 1024 rows of 131072 with 8 best 53 us with 64, 61 with 32.
 constexpr int kShortRow = 65536, kLongEl = 64;
 int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 256 * kLongEl - 1) / (256 * kLongEl); }
 

@@ -419,6 +419,24 @@ def test_logprobs_infinities_and_the_largest():
     assert h[0] == 0 and abs(float(h[1]) - math.log(2)) < 1e-6 and h[2] == 0
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [900, 32000, 100000])
+def test_logprobs_of_rows_that_are_sure(n, dtype):
+    """The sum is 1 and a little more: the terms beside the largest alone are off by 2^-22 |z| and 2^-22 each, their sum by
+    2^-16, so that what is left of entropy and log probability keeps its relative precision: 2^-15 (1 + |z|), |z| < 64. The sum
+    itself stands in 64 bits next to 1, where some four roundings of 2^-53 are absolute: 2^-50."""
+    x = randn((6, n), dtype, n, scale=1.5)
+    top = torch.arange(6, device=DEV) * (n // 6) + 3
+    x[torch.arange(6, device=DEV), top] = torch.tensor([16.0, 20.0, 24.0, 30.0, 40.0, 55.0], device=DEV).to(dtype)
+    logp, h, ids, best = B.moe_token_logprobs(x, tokens=top.int()[:, None], k=2, entropy=True)
+    z = x.double() - x.double().amax(1, keepdim=True)
+    e = torch.exp(z)
+    rest = torch.where(z < 0, e, torch.zeros_like(e)).sum(1)
+    want = torch.log1p(rest) - (e * z).sum(1) / (1 + rest)
+    assert ((h.double() - want).abs() <= want * 2.0 ** -15 * 65 + 2.0 ** -50).all() and (ids[:, 0] == top).all()
+    assert ((logp[:, 0].double() + torch.log1p(rest)).abs() <= torch.log1p(rest) * 2.0 ** -15 + 2.0 ** -50).all() and (h >= 0).all()
+
+
 @pytest.mark.parametrize("given,k,entropy", [(0, 3, False), (2, 0, False), (0, 0, True), (64, 32, True)])
 def test_logprobs_outputs_asked_for(given, k, entropy):
     x = randn((6, 9000), BF16, 3, scale=2.0)
