@@ -1147,8 +1147,8 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 // k_scores takes a piece into registers, reads it once, and leaves its maximum, its sums of e = exp(z) and of e z, and the best
 // tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The
 // pieces' bound for the best is the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at
-// least that, and few values are above it. 1024 x 131072 bf16: 53 us for k = 8 (5.0 TB/s), 48 for none, 72 for 32; the join
-// 7, 5 and 17. Slower: workgroups that go on to further pieces with the next one's values on their way (75; 55 for none).
+// least that, and few values are above it. 1024 x 131072 bf16: 62 us for k = 8 (4.4 TB/s), 47 for none; the join
+// 7 and 5. Slower: workgroups that go on to further pieces with the next one's values on their way (75; 55 for none).
 
 struct ScoreArgs {
   const void* logits;
@@ -1241,6 +1241,21 @@ struct Eight {
     const uint32_t v = sizeof(T) == 4 ? 0xFF800000u : (uint32_t)__builtin_bit_cast(uint16_t, from_f<std::conditional_t<sizeof(T) == 4, bf16_t, T>>(-__builtin_inff()));
     return sizeof(T) == 4 ? v : v | v << 16;
   }
+  // Values of the bits of `top` become -infinity; returns `bits` and the bits of these values.
+  __device__ __forceinline__ int take_out(float top, int bits) {
+    const uint32_t t = sizeof(T) == 4 ? __builtin_bit_cast(uint32_t, top)
+                                      : (uint32_t)__builtin_bit_cast(uint16_t, from_f<std::conditional_t<sizeof(T) == 4, bf16_t, T>>(top)) * 0x10001u;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const uint32_t d = w[i] ^ t;
+      uint32_t m;
+      if constexpr (sizeof(T) == 4) m = (uint32_t)((int32_t)((d >> 1 | (d & 1)) - 1) >> 31);
+      else m = ((uint32_t)((int32_t)((d & 0xFFFFu) - 1) >> 31) & 0xFFFFu) | ((uint32_t)((int32_t)((d >> 16) - 1) >> 31) & 0xFFFF0000u);
+      w[i] = (w[i] & ~m) | (none() & m);
+      bits += __builtin_popcount(m);
+    }
+    return bits;
+  }
   // What follows converts anew rather than keep a register for each value.
   __device__ __forceinline__ void forget() {
 #pragma unroll
@@ -1302,6 +1317,17 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   const bool none = most <= kMasked;
   const float top = none ? 0.0f : value_of(most);
 
+  // A row that is sure of a token has a sum of 1 and little more, and that little is what its entropy hangs on: the lanes
+  // that have the maximum take it out (any number of times; +0 for -0 stays, and infinity, with which nothing is lost), and
+  // the join counts the maxima. Without branches or masks, which cost registers: 53 us for the 1024 x 131072 without
+  // this, 62 with it, 82 by a second pass over the lane's values.
+  if (mine == top && !none) {
+    int bits = 0;
+#pragma unroll
+    for (int p = 0; p < PIECES; ++p) bits = raw[p].take_out(top, bits);
+    atomicAdd(&s_tops, bits / (8 * (int)sizeof(T)));
+  }
+
   // below -200 (masked tokens too) z counts as that, and e is 0
   const float c = unit_of(a.scale), tc = top * c;
   float sum = 0.0f, dot = 0.0f;
@@ -1329,26 +1355,6 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
         dot = __builtin_fmaf(y, z, dot);
       }
     }
-  }
-  // A row that is sure of a token has a sum of 1 and little more, and that little is what its entropy hangs on: the lanes
-  // that have the maximum add up the others alone, and the join counts the maxima.
-  if (mine == top) {
-    sum = dot = 0.0f;
-    int tops = 0;
-#pragma unroll
-    for (int p = 0; p < PIECES; ++p) {
-      raw[p].forget();
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float v = masked_logit(raw[p].at(e));
-        const float z = __builtin_fmaxf(__builtin_fabsf(tc) < kFused ? __builtin_fmaf(v, c, -tc) : (v - top) * c, -200.0f);
-        const float y = v == top ? 0.0f : __builtin_amdgcn_exp2f(z);
-        tops += v == top;
-        sum += y;
-        dot = __builtin_fmaf(y, z, dot);
-      }
-    }
-    if (!none) atomicAdd(&s_tops, tops);
   }
   sum = wave_sum_f(sum);
   dot = wave_sum_f(dot);
