@@ -466,7 +466,7 @@ typedef struct moe_window {
 typedef enum { MOE_ROPE_HALF = 1, MOE_ROPE_PAIRS = 2 } moe_rope;
 int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
                       const void* k, int64_t ldk, const void* v, int64_t ldv, int n_heads, int w_dtype, const void* q_weight,
-                      const void* k_weight, float eps, const float* freq, int n_rot, int layout, float amp, int o_dtype,
+                      const void* k_weight, float eps, const float* freq, int n_rot, int layout, double amp, int o_dtype,
                       void* q_out, int64_t ldqo);
 
 /* Attention of the window's queries over the cache, the window's own keys (appended before) among them: per row and

@@ -67,7 +67,8 @@ struct AppendArgs {
   void* q_out;
   int64_t ldq, ldk, ldv, ldo;
   int n_heads, n_rot, layout, w_dtype, o_dtype, c_dtype, units;
-  float eps, amp;
+  float eps;
+  double amp;   // as given: rounded to float32 it would move one value in thousands to the next code
 };
 
 // cos and sin of a (|a| < 2^40; else NaN): a = n pi / 2 + r, |r| <= pi / 4, and the power series to r^17 and
@@ -265,8 +266,8 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     if (key < 0) continue;
     double c, s;
     turn64((double)(a.w.pos ? a.w.pos[first_row + t] : key) * (double)a.freq[p], c, s);
-    s_turn[t][p][0] = (double)a.amp * c;
-    s_turn[t][p][1] = (double)a.amp * s;
+    s_turn[t][p][0] = a.amp * c;
+    s_turn[t][p][1] = a.amp * s;
   }
   __syncthreads();
   for (; row < first_row + TK && u < last; next(row, u)) {
@@ -1673,7 +1674,8 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
-// Values of a lane: 32 spread short rows over more workgroups; 1024 rows of 131072 with 8 best 53 us with 64, 61 with 32.
+// Values of a lane: 32 spread short rows over more workgroups; 1024 rows of 131072 with 8 best 53 us with 64, 61 with 32
+// (both with the maxima left in the sum).
 constexpr int kShortRow = 65536, kLongEl = 64;
 int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 256 * kLongEl - 1) / (256 * kLongEl); }
 
@@ -1687,13 +1689,13 @@ extern "C" {
 
 int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
                       const void* k, int64_t ldk, const void* v, int64_t ldv, int n_heads, int w_dtype, const void* q_weight,
-                      const void* k_weight, float eps, const float* freq, int n_rot, int layout, float amp, int o_dtype,
+                      const void* k_weight, float eps, const float* freq, int n_rot, int layout, double amp, int o_dtype,
                       void* q_out, int64_t ldqo) {
   if (const int rc = check_cache(C)) return rc;
   if (const int rc = check_window(W, *C)) return rc;
   if (!type_ok(dtype) || !q != !q_out || (q && !type_ok(o_dtype))) return MOE_E_ARG;
   if ((q_weight || k_weight) && (!type_ok(w_dtype) || !(eps > 0.0f) || !(eps < __builtin_inff()))) return MOE_E_ARG;
-  if (!(__builtin_fabsf(amp) < __builtin_inff()) || (layout != MOE_ROPE_HALF && layout != MOE_ROPE_PAIRS)) return MOE_E_ARG;
+  if (!(__builtin_fabs(amp) < __builtin_inff()) || (layout != MOE_ROPE_HALF && layout != MOE_ROPE_PAIRS)) return MOE_E_ARG;
   const int d = C->head_dim, n = W->n_tokens;
   if (n_rot < 0 || n_rot > d || n_rot % 2 || (q && (n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv))) return MOE_E_SHAPE;
   if (W->n_seqs == 0 || n == 0) return MOE_OK;

@@ -451,3 +451,11 @@ def test_logprobs_rows_alone_and_among_others():
     for r in (0, 17, 40):
         for a, b in zip(every, B.moe_token_logprobs(x[r:r + 1], tokens=t[r:r + 1], k=20, entropy=True)):
             assert torch.equal(a[r:r + 1], b)
+
+
+def test_append_keeps_an_amplitude_that_float32_does_not_hold():
+    """At angles of zero a turned value is the product with amp, of 64 bits, rounded once: bit for bit."""
+    p = Place([3, 2], [5, 0], d=64, cache=I8)
+    q, k, v = randn((p.rows, 256), F32, 31), randn((p.rows, p.n_kv * 64), F32, 32), randn((p.rows, p.n_kv * 64), F32, 33)
+    out = B.moe_window_append(p.cache, p.window, q, k, v, freq=torch.zeros(32, device=DEV), amp=1.2, q_out=torch.empty_like(q))
+    assert torch.equal(out[:p.n], (q[:p.n].double() * 1.2).float())
