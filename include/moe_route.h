@@ -408,9 +408,10 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
  * follows its lengths, pages, positions and masks. Offsets into the cache are 64-bit. The calls that take a workspace
  * need nothing in it beforehand and leave nothing for the next; calls that overlap need one each. A call of no tokens
  * or no sequences does nothing and succeeds. Problems that only the device sees are OR-ed into *window->err:
- * MOE_ERR_WINDOW: a sequence whose rows are not in ascending order within [0, n_tokens), whose window is longer than
- * max_window (attention only) or whose context is negative or does not fit its pages: the sequence is left out, its
- * rows as they were. MOE_ERR_PAGE: a page out of [0, n_pages): its keys are not written, and nobody sees them. */
+ * MOE_ERR_WINDOW: a sequence whose rows are not in ascending order within [0, n_tokens), that starts below an earlier
+ * entry of row_start (its rows could be another's too), whose window is longer than max_window (attention only) or whose
+ * context is negative or does not fit its pages: the sequence is left out, its rows as they were. MOE_ERR_PAGE: a page out
+ * of [0, n_pages): its keys are not written, and nobody sees them. */
 
 /* A layer's cache. Row (page p, head h, slot i) of k and of v starts p * page_stride + h * head_stride + i *
  * slot_stride elements from k and v and holds head_dim elements; strides are positive multiples of 16, slot_stride at most

@@ -33,25 +33,29 @@ struct Seq {
 __device__ __forceinline__ bool seq_ok(const WindowArgs& w, int start, int end, int ctx, int most) {
   return start >= 0 && start <= end && end <= w.n_tokens && end - start <= most && ctx >= 0 && ctx <= w.max_keys - (end - start);
 }
-// The sequence that a row is of (the last that starts at or before it: one without tokens is passed over); tokens = 0:
-// none, or one that is left out. Uniform over the wave: a lane looks at one sequence in 64, all it needs at once.
+// The sequence that a row is of; tokens = 0: none, or one that is left out. Uniform over the wave: a lane looks at one sequence
+// in 64, all it needs at once. The first entry past the row ends the only sequence that can have it: where the list
+// ascends, that is its sequence; where it goes back, a sequence that starts below an earlier entry is left out.
 __device__ __forceinline__ Seq seq_of(const WindowArgs& w, int row, int most) {
-  Seq q{0, 0, 0, 0};
+  const int lane = threadIdx.x & 63;
+  int largest = (int)0x80000000;   // of the starts before, this lane's
   for (int i = 0; i < w.n_seqs; i += 64) {
-    const int at = min(i + (int)(threadIdx.x & 63), w.n_seqs - 1);
+    const int at = min(i + lane, w.n_seqs - 1);
     const int start = w.row_start[at], end = w.row_start[at + 1], ctx = w.ctx_len[at];
-    const int n = __popcll(__ballot(start <= row && i + (int)(threadIdx.x & 63) < w.n_seqs));
-    if (n == 0) continue;   // of an ascending list: the ones before have it
-    q.s = i + n - 1;
-    q.start = __builtin_amdgcn_readlane(start, n - 1);
-    q.tokens = __builtin_amdgcn_readlane(end, n - 1);   // the end, so far
-    q.ctx = __builtin_amdgcn_readlane(ctx, n - 1);
+    const uint64_t past = __ballot(end > row);
+    if (past != 0) {
+      const int n = __builtin_ctzll(past);
+      const int first = __builtin_amdgcn_readlane(start, n), last = __builtin_amdgcn_readlane(end, n);
+      const int before = __builtin_amdgcn_readlane(ctx, n);
+      if (lane < n) largest = max(largest, start);
+      if (first > row || __ballot(largest > first) || !seq_ok(w, first, last, before, most)) break;
+      return Seq{i + n, first, last - first, before};
+    }
+    largest = max(largest, start);
   }
-  if (row >= q.tokens || !seq_ok(w, q.start, q.tokens, q.ctx, most)) return Seq{0, 0, 0, 0};
-  q.tokens -= q.start;
-  return q;
+  return Seq{0, 0, 0, 0};
 }
-// One workgroup of a launch looks at every sequence.
+// One workgroup of a launch looks at every sequence (a list that goes back has a sequence whose end is below its start).
 __device__ __forceinline__ void check_seqs(const WindowArgs& w, int most, int threads) {
   for (int i = threadIdx.x; i < w.n_seqs; i += threads)
     if (!seq_ok(w, w.row_start[i], w.row_start[i + 1], w.ctx_len[i], most)) atomicOr(w.err, MOE_ERR_WINDOW);
@@ -482,7 +486,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
   int* const s_end = (int*)(s_ring + (WIDE ? STAGES * STAGE : 0));   // [n_seqs]: items of the sequences up to this one
   const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quad = lane >> 4;
   const int G = a.n_heads / a.c.n_kv, d = a.c.d;
-  auto items_of = [&](int i, int start, int end, int ctx) {
+  auto items_of = [&](int start, int end, int ctx) {
     if (!seq_ok(a.w, start, end, ctx, a.w.max_window)) {
       if (blockIdx.x == 0) atomicOr(a.w.err, MOE_ERR_WINDOW);
       return 0;
@@ -497,6 +501,12 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     }
     return n;
   };
+  auto largest = [&](int n) {   // of the lanes before this one
+#pragma unroll
+    for (int o = 1; o < 64; o *= 2) n = max(n, __shfl_up(n, o));
+    n = __shfl_up(n, 1);
+    return lane > 0 ? n : (int)0x80000000;
+  };
   // items of the sequences up to each: in the lanes of every wave, or, of more than 64, in LDS
   int total = 0, my_start = 0, my_end = 0, my_ctx = 0, my_items = 0;
   const bool few = a.w.n_seqs <= 64;
@@ -504,14 +514,38 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     int n = 0;
     if (lane < a.w.n_seqs) {
       my_start = a.w.row_start[lane], my_end = a.w.row_start[lane + 1], my_ctx = a.w.ctx_len[lane];
-      n = items_of(lane, my_start, my_end, my_ctx);
+      n = items_of(my_start, my_end, my_ctx);
+    }
+    if (__ballot(my_end < my_start)) {   // the list goes back
+      const int earlier = largest(my_start);
+      if (earlier > my_start) n = 0;
     }
     my_items = scan(n);
     total = __builtin_amdgcn_readlane(my_items, 63);
   } else {
+    bool back = false;
+    int top = (int)0x80000000;   // the largest start of the sequences before these 256, from the first that goes back on
     for (int i0 = 0; i0 < a.w.n_seqs; i0 += 256) {
       const int i = i0 + tid;
-      int n = scan(i < a.w.n_seqs ? items_of(i, a.w.row_start[i], a.w.row_start[i + 1], a.w.ctx_len[i]) : 0);
+      int n = 0, start = top, end = top;
+      if (i < a.w.n_seqs) {
+        start = a.w.row_start[i], end = a.w.row_start[i + 1];
+        n = items_of(start, end, a.w.ctx_len[i]);
+      }
+      if (__syncthreads_or(end < start)) back = true;
+      if (back) {
+        int earlier = largest(start);
+        if (lane == 63) s_wave[wave] = max(earlier, start);
+        earlier = max(earlier, top);
+        __syncthreads();
+        for (int w = 0; w < 4; ++w) {
+          if (w < wave) earlier = max(earlier, s_wave[w]);
+          top = max(top, s_wave[w]);
+        }
+        if (earlier > start) n = 0;
+        __syncthreads();
+      }
+      n = scan(n);
       if (lane == 63) s_wave[wave] = n;
       __syncthreads();
       for (int w = 0; w < wave; ++w) n += s_wave[w];

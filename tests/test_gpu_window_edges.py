@@ -1,0 +1,73 @@
+"""The calls on windows at the edges of what they accept: lists of rows that go back, contexts next to the largest, scales, weights
+and values far apart. Tolerances are window_util.attend_ref's, or stand at the test."""
+import numpy as np
+import pytest
+import torch
+
+from moe_routed_expert_route_amd import binding as B
+from tests.test_gpu_window import randn
+from tests.window_util import BF16, DEV, F16, I8, Place, attend_ref, host
+
+pytestmark = pytest.mark.gpu
+
+
+def owned(starts, n):
+    """The rows of each sequence of a list of starts: none where its rows do not ascend within [0, n), or where it starts below
+    an earlier entry."""
+    out = []
+    for s in range(len(starts) - 1):
+        a, b = starts[s], starts[s + 1]
+        out.append(range(a, b) if 0 <= a <= b <= n and a >= max(starts[:s + 1]) else range(0))
+    return out
+
+
+def back(n_seqs, at):
+    """A list of n_seqs sequences of two rows each that falls back to row 1 after sequence `at`."""
+    starts = [2 * s for s in range(n_seqs + 1)]
+    starts[at + 1:] = [1 + 2 * s for s in range(n_seqs - at)]
+    return starts
+
+
+LISTS = [[0, 5, 3, 8], [100, 104, 0, 4], [4, 0, 8], [0, 3, 3, -2, 1, 4, 9], [-5, 2, 6], [0, 4, 1000, 8, 12], [7, 6, 5, 0], [0, 5, 3, 4, 5, 9],
+         back(64, 40), back(65, 62), back(200, 70), back(300, 255), back(600, 511), [0] + [2] * 300 + [1, 3], [9] * 100 + [0, 4] + [9, 12]]
+
+
+@pytest.mark.parametrize("dtype,cache,tokens", [(BF16, BF16, 1), (F16, I8, 1), (BF16, BF16, 12)])
+@pytest.mark.parametrize("starts", LISTS, ids=lambda s: f"{len(s) - 1}:{s[:6]}")
+def test_lists_of_rows_that_go_back(starts, dtype, cache, tokens):
+    """A sequence that starts below an earlier entry is left out by every call; the others are as without it, and no row but theirs is
+    written. `tokens` = 12: the same with windows of twelve times the rows (keys through LDS)."""
+    n = tokens * max(12, min(max(starts), 700))
+    starts = [tokens * a for a in starts]
+    rows = owned(starts, n)
+    assert any(len(r) != starts[s + 1] - starts[s] for s, r in enumerate(rows))
+    rng = np.random.default_rng(len(starts))
+    p = Place([len(r) for r in rows], rng.integers(100, 150, len(rows)), n_kv=1, d=64, cache=cache)
+    ints = lambda v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    p.start, p.n, p.rows = np.array(starts, dtype=np.int64), n, n
+    p.window = B.Window(ints(starts), p.window.ctx_len, p.window.pages, n, 8 if tokens == 1 else 64)
+    mine = torch.zeros(n, dtype=torch.bool)
+    for r in rows:
+        mine[r.start:r.stop] = True
+    pools = [t.clone() for t in (p.k, p.v)]
+    q, k, v = randn((n, 128), dtype, 1), randn((n, 64), dtype, 2), randn((n, 64), dtype, 3)
+    q_out = torch.full_like(q, 5.0)
+    B.moe_window_append(p.cache, p.window, q, k, v, q_out=q_out)
+    assert p.window.errors() == 128
+    assert torch.equal(q_out[mine], q[mine]) and (q_out[~mine] == 5.0).all()
+    written = torch.zeros(p.k.shape[0], p.k.shape[2], dtype=torch.bool)
+    for s, r in enumerate(rows):
+        for j in range(len(r)):
+            page, slot = p.key_at(s, p.ctx[s] + j)
+            written[page, slot] = True
+            if cache is not I8:
+                assert torch.equal(p.k[page, 0, slot], k[r.start + j]) and torch.equal(p.v[page, 0, slot], v[r.start + j])
+    for pool, old in zip((p.k, p.v), pools):
+        assert torch.equal(pool[:, 0].cpu()[~written], old[:, 0].cpu()[~written])
+    p.window.err.zero_()
+    out, lse = torch.full_like(q, 5.0), torch.full((n, 2), 5.0, device=DEV)
+    B.moe_window_attention(p.cache, p.window, q, 0.125, out=out, lse=lse)
+    assert p.window.errors() == 128
+    want, want_lse, tol, lse_tol = attend_ref(p, q, 2, 0.125)
+    assert (np.abs(host(out) - want)[mine] <= tol[mine]).all() and (np.abs(host(lse) - want_lse)[mine] <= lse_tol[mine]).all()
+    assert (out[~mine] == 5.0).all() and (lse[~mine] == 5.0).all()
