@@ -593,7 +593,9 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     const int part = rest % runs, head = rest / runs;   // of the cache
     const int key0 = part * run, len = min(run, keys - key0);
     const int steps = WIDE ? (len + 31) >> 5 : 2 * (len >> 8) + min(2, max(0, (len & 255) - 64 * wave + 31) >> 5);
-    auto key_of = [&](int step) { return WIDE ? key0 + step * 32 : key0 + (step >> 1) * 256 + wave * 64 + (step & 1) * 32; };
+    // a step's first key, from the run's first: past the run's end it still counts in 32 bits, the key itself may not
+    auto rel_of = [&](int step) { return WIDE ? step * 32 : (step >> 1) * 256 + wave * 64 + (step & 1) * 32; };
+    auto key_of = [&](int step) { return key0 + rel_of(step); };
 
     // rows: this lane's row of each tile of 16, its token's mask, and its part of Q^T
     uint64_t seen[NT];
@@ -635,9 +637,9 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     uint32_t at_lo = 0, at_hi = 0, sc_lo = 0, sc_hi = 0;
     uint64_t there = 0;
     auto pages = [&](int batch) {
-      const int key = key_of(batch + (lane >> 1)) + 16 * (lane & 1);
+      const int rel = rel_of(batch + (lane >> 1)) + 16 * (lane & 1), key = key0 + (rel < len ? rel : 0);
       int page = -1, slot = 0;
-      if (key < key0 + len) {
+      if (rel < len) {
         page = a.w.pages[s * a.w.ld_pages + key / a.c.page_size];
         slot = key % a.c.page_size;
         if (page < 0 || page >= a.c.n_pages) {
@@ -760,7 +762,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     // One step; `next` is called when the keys (true) and then the values (false) are used up.
     // Steps of the context whose pages are all there (`plain`) need no masks; a loop of their own keeps the masks' registers
     // out of it.
-    auto plain = [&](int step, const bool (&live)[2]) { return key_of(step) + 32 <= ctx && live[0] && live[1]; };
+    auto plain = [&](int step, const bool (&live)[2]) { return rel_of(step) + 32 <= ctx - key0 && live[0] && live[1]; };
     auto use = [&](auto checked, KV& kv, int step, const bool (&live)[2], auto next) {
       constexpr bool check = checked();
       const int key = key_of(step);

@@ -6,7 +6,7 @@ import torch
 
 from moe_routed_expert_route_amd import binding as B
 from tests.test_gpu_window import randn
-from tests.window_util import BF16, DEV, F16, I8, Place, attend_ref, host
+from tests.window_util import BF16, DEV, F16, HALF_STEP, I8, TINY, Place, attend_ref, host
 
 pytestmark = pytest.mark.gpu
 
@@ -71,3 +71,32 @@ def test_lists_of_rows_that_go_back(starts, dtype, cache, tokens):
     want, want_lse, tol, lse_tol = attend_ref(p, q, 2, 0.125)
     assert (np.abs(host(out) - want)[mine] <= tol[mine]).all() and (np.abs(host(lse) - want_lse)[mine] <= lse_tol[mine]).all()
     assert (out[~mine] == 5.0).all() and (lse[~mine] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype,tokens", [(BF16, 2), (F16, 40)])
+def test_contexts_next_to_the_largest(dtype, tokens):
+    """2^31 - 1064 keys, of which the table shares all but the last 984 in one page. A query of zeros takes the mean of the values:
+    sums of ones and zeros that float32 holds, so that the rounding of the quotient (2^-24 twice), of exp2 (1 for 0) and of the
+    output remain; a query of ones one key of the last page alone. Slots past the last key hold NaN."""
+    page, cols = 1024, (1 << 21) - 1
+    keys = page * cols - 40
+    k, v = (torch.zeros((2, 1, page, 16), dtype=dtype, device=DEV) for _ in range(2))
+    v[0, 0, ::4, ::2] = 1.0
+    k[1, 0, 100], v[1, 0, 100] = 30.0, 5.0
+    for pool in (k, v):
+        pool[1, 0, page - 40:] = float("nan")
+    table = torch.zeros((1, cols), dtype=torch.int32, device=DEV)
+    table[0, -1] = 1
+    ints = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    seen = torch.full((tokens,), -1, dtype=torch.int64, device=DEV)
+    w = B.Window(ints(0, tokens), ints(keys - tokens), table, tokens, tokens, seen=seen)
+    q = torch.zeros((tokens, 16), dtype=dtype, device=DEV)
+    q[1::2] = 1.0
+    lse = torch.zeros((tokens, 1), device=DEV)
+    out = B.moe_window_attention(B.KVCache(k, v), w, q, 1.0, lse=lse)
+    assert w.errors() == 0
+    out, lse = host(out), host(lse)[:, 0]
+    mean = (np.where(np.arange(16) % 2 == 0, (cols - 1) * (page // 4), 0) + 5.0) / keys
+    assert (np.abs(out[::2] - mean) <= mean * (HALF_STEP[dtype] + 2.0 ** -22) + TINY[dtype]).all()
+    assert (out[1::2] == 5.0).all()
+    assert (np.abs(lse[::2] - np.log(keys)) <= 2.0 ** -20 * 22).all() and (np.abs(lse[1::2] - 480.0) <= 480 * 2.0 ** -22).all()
