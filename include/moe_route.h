@@ -424,6 +424,7 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
 #define MOE_MAX_HEADS 1024
 #define MOE_MAX_SEQS 4096
 #define MOE_MAX_WINDOW 64         /* tokens of one sequence in moe_window_attention */
+#define MOE_MAX_JOIN 67108860     /* n_tokens x n_heads of moe_window_attention, where a sequence's keys can take several runs */
 typedef struct moe_kv_cache {
   int32_t dtype, n_pages, page_size, n_kv, head_dim;
   int64_t page_stride, head_stride, slot_stride;
@@ -483,7 +484,8 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
  * depend on what the other sequences of the call hold.
  * workspace: moe_window_attention_bytes, 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type or
  * stride, scale not finite, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
- * not a multiple of n_kv), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
+ * not a multiple of n_kv, n_tokens x n_heads past MOE_MAX_JOIN where max_pages * page_size is more than a run: 256 to 1024
+ * by the call's sizes), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
 size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, int n_heads);   /* host */
 int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
                          int n_heads, float scale, void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes);
@@ -499,8 +501,10 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
  * given <= 64, k <= 32 and k <= n. Sums of up to 2^14 terms in float32 (up to 64 one after the other), of those in 64 bits; a row's bits do not depend on the others.
  * workspace: moe_token_logprobs_bytes (0 for sizes that the call refuses), 16-byte aligned. Errors: MOE_E_ARG (null or
  * misaligned pointer, bad type, stride, count or scale, overlap), MOE_E_SHAPE (rows > MOE_MAX_ROWS, n not in
- * 1..MOE_MAX_VOCAB), MOE_E_WS. */
+ * 1..MOE_MAX_VOCAB, or more than MOE_MAX_PIECES pieces: rows x n / 8192, or / 16384 above 65536, n rounded up to a piece),
+ * MOE_E_WS. */
 #define MOE_MAX_VOCAB (1 << 22)
+#define MOE_MAX_PIECES 16777215
 size_t moe_token_logprobs_bytes(int rows, int n, int k);   /* host */
 int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, int rows, int n, float scale,
                        const int32_t* tokens, int given, float* logp, float* entropy, int k, int32_t* top_ids,

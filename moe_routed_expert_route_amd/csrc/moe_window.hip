@@ -1668,12 +1668,22 @@ int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
 
 constexpr int kAppendFew = 512;   // tokens whose heads are spread over several workgroups
 constexpr int kJoinWide = 1024;   // rows and heads that get four waves each
+
+// Attention's sizes beside those of the cache and the window, for the call and for the size of its workspace.
+int check_attend(const moe_kv_cache& c, const moe_window& w, int n_heads) {
+  if (n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % c.n_kv) return MOE_E_SHAPE;
+  if (w.n_seqs == 0 || w.n_tokens == 0) return MOE_OK;
+  if (w.max_window > MOE_MAX_WINDOW) return MOE_E_SHAPE;
+  if (max_runs(c, w, n_heads) > 1 && (int64_t)w.n_tokens * n_heads > MOE_MAX_JOIN) return MOE_E_SHAPE;
+  return MOE_OK;
+}
+static_assert(MOE_MAX_JOIN / 4 * 256ll <= kLaunchThreads && MOE_MAX_JOIN % 4 == 0 && kJoinWide * 256ll <= kLaunchThreads);
+
 template <typename T, bool I8, int HD, int NT, bool WIDE>
 int launch_attend(hipStream_t st, const AttendArgs& a) {
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1);
   const int64_t tiles = ((int64_t)a.w.max_window * (a.n_heads / a.c.n_kv) + ROWS - 1) / ROWS;
-  const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;
-  if (items > 0x7FFFFFFF) return MOE_E_SHAPE;
+  const int64_t items = tiles * a.max_runs * a.c.n_kv * a.w.n_seqs;   // at most 2048 * 64 * 4096
   const int grid = (int)std::min<int64_t>(256 * kAttendWaves(HD), (items + 7) & ~7ll);
   const int lds = (WIDE ? ring_bytes(HD, I8) : 0) + 4 * a.w.n_seqs;
   const auto kern = k_attend<T, I8, HD, NT, WIDE>;
@@ -1694,7 +1704,6 @@ int launch_attend(hipStream_t st, const AttendArgs& a) {
 template <typename T>
 int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   const int rows = a.w.max_window * (a.n_heads / a.c.n_kv);
-  if ((int64_t)a.w.n_tokens * a.n_heads * 256 > kLaunchThreads) return MOE_E_SHAPE;
   auto tiles = [&](auto i, auto hd) {
     constexpr bool I8 = decltype(i)::value;
     constexpr int HD = decltype(hd)::value;
@@ -1714,6 +1723,12 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
 // (both with the maxima left in the sum).
 constexpr int kShortRow = 65536, kLongEl = 64;
 int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 256 * kLongEl - 1) / (256 * kLongEl); }
+// The sizes of log probabilities, for the call and for the size of its workspace.
+int check_scores(int rows, int n) {
+  if (rows > MOE_MAX_ROWS || n < 1 || n > MOE_MAX_VOCAB || (int64_t)rows * pieces_of(n) > MOE_MAX_PIECES) return MOE_E_SHAPE;
+  return MOE_OK;
+}
+static_assert(MOE_MAX_PIECES * 256ll <= kLaunchThreads);
 
 }  // namespace moe
 
@@ -1779,10 +1794,8 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
 }
 
 size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, int n_heads) {
-  if (check_cache(C) || check_window(W, *C) || n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv ||
-      W->max_window > MOE_MAX_WINDOW)
-    return 0;
-  const size_t runs = max_runs(*C, *W, n_heads);
+  if (check_cache(C) || check_window(W, *C) || check_attend(*C, *W, n_heads)) return 0;
+  const size_t runs = W->n_seqs && W->n_tokens ? max_runs(*C, *W, n_heads) : 1;
   return runs == 1 ? 16 : ((size_t)W->n_tokens * n_heads * runs * (C->head_dim + 2) * 4 + 15) & ~(size_t)15;
 }
 
@@ -1792,10 +1805,9 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
   if (const int rc = check_window(W, *C)) return rc;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_E_ARG;
   if ((C->dtype != MOE_I8 && C->dtype != dtype) || !(__builtin_fabsf(scale) < __builtin_inff())) return MOE_E_ARG;
-  if (n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv) return MOE_E_SHAPE;
+  if (const int rc = check_attend(*C, *W, n_heads)) return rc;
   const int n = W->n_tokens;
   if (W->n_seqs == 0 || n == 0) return MOE_OK;
-  if (W->max_window > MOE_MAX_WINDOW) return MOE_E_SHAPE;
   const int64_t wide = (int64_t)n_heads * C->head_dim;
   if (!q || !out || bad_stride(ldq, wide, n) || bad_stride(ldo, wide, n) || !aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4))
     return MOE_E_ARG;
@@ -1823,7 +1835,7 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
 }
 
 size_t moe_token_logprobs_bytes(int rows, int n, int k) {
-  if (rows < 1 || rows > MOE_MAX_ROWS || n < 1 || n > MOE_MAX_VOCAB || k < 0 || k > 32 || k > n) return 0;
+  if (rows < 1 || k < 0 || k > 32 || k > n || check_scores(rows, n)) return 0;
   return (size_t)rows * pieces_of(n) * (16 + (k ? 8 * kKept : 0));
 }
 
@@ -1832,7 +1844,7 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
                        float* top_logp, void* workspace, size_t ws_bytes) {
   if (!type_ok(dtype) || rows < 0 || given < 0 || given > 64 || k < 0 || k > 32 || !(scale > 0.0f) || !(scale < __builtin_inff()))
     return MOE_E_ARG;
-  if (rows > MOE_MAX_ROWS || n < 1 || n > MOE_MAX_VOCAB) return MOE_E_SHAPE;
+  if (const int rc = check_scores(rows, n)) return rc;
   if (k > n) return MOE_E_ARG;
   if (rows == 0) return MOE_OK;
   if (!logits || bad_stride(ld, n, rows) || !tokens != !given || !logp != !given || !top_ids != !k || !top_logp != !k ||
@@ -1854,7 +1866,6 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
   }
   const int pieces = pieces_of(n);
   const int64_t blocks = (int64_t)rows * pieces;
-  if (blocks * 256 > kLaunchThreads) return MOE_E_SHAPE;
   float* const stats = (float*)workspace;
   const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, stats, (uint64_t*)(stats + 4 * blocks), ld, n, given, k, pieces, scale};
   with_type(dtype, [&](auto t) {
