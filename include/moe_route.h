@@ -418,7 +418,7 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
  * 2^24, of any nesting order, and rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k and v are
  * 16-byte aligned.
  * dtype MOE_BF16, MOE_F16, or MOE_I8: i8 rows, one scale a row at [(p * n_kv + h) * page_size + i] of k_scale and v_scale
- * (NULL for the others). page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple of 16 up to 256; n_kv up to
+ * (NULL for the others), outside of the rows' span. page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple of 16 up to 256; n_kv up to
  * MOE_MAX_HEADS. Host struct holding device pointers. */
 #define MOE_MAX_PAGE 65536
 #define MOE_MAX_HEADS 1024

@@ -1600,7 +1600,12 @@ int check_cache(const moe_kv_cache* c) {
   if (c->dtype == MOE_I8) {
     if (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)) return MOE_E_ARG;
     const int64_t n = (int64_t)c->n_pages * c->n_kv * c->page_size;
-    if (overlap(rows_of(c->k_scale, 1, n, n, 4), rows_of(c->v_scale, 1, n, n, 4))) return MOE_E_ARG;
+    const int64_t bytes = cache_extent(*c).bytes;
+    const Rows apart[] = {rows_of(c->k_scale, 1, n, n, 4), rows_of(c->v_scale, 1, n, n, 4), rows_of(c->k, 1, bytes, bytes, 1),
+                          rows_of(c->v, 1, bytes, bytes, 1)};
+    for (int i = 1; i < 4; ++i)   // k and v may share their span (cache_extent has looked at their rows)
+      for (int j = 0; j < std::min(i, 2); ++j)
+        if (overlap(apart[i], apart[j])) return MOE_E_ARG;
   } else if (c->k_scale || c->v_scale) {
     return MOE_E_ARG;
   }

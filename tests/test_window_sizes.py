@@ -1,4 +1,4 @@
-"""The sizes at which the calls on windows begin to refuse, and the workspaces that they name up to there. On the host alone, with
+"""Operands over each other in a cache, and the sizes at which the calls on windows begin to refuse, and the workspaces that they name up to there. On the host alone, with
 pointers that are fakes: a call that passes its checks ends in the launch's own error where there is no GPU."""
 import ctypes
 import os
@@ -6,7 +6,7 @@ import os
 import pytest
 
 from moe_routed_expert_route_amd import binding as B
-from tests.test_window_refusals import CACHE, HIP, OK, SCORES, SHAPE, WINDOW, no_gpu, over_cache
+from tests.test_window_refusals import ARG, CACHE, HIP, I8, OK, P, SCORES, SHAPE, WINDOW, no_gpu, over_cache
 
 pytestmark = pytest.mark.skipif(not os.path.exists(B.LIB_PATH), reason="library not built")
 
@@ -55,3 +55,18 @@ def test_pieces_of_log_probabilities(rows, n, refused):
 @no_gpu
 def test_pieces_of_log_probabilities_reach_the_launch():
     assert B.lib().moe_token_logprobs(None, *dict(SCORES, rows=4194303, n=32768, ld=32768, ws_bytes=1 << 40).values()) == HIP
+
+
+# the rows of k and of v: 10 pages x 4096 bytes; a scale array: 640 x 4 bytes
+@pytest.mark.parametrize("name", ["moe_window_append", "moe_window_attention"])
+@pytest.mark.parametrize("change", [dict(k_scale=P[1]), dict(k_scale=P[2] + 40956), dict(v_scale=P[1] + 4096), dict(v_scale=P[2] - 2556),
+                                    dict(k_scale=P[1] + 8 + 4096, v=P[1] + 4096, page_stride=8192)])
+def test_scales_over_the_rows_of_a_cache(name, change):
+    assert over_cache(name, cache=dict(I8, **change)) == ARG
+
+
+@no_gpu
+@pytest.mark.parametrize("change", [dict(k_scale=P[1] + 40960), dict(v_scale=P[1] - 2560), dict(k_scale=P[2] - 2560, v_scale=P[2] + 40960)])
+def test_scales_beside_the_rows_of_a_cache(change):
+    for name in ("moe_window_append", "moe_window_attention"):
+        assert over_cache(name, cache=dict(I8, **change)) == HIP
