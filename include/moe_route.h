@@ -474,6 +474,7 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
 /* Attention of the window's queries over the cache, the window's own keys (appended before) among them: per row and
  * head, over the keys that the row sees,
  *   s_i = scale * q . k_i,  out = sum exp(s_i) v_i / sum exp(s_i),  lse = log sum exp(s_i)   (lse NULL: not wanted).
+ * |scale| <= 2^127; scores are float32 numbers (a row with one past their range gets numbers that mean nothing).
  * A row that sees nothing gets out = 0 and lse = -infinity. Keys that a row does not see, and slots past the last key, count
  * for nothing whatever they hold (infinities and NaN too). Head h reads the cache's head h / (n_heads / n_kv).
  * q, out [n_tokens][ldq], [ldo] in `dtype`: the cache's type, or MOE_BF16 or MOE_F16 over an i8 cache; lse float32
@@ -483,7 +484,7 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
  * runs whose length depends on its own key count and on the call's sizes (n_seqs, max_window, heads): a token's bits do not
  * depend on what the other sequences of the call hold.
  * workspace: moe_window_attention_bytes, 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type or
- * stride, scale not finite, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
+ * stride, scale past 2^127 or NaN, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
  * not a multiple of n_kv, n_tokens x n_heads past MOE_MAX_JOIN where max_pages * page_size is more than a run: 256 to 1024
  * by the call's sizes), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
 size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, int n_heads);   /* host */
@@ -495,7 +496,7 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
  *   logp[r][j] = log p(tokens[r][j]) (-infinity for an id out of [0, n): no token);  entropy[r] = -sum p log p;
  *   top_ids[r], top_logp[r] = the k tokens of the largest logits, largest first, ties to the lower id, and their log p.
  * A logit of -infinity or NaN masks its token: p = 0, log p = -infinity, and it comes after every unmasked one in the order, lowest
- * id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. scale > 0.
+ * id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. 0 < scale <= 2^127.
  * Each output is written when its pointer is not NULL (tokens and logp, given > 0: all or none; top_ids and top_logp, k > 0:
  * all or none; at least one output). logits [rows][ld] in `dtype`, tokens int32 [rows][given]. n <= MOE_MAX_VOCAB,
  * given <= 64, k <= 32 and k <= n. Sums of up to 2^14 terms in float32 (up to 64 one after the other), of those in 64 bits; a row's bits do not depend on the others.

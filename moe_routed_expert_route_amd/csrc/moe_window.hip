@@ -1552,6 +1552,8 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
 
 // ------------------------------------------------------------------ host checks -------------
 
+constexpr float kMaxScale = 0x1p127f;   // times log2(e), the unit of the exponentials, still a float32
+
 // Rows of a cache in memory, in bytes from k: whether they lie apart, and the bytes from the first to the last.
 struct Extent {
   bool ok;
@@ -1809,7 +1811,7 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
   if (const int rc = check_cache(C)) return rc;
   if (const int rc = check_window(W, *C)) return rc;
   if (dtype != MOE_BF16 && dtype != MOE_F16) return MOE_E_ARG;
-  if ((C->dtype != MOE_I8 && C->dtype != dtype) || !(__builtin_fabsf(scale) < __builtin_inff())) return MOE_E_ARG;
+  if ((C->dtype != MOE_I8 && C->dtype != dtype) || !(__builtin_fabsf(scale) <= kMaxScale)) return MOE_E_ARG;
   if (const int rc = check_attend(*C, *W, n_heads)) return rc;
   const int n = W->n_tokens;
   if (W->n_seqs == 0 || n == 0) return MOE_OK;
@@ -1847,7 +1849,7 @@ size_t moe_token_logprobs_bytes(int rows, int n, int k) {
 int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, int rows, int n, float scale,
                        const int32_t* tokens, int given, float* logp, float* entropy, int k, int32_t* top_ids,
                        float* top_logp, void* workspace, size_t ws_bytes) {
-  if (!type_ok(dtype) || rows < 0 || given < 0 || given > 64 || k < 0 || k > 32 || !(scale > 0.0f) || !(scale < __builtin_inff()))
+  if (!type_ok(dtype) || rows < 0 || given < 0 || given > 64 || k < 0 || k > 32 || !(scale > 0.0f) || !(scale <= kMaxScale))
     return MOE_E_ARG;
   if (const int rc = check_scores(rows, n)) return rc;
   if (k > n) return MOE_E_ARG;

@@ -6,7 +6,7 @@ import torch
 
 from moe_routed_expert_route_amd import binding as B
 from tests.test_gpu_window import randn
-from tests.window_util import BF16, DEV, F16, HALF_STEP, I8, TINY, Place, attend_ref, host
+from tests.window_util import BF16, DEV, F16, F32, HALF_STEP, I8, TINY, Place, attend_ref, host
 
 pytestmark = pytest.mark.gpu
 
@@ -100,3 +100,36 @@ def test_contexts_next_to_the_largest(dtype, tokens):
     assert (np.abs(out[::2] - mean) <= mean * (HALF_STEP[dtype] + 2.0 ** -22) + TINY[dtype]).all()
     assert (out[1::2] == 5.0).all()
     assert (np.abs(lse[::2] - np.log(keys)) <= 2.0 ** -20 * 22).all() and (np.abs(lse[1::2] - 480.0) <= 480 * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+def test_log_probabilities_of_the_largest_scale(dtype):
+    """Logits apart by 2^-14 and more: a score of 0 and of less than -2^112, so probabilities of one, of a half where two are largest,
+    and of none."""
+    x = torch.tensor([[1.0, 2.0, 2.0 ** -14, -1.0], [0.5, 0.5, 0.0, -0.5], [-1.0, -2.0, -3.0, -4.0]], device=DEV).to(dtype)
+    logp, h, ids, top = B.moe_token_logprobs(x, tokens=torch.tensor([[1, 0], [1, 2], [0, 3]], dtype=torch.int32, device=DEV), k=2, entropy=True,
+                                             scale=2.0 ** 127)
+    assert ids.tolist() == [[1, 0], [0, 1], [0, 1]]
+    half = -float(np.log(2))
+    assert logp[0, 0] == 0 and logp[2, 0] == 0 and abs(float(logp[1, 0]) - half) < 2.0 ** -22
+    assert (logp[:, 1] < -2.0 ** 112).all() and h[0] == 0 and abs(float(h[1]) + half) < 2.0 ** -22 and h[2] == 0
+    assert top[0, 0] == 0 and abs(float(top[1, 1]) - half) < 2.0 ** -22 and top[2, 1] < -2.0 ** 112
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tokens", [2, 40])
+def test_attention_of_the_largest_scale(tokens, dtype):
+    """One key of 2^-14 times a query of 2^-8: a score of 2^105 beside zeros, which alone counts; a query of zeros beside it."""
+    p = Place([tokens], [50], n_kv=1, d=64, cache=dtype)
+    p.k.zero_()
+    for i in range(50 + tokens):
+        page, slot = p.key_at(0, i)
+        p.k[page, 0, slot, 0] = 2.0 ** -14 if i == 17 else 0.0
+    q = torch.zeros((tokens, 64), dtype=dtype, device=DEV)
+    q[:, 0] = torch.where(torch.arange(tokens, device=DEV) % 2 == 0, 2.0 ** -8, 0.0)
+    lse = torch.zeros((tokens, 1), device=DEV)
+    out = B.moe_window_attention(p.cache, p.window, q, 2.0 ** 127, lse=lse)
+    page, slot = p.key_at(0, 17)
+    assert torch.equal(out[::2], p.v[page, 0, slot].expand_as(out[::2])) and (lse[::2, 0] == 2.0 ** 105).all()
+    want, want_lse, tol, lse_tol = attend_ref(p, q, 1, 2.0 ** 127)
+    assert (np.abs(host(out) - want)[1::2] <= tol[1::2]).all() and (np.abs(host(lse) - want_lse)[1::2] <= lse_tol[1::2]).all()

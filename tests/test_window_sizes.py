@@ -4,6 +4,7 @@ import ctypes
 import os
 
 import pytest
+import torch
 
 from moe_routed_expert_route_amd import binding as B
 from tests.test_window_refusals import ARG, CACHE, HIP, I8, OK, P, SCORES, SHAPE, WINDOW, no_gpu, over_cache
@@ -70,3 +71,14 @@ def test_scales_over_the_rows_of_a_cache(name, change):
 def test_scales_beside_the_rows_of_a_cache(change):
     for name in ("moe_window_append", "moe_window_attention"):
         assert over_cache(name, cache=dict(I8, **change)) == HIP
+
+
+@pytest.mark.parametrize("scale,ok", [(2.0 ** 127, True), (2.0 ** 127 * (1 + 2.0 ** -23), False), (2.4e38, False), (3.4e38, False), (1e-45, True)])
+def test_largest_scales(scale, ok):
+    """Above 2^127 the unit of the exponentials, scale times log2(e), need not be a float32."""
+    calls = [lambda: over_cache("moe_window_attention", scale=scale), lambda: over_cache("moe_window_attention", scale=-scale),
+             lambda: B.lib().moe_token_logprobs(None, *dict(SCORES, scale=scale).values())]
+    if not ok:
+        assert [c() for c in calls] == [ARG] * 3
+    elif not torch.cuda.is_available():
+        assert [c() for c in calls] == [HIP] * 3
