@@ -1354,8 +1354,18 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
   const bool none = most <= kMasked;
   const float top = none ? 0.0f : value_of(most);
 
+  // Infinity counts as the largest number. (In 16 bits that number is infinity, which the next step takes out.)
+  if constexpr (sizeof(T) == 4) {
+    if (top == 0x1.fffffep127f) {
+#pragma unroll
+      for (int p = 0; p < PIECES; ++p)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) raw[p].w[e] = raw[p].w[e] == 0x7F800000u ? 0x7F7FFFFFu : raw[p].w[e];
+    }
+  }
+
   // A row that is sure of a token has a sum of 1 and little more, and that little is what its entropy hangs on: the lanes
-  // that have the maximum take it out (any number of times; +0 for -0 stays, and infinity, with which nothing is lost), and
+  // that have the maximum take it out (any number of times; +0 for -0 stays, with which nothing is lost), and
   // the join counts the maxima. Without branches or masks, which cost registers: 53 us for the 1024 x 131072 without
   // this, 62 with it, 82 by a second pass over the lane's values.
   if (mine == top && !none) {

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from moe_routed_expert_route_amd import binding as B
-from tests.test_gpu_window import randn
+from tests.test_gpu_window import check_logprobs, randn
 from tests.window_util import BF16, DEV, F16, F32, HALF_STEP, I8, TINY, Place, attend_ref, host
 
 pytestmark = pytest.mark.gpu
@@ -133,3 +133,15 @@ def test_attention_of_the_largest_scale(tokens, dtype):
     assert torch.equal(out[::2], p.v[page, 0, slot].expand_as(out[::2])) and (lse[::2, 0] == 2.0 ** 105).all()
     want, want_lse, tol, lse_tol = attend_ref(p, q, 1, 2.0 ** 127)
     assert (np.abs(host(out) - want)[1::2] <= tol[1::2]).all() and (np.abs(host(lse) - want_lse)[1::2] <= lse_tol[1::2]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("scale", [1e-38, 2.5e-37])
+@pytest.mark.parametrize("n", [12, 5000, 70000])
+def test_log_probabilities_of_infinities_under_a_small_scale(n, scale, dtype):
+    """Infinity counts as the largest float32, also where the scale makes a score of a few units of it."""
+    x = randn((6, n), F32, n, 4, scale=1e38).clamp(-3e38, 3e38)
+    x[0, 3] = x[1, 2] = x[1, n - 1] = x[1, n // 2] = x[3, 5] = float("inf")
+    x[2, 7], x[3, 1], x[4, 4], x[4, 0] = 3.4028234663852886e38, 3.4028234663852886e38, float("nan"), float("-inf")
+    x[5, ::2] = float("inf")
+    check_logprobs(x.to(dtype), torch.tensor([[3, 1, 5, 7, 0, n - 1]] * 6, dtype=torch.int32, device=DEV), min(n, 20), scale)
