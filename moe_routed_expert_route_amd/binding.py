@@ -709,6 +709,8 @@ def moe_window_append(cache: KVCache, window: Window, q, k, v, freq=None, layout
         o_type = _DTYPE[q_out.dtype]
     elif q_out is not None or q_weight is not None:
         raise ValueError(f"{what}: q_out and q_weight without q")
+    if layout not in (ROPE_HALF, ROPE_PAIRS):
+        raise ValueError(f"{what}: layout {layout}")
     if freq is not None:
         n_rot = 2 * freq.shape[0]
         _packed(what, "freq", freq, (n_rot // 2,), torch.float32, dev)

@@ -145,3 +145,13 @@ def test_log_probabilities_of_infinities_under_a_small_scale(n, scale, dtype):
     x[2, 7], x[3, 1], x[4, 4], x[4, 0] = 3.4028234663852886e38, 3.4028234663852886e38, float("nan"), float("-inf")
     x[5, ::2] = float("inf")
     check_logprobs(x.to(dtype), torch.tensor([[3, 1, 5, 7, 0, n - 1]] * 6, dtype=torch.int32, device=DEV), min(n, 20), scale)
+
+
+@pytest.mark.parametrize("layout", [0, 3, (1 << 32) + 1, -(1 << 32) + 2])
+def test_layouts_that_are_none(layout):
+    p = Place([2], [3], d=64)
+    q, k, v = (randn((2, 128), BF16, i) for i in range(3))
+    k0 = p.k.clone()
+    with pytest.raises(ValueError, match="layout"):
+        B.moe_window_append(p.cache, p.window, q, k, v, freq=torch.ones(32, device=DEV), layout=layout)
+    assert torch.equal(p.k, k0)
