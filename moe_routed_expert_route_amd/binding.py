@@ -607,6 +607,7 @@ def moe_matmul_i8(a, sa, b, sb, c=None, dtype=torch.float32, accumulate=False, s
 
 I8 = 4                                   # moe_kv_cache.dtype of int8 rows
 ROPE_HALF, ROPE_PAIRS = 1, 2             # moe_rope
+MAX_WINDOW = 64                          # tokens of one sequence in moe_window_attention
 _CACHE_DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.int8: I8}
 
 
@@ -647,9 +648,10 @@ class KVCache:
 
 class Window:
     """The tokens of one call: row_start int32 [n_seqs + 1], ctx_len int32 [n_seqs], pages int32 [n_seqs, max_pages] (any
-    row stride), the number of rows, the most tokens of one sequence (as many as there are rows, if not given),
-    pos int32 [n_tokens] (rotary positions, if not the keys' indices) and seen int64 [n_tokens] (the tokens of its
-    window that each sees, as bits, if not itself and those before it). The tensors are read when a call runs."""
+    row stride), the number of rows, the most tokens of one sequence (attention's tiles of rows go by it; if not given, as
+    many as there are rows, of several sequences 64 at most, which is what attention takes), pos int32 [n_tokens]
+    (rotary positions, if not the keys' indices) and seen int64 [n_tokens] (the tokens of its window that each sees, as
+    bits, if not itself and those before it). The tensors are read when a call runs."""
 
     def __init__(self, row_start, ctx_len, pages, n_tokens, max_window=None, pos=None, seen=None):
         what = "Window"
@@ -663,7 +665,8 @@ class Window:
             _packed(what, "pos", pos, (n_tokens,), torch.int32, self.device)
         if seen is not None:
             _packed(what, "seen", seen, (n_tokens,), torch.int64, self.device)
-        max_window = max(1, n_tokens) if max_window is None else max_window
+        if max_window is None:
+            max_window = max(1, n_tokens if n == 1 else min(n_tokens, MAX_WINDOW))
         if not 0 < max_window < 1 << 31:
             raise ValueError(f"{what}: max_window {max_window}")
         self.row_start, self.ctx_len, self.pages, self.pos, self.seen = row_start, ctx_len, pages, pos, seen

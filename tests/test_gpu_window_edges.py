@@ -155,3 +155,31 @@ def test_layouts_that_are_none(layout):
     with pytest.raises(ValueError, match="layout"):
         B.moe_window_append(p.cache, p.window, q, k, v, freq=torch.ones(32, device=DEV), layout=layout)
     assert torch.equal(p.k, k0)
+
+
+@pytest.mark.parametrize("tokens", [[1] * 65, [1] * 300, [64, 1, 40], [3] * 30])
+def test_windows_of_a_length_that_is_not_given(tokens):
+    """Batches of more rows than a window may have, without a longest window."""
+    p = Place(tokens, [5 * (s % 40) for s in range(len(tokens))], n_kv=1, d=64)
+    p.window = B.Window(p.window.row_start, p.window.ctx_len, p.window.pages, p.rows)
+    q = randn((p.rows, 256), BF16, 2)
+    out = B.moe_window_attention(p.cache, p.window, q, 0.125)
+    want, _, tol, _ = attend_ref(p, q, 4, 0.125)
+    assert (np.abs(host(out) - want) <= tol).all() and p.window.errors() == 0
+
+
+def test_a_window_that_is_too_long_without_its_length():
+    """Alone it is refused, among others left out and flagged; append takes windows of any length."""
+    for tokens in ([65], [65, 2]):
+        p = Place(tokens, [0] * len(tokens), n_kv=1, d=64)
+        w = B.Window(p.window.row_start, p.window.ctx_len, p.window.pages, p.rows)
+        q = randn((p.rows, 64), BF16, 2)
+        B.moe_window_append(p.cache, w, q, q, q)
+        assert w.errors() == 0
+        out = torch.full_like(q, 5.0)
+        if len(tokens) == 1:
+            with pytest.raises(RuntimeError):
+                B.moe_window_attention(p.cache, w, q, 0.125, out=out)
+        else:
+            B.moe_window_attention(p.cache, w, q, 0.125, out=out)
+            assert w.errors() == 128 and (out[:65] == 5.0).all() and not (out[65:] == 5.0).all()
