@@ -435,7 +435,7 @@ typedef struct moe_kv_cache {
 } moe_kv_cache;
 
 /* The tokens of one call. Sequence s has rows row_start[s] .. row_start[s + 1] - 1 of the call's n_tokens rows (rows of
- * no sequence, such as padding behind the last, are neither read nor written) and ctx_len[s] keys before them in its
+ * no sequence, such as padding behind the last, are not written, and what they hold counts for nothing) and ctx_len[s] keys before them in its
  * pages: key i is slot i % page_size of page pages[s * ld_pages + i / page_size], and the window's token j is key
  * ctx_len[s] + j. Pages may be shared between sequences where nothing is written to them. max_pages <= ld_pages columns are
  * read at most, max_pages * page_size < 2^31. max_window: the most tokens of a sequence. pos (NULL: the token's key

@@ -183,3 +183,24 @@ def test_a_window_that_is_too_long_without_its_length():
         else:
             B.moe_window_attention(p.cache, w, q, 0.125, out=out)
             assert w.errors() == 128 and (out[:65] == 5.0).all() and not (out[65:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F16, I8)])
+@pytest.mark.parametrize("tokens", [[3, 0, 2], [300, 20, 400]])
+def test_rows_of_no_sequence_count_for_nothing(tokens, dtype, cache):
+    """NaN and infinities in padded rows behind the last sequence, which append and attention may read: the same bits everywhere, and
+    the padded rows of the outputs as they were."""
+    got = []
+    for bad in (0.0, float("nan"), float("inf")):
+        p = Place(tokens, [9, 4, 0], d=64, cache=cache, pad=7)
+        q, k, v = randn((p.rows, 256), dtype, 1), randn((p.rows, 128), dtype, 2), randn((p.rows, 128), dtype, 3)
+        q[p.n:], k[p.n:], v[p.n:] = bad, bad, bad
+        q_out, out, lse = torch.full_like(q, 5.0), torch.full_like(q, 5.0), torch.full((p.rows, 4), 5.0, device=DEV)
+        w = torch.ones(64, dtype=dtype, device=DEV)
+        B.moe_window_append(p.cache, p.window, q, k, v, freq=torch.ones(16, device=DEV), q_weight=w, k_weight=w, q_out=q_out)
+        if max(tokens) <= 64:
+            B.moe_window_attention(p.cache, p.window, q, 0.125, out=out, lse=lse)
+        assert p.window.errors() == 0 and all((t[p.n:] == 5.0).all() for t in (q_out, out, lse))
+        got.append([q_out, out, lse, p.k, p.v] + ([p.k_scale, p.v_scale] if cache is I8 else []))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
