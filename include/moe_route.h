@@ -478,8 +478,9 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
  * A row that sees nothing gets out = 0 and lse = -infinity. Keys that a row does not see, and slots past the last key, count
  * for nothing whatever they hold (infinities and NaN too). Head h reads the cache's head h / (n_heads / n_kv).
  * q, out [n_tokens][ldq], [ldo] in `dtype`: the cache's type, or MOE_BF16 or MOE_F16 over an i8 cache; lse float32
- * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max), times the value's scale over an i8
- * cache, is rounded to `dtype` in front of its product, and the sum below is of the unrounded ones.
+ * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max) is rounded to `dtype` in front of its product,
+ * over an i8 cache, times the value's scale, to 16 bits of float32's range (of bfloat16 queries of more than 32 rows a
+ * cache head, max_window x n_heads / n_kv, to bfloat16). The sum below is of the unrounded ones.
  * A value of a window's key that is not finite reaches the rows that see it, and no others. A sequence's keys are summed in
  * runs whose length depends on its own key count and on the call's sizes (n_seqs, max_window, heads): a token's bits do not
  * depend on what the other sequences of the call hold.

@@ -473,6 +473,14 @@ template <typename T, bool I8, int HD, int NT, bool WIDE>
 __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) {
   using M = Mat<T>;
   using KV = Keys<I8, HD>;
+  // In front of V a weight is rounded to T, which costs bits: the error of bfloat16 outputs of 1 x 4 tokens over 131072 keys against
+  // 64 bits is 2.1e-3 instead of 1.7e-3. (Two parts of 8 bits each, two products: as fast there, but 8 x 64 bf16 258 us
+  // instead of 219.) Over an int8 cache a weight has its value's scale in it, of float32's range and any size next to the
+  // others', and is bfloat16 whatever T: float16 under a common power of two lost the rows whose scales are small. It is
+  // in two parts there (64 x 4 of 8192: 2.4e-3 and 1.7e-3, 136 us and 137), but for bfloat16 queries of many rows, which
+  // the products bound (8 x 64: 261 us, in two parts 290 to 303).
+  using MV = Mat<std::conditional_t<I8, bf16_t, T>>;
+  constexpr bool PARTS = I8 && (!WIDE || std::is_same_v<T, f16_t>);
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1), KS = HD / 32, E0 = HD < 128 ? 4 : 8, NH = HD < 128 ? 1 : HD / 128, DT = E0 * NH;
   constexpr int SIZE = I8 ? 1 : 2, STRIDE = HD + 4;
   __shared__ float s_m[4][WIDE ? 1 : ROWS], s_l[4][WIDE ? 1 : ROWS], s_o[4][WIDE ? 1 : 16 * STRIDE];
@@ -622,7 +630,6 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     }
     if constexpr (Q_LDS) __syncthreads();
     float m[NT], l[NT];
-    int e_ref = -127;   // of an i8 cache's scales: weights are times scale / 2^e_ref
     f32x4 acc[NT][DT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -851,36 +858,21 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
         top[n] = max4(x);
         grows |= top[n] > m[n];
       }
-      int e = e_ref;
-      float unit = 1.0f;
-      if constexpr (I8 && M::kBoost > 0.0f) {
-        float most = 0.0f;
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) most = __builtin_fmaxf(most, kv.vs[t][i] < __builtin_inff() ? kv.vs[t][i] : 0.0f);
-        e = max(e, (int)(__builtin_bit_cast(uint32_t, max4(most)) >> 23) - 127);
-        e = __builtin_amdgcn_readfirstlane(e);
-        grows |= e > e_ref;
-        unit = __builtin_ldexpf(1.0f, -e);
-      }
       if (__ballot(grows)) {
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
           const float ref = top[n] == -__builtin_inff() ? 0.0f : top[n];
           const float keep = __builtin_amdgcn_exp2f((m[n] - ref) * c);
           l[n] *= keep;
-          const float keep_o = I8 && M::kBoost > 0.0f ? __builtin_ldexpf(keep, e_ref - e) : keep;
 #pragma unroll
-          for (int x = 0; x < DT; ++x) acc[n][x] *= keep_o;
+          for (int x = 0; x < DT; ++x) acc[n][x] *= keep;
           m[n] = top[n];
         }
-        e_ref = e;
       }
-      u32x4 w[NT];
+      u32x4 w[NT], w_lo[PARTS ? NT : 1];
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float mc = (m[n] == -__builtin_inff() ? 0.0f : m[n]) * c - M::kBoost;
+        const float mc = (m[n] == -__builtin_inff() ? 0.0f : m[n]) * c - MV::kBoost;
         float sum = 0.0f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -890,10 +882,15 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
           f32x4 y = p[t][n];
           if constexpr (I8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = check && y[i] == 0.0f ? 0.0f : y[i] * (kv.vs[t][i] * unit);
+            for (int i = 0; i < 4; ++i) y[i] = check && y[i] == 0.0f ? 0.0f : y[i] * kv.vs[t][i];
           }
-          w[n][2 * t] = M::pack(y[0], y[1]);
-          w[n][2 * t + 1] = M::pack(y[2], y[3]);
+#pragma unroll
+          for (int i = 0; i < 4; i += 2) {
+            const uint32_t hi = MV::pack(y[i], y[i + 1]);
+            w[n][2 * t + i / 2] = hi;
+            if constexpr (PARTS)
+              w_lo[n][2 * t + i / 2] = MV::pack(y[i] - __builtin_bit_cast(float, hi << 16), y[i + 1] - __builtin_bit_cast(float, hi & 0xFFFF0000u));
+          }
         }
         l[n] += sum;
       }
@@ -907,14 +904,17 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             if constexpr (I8) {
               constexpr int W = E0 / 4;
               const uint32_t lo = kv.v[2 * y][h * W + e8 / 4] >> (8 * (e8 & 3)), hi = kv.v[2 * y + 1][h * W + e8 / 4] >> (8 * (e8 & 3));
-              f[y] = M::pack((float)(int8_t)lo, (float)(int8_t)hi);
+              f[y] = MV::pack((float)(int8_t)lo, (float)(int8_t)hi);
             } else {
               constexpr int W = E0 / 2;
               f[y] = __builtin_amdgcn_perm(kv.v[2 * y + 1][h * W + e8 / 2], kv.v[2 * y][h * W + e8 / 2], e8 & 1 ? 0x07060302u : 0x05040100u);
             }
           }
 #pragma unroll
-          for (int n = 0; n < NT; ++n) acc[n][h * E0 + e8] = M::mma(f, w[n], acc[n][h * E0 + e8]);
+          for (int n = 0; n < NT; ++n) {
+            acc[n][h * E0 + e8] = MV::mma(f, w[n], acc[n][h * E0 + e8]);
+            if constexpr (PARTS) acc[n][h * E0 + e8] = MV::mma(f, w_lo[n], acc[n][h * E0 + e8]);
+          }
         }
       next(false);
     };
@@ -1012,7 +1012,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
         const float sum = sum4(l[n]);
         const int r = tile * ROWS + 16 * (wave * NT + n) + col;
         if (r >= rows) continue;
-        const float best = m[n] == -__builtin_inff() ? 0.0f : m[n], unit = I8 && M::kBoost > 0.0f ? __builtin_ldexpf(1.0f, e_ref) : 1.0f;
+        const float best = m[n] == -__builtin_inff() ? 0.0f : m[n];
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         const int64_t row = start + r / G;
         const int qh = head * G + r % G;
@@ -1025,7 +1025,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             if (at >= d) continue;
             float o[E0];
 #pragma unroll
-            for (int x = 0; x < E0; ++x) o[x] = acc[n][h * E0 + x][i] * unit;
+            for (int x = 0; x < E0; ++x) o[x] = acc[n][h * E0 + x][i];
             if (runs == 1) {
               T y[E0];
 #pragma unroll
@@ -1036,9 +1036,9 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             }
           }
         if (quad == 0 && runs == 1 && a.lse)
-          a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - M::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
+          a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - MV::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
         if (quad == 0 && runs > 1) {
-          a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - M::kBoost;
+          a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - MV::kBoost;
           a.part_ml[2 * idx + 1] = sum;
         }
       }
@@ -1062,8 +1062,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
         const float x = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
         return x == -__builtin_inff() ? 0.0f : x;
       };
-      float f = __builtin_amdgcn_exp2f((m[n] - best_of(16 * n + col)) * c);
-      if constexpr (I8 && M::kBoost > 0.0f) f = __builtin_ldexpf(f, e_ref);
+      const float f = __builtin_amdgcn_exp2f((m[n] - best_of(16 * n + col)) * c);
 #pragma unroll
       for (int h = 0; h < NH; ++h)
 #pragma unroll
@@ -1101,12 +1100,12 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
           for (int x = 0; x < HD / 16; ++x) y[x] = from_f<T>(sum == 0.0f ? 0.0f : o[x] * inv);
           __builtin_memcpy(out, y, sizeof y);
           if (a.lse && at == 0)
-            a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - M::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
+            a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - MV::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
         } else {
           const int64_t idx = (row * a.n_heads + qh) * a.max_runs + part;
           __builtin_memcpy(a.part + idx * d + at, o, sizeof o);
           if (at == 0) {
-            a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - M::kBoost;
+            a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - MV::kBoost;
             a.part_ml[2 * idx + 1] = sum;
           }
         }

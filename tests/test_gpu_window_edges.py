@@ -204,3 +204,49 @@ def test_rows_of_no_sequence_count_for_nothing(tokens, dtype, cache):
         got.append([q_out, out, lse, p.k, p.v] + ([p.k_scale, p.v_scale] if cache is I8 else []))
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+# a head's rows in each kind of tile: up to 16, up to 32, up to 64 and more (n_heads / n_kv times the longest window)
+TILES = [(1, 4), (3, 8), (10, 4), (40, 4)]
+
+
+@pytest.mark.parametrize("tokens,n_heads,dtype", [(*t, BF16) for t in TILES[:2]] + [(*t, F16) for t in TILES])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_weights_over_int8_rows_keep_more_than_16_bits(tokens, n_heads, d, dtype):
+    """A weight times its value's scale, in two bfloat16 parts (of up to 32 rows a head, and for float16 queries), is off by 2^-16
+    at most: twice 8 bits. The bound for queries of float32 counts all but that and the rounding of the output."""
+    p = Place([tokens, 1], [700, 90], n_kv=1, d=d, cache=I8, key=d)
+    q = randn((p.n, n_heads * d), dtype, 7, scale=0.3)
+    out = B.moe_window_attention(p.cache, p.window, q, d ** -0.5)
+    want, _, tol, _ = attend_ref(p, q.float(), n_heads, d ** -0.5)
+    most = float((p.v.double() * p.v_scale.double()[..., None]).abs().max())
+    tol += 2.0 ** -16 * most + np.abs(want) * HALF_STEP[dtype] + TINY[dtype]
+    assert (np.abs(host(out) - want) <= tol).all(), float((np.abs(host(out) - want) / tol).max())
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tokens,n_heads", TILES[1:])
+def test_values_scales_far_apart(tokens, n_heads, dtype):
+    """int8 rows whose scales are far above the others': that of a token which only itself sees changes nothing of the rows that do not see
+    it; that of a key which the softmax all but leaves out (2^-60 next to 1) counts by its weight."""
+    d, ctx = 64, 100
+    seen = [1 << j if j == 1 else ((2 << j) - 1) & ~2 for j in range(tokens)]
+    p = Place([tokens], [ctx], n_kv=1, d=d, cache=I8, seen=seen)
+    q = randn((tokens, n_heads * d), dtype, 3, scale=0.2)
+    clean = B.moe_window_attention(p.cache, p.window, q, 0.125)
+    rows = [j for j in range(tokens) if j != 1]
+    page, slot = p.key_at(0, ctx + 1)
+    p.v_scale[page, 0, slot] = 2.0 ** 60
+    out = B.moe_window_attention(p.cache, p.window, q, 0.125)
+    assert torch.equal(out[rows], clean[rows]) and torch.isfinite(clean).all()
+    # a key whose codes are 127 where q's are negative: a score of -60 log 2 beside zeros
+    p = Place([tokens], [ctx], n_kv=1, d=d, cache=I8)
+    p.k.zero_()
+    page, slot = p.key_at(0, 37)
+    p.k[page, 0, slot, 0], p.k_scale[page, 0, slot], p.v_scale[page, 0, slot] = 60, 1.0, 2.0 ** 40
+    q = torch.zeros((tokens, n_heads * d), dtype=dtype, device=DEV)
+    q.view(tokens, n_heads, d)[:, :, 0] = -1.0
+    scale = float(np.float32(np.log(2.0)))
+    out = B.moe_window_attention(p.cache, p.window, q, scale)
+    want, _, tol, _ = attend_ref(p, q, n_heads, scale)
+    assert (np.abs(host(out) - want) <= tol).all() and np.abs(want).max() < 10
