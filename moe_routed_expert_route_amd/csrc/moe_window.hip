@@ -813,6 +813,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             for (int i = 0; i < 4; ++i) p[t][n][i] *= kv.ks[t][i];
       }
       next(true);
+      uint32_t sight[NT] = {};   // I8: the keys that a row sees, whose scales count though their weights may round to 0
       if constexpr (check) {
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -827,9 +828,8 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             for (int n = 0; n < NT; ++n) {
               const bool sees = live[t] && (rel < 0 || (rel < 64 && (seen[n] >> (rel & 63) & 1)));
               p[t][n][i] = sees ? p[t][n][i] : -__builtin_inff();
+              if constexpr (I8) sight[n] |= sees ? 1u << (4 * t + i) : 0;
             }
-            if constexpr (I8)
-              if (rel >= tokens) kv.vs[t][i] = 0.0f;
           }
         // A value of a drafted token that is not finite must not reach rows that do not see it (0 times it is NaN): it
         // counts as 0 here, and add_odd adds it to the rows that do.
@@ -882,7 +882,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
           f32x4 y = p[t][n];
           if constexpr (I8) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) y[i] = check && y[i] == 0.0f ? 0.0f : y[i] * kv.vs[t][i];
+            for (int i = 0; i < 4; ++i) y[i] = check && !(sight[n] >> (4 * t + i) & 1) ? 0.0f : y[i] * kv.vs[t][i];
           }
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {

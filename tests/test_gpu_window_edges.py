@@ -250,3 +250,20 @@ def test_values_scales_far_apart(tokens, n_heads, dtype):
     out = B.moe_window_attention(p.cache, p.window, q, scale)
     want, _, tol, _ = attend_ref(p, q, n_heads, scale)
     assert (np.abs(host(out) - want) <= tol).all() and np.abs(want).max() < 10
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("tokens,n_heads", TILES[1:])
+def test_values_that_are_none_reach_rows_that_hardly_weigh_them(tokens, n_heads, dtype):
+    """int8 rows whose scale is NaN (a row with an infinity in it) have values that are NaN: of every row that sees the token, also where
+    its weight, exp(-200) beside 1, is 0 in float32."""
+    seen = [1 << j if j == 1 else ((2 << j) - 1) & ~(2 if j % 2 else 0) for j in range(tokens)]
+    p = Place([tokens], [100], n_kv=1, d=64, cache=I8, seen=seen)
+    p.k.zero_()
+    page, slot = p.key_at(0, 101)
+    p.k[page, 0, slot, 0], p.k_scale[page, 0, slot], p.v_scale[page, 0, slot] = -100, 2.0, float("nan")
+    q = torch.zeros((tokens, n_heads * 64), dtype=dtype, device=DEV)
+    q.view(tokens, n_heads, 64)[:, :, 0] = 1.0
+    out = B.moe_window_attention(p.cache, p.window, q, 1.0)
+    for j in range(tokens):
+        assert torch.isnan(out[j]).all() if seen[j] & 2 else torch.isfinite(out[j]).all()
