@@ -1499,7 +1499,7 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
   dot = wave_sum(dot);
   const double log_sum = none ? 0.0 : log(sum), base = none ? 0.0 : (double)top;
   const double rest = ((base * (double)c) - ref) * ln2 - log_sum;
-  auto logp_of = [&](float v) { return (float)(((double)v - base) * (double)a.scale + rest); };
+  auto logp_of = [&](float v) { return (float)__builtin_fmin(((double)v - base) * (double)a.scale + rest, 0.0); };   // rest may be 2^-53 above
   if (lane == 0 && a.entropy) a.entropy[row] = none ? 0.0f : (float)__builtin_fmax(log_sum - dot / sum * ln2, 0.0);
   if (lane < a.given) {
     const int id = a.tokens[row * a.given + lane];

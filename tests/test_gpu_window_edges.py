@@ -267,3 +267,15 @@ def test_values_that_are_none_reach_rows_that_hardly_weigh_them(tokens, n_heads,
     out = B.moe_window_attention(p.cache, p.window, q, 1.0)
     for j in range(tokens):
         assert torch.isnan(out[j]).all() if seen[j] & 2 else torch.isfinite(out[j]).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16, F16])
+@pytest.mark.parametrize("n", [1, 3, 5000, 70000])
+def test_no_log_probability_is_above_none(n, dtype):
+    """Rows that are sure of a token: its log probability is 0 to 2^-50 (64-bit roundings next to 1) and no more than 0."""
+    x = randn((300, n), dtype, n, 9, scale=3.0)
+    x[:, 0] += 90.0 + torch.arange(300, device=DEV).to(dtype) / 7
+    for scale in (0.7, 1.0, 1000.0):
+        logp, _, _, top = B.moe_token_logprobs(x, tokens=torch.zeros((300, 1), dtype=torch.int32, device=DEV), k=1, scale=scale)
+        for y in (logp, top):
+            assert (y <= 0).all() and (y >= -2.0 ** -50 - n * np.exp(-60 * scale)).all()
