@@ -1,0 +1,91 @@
+"""Calls on windows that the other tests leave out: prompts of more than 512 tokens in append (four tokens a workgroup), every kind of
+attention's tiles captured and replayed, and logits far from 0. Tolerances are those of test_gpu_window."""
+import numpy as np
+import pytest
+import torch
+
+from moe_routed_expert_route_amd import binding as B
+from moe_routed_expert_route_amd import synth
+from tests.test_gpu_window import TYPES, check_append, check_logprobs, randn
+from tests.test_gpu_window_tiles import TILES
+from tests.window_util import BF16, DEV, F16, F32, I8, Place, tree
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("cache", [BF16, F16, I8])
+@pytest.mark.parametrize("d,n_rot,layout", [(64, 64, B.ROPE_HALF), (128, 128, B.ROPE_HALF), (128, 100, B.ROPE_PAIRS), (80, 36, B.ROPE_PAIRS),
+                                            (16, 2, B.ROPE_HALF), (96, 0, B.ROPE_HALF), (112, 62, B.ROPE_HALF), (256, 250, B.ROPE_HALF),
+                                            (240, 6, B.ROPE_PAIRS)])
+def test_append_prompts(d, n_rot, layout, cache):
+    """513 and more tokens, in sequences that begin and end inside a workgroup's four, some of none."""
+    p = Place([300, 0, 1, 17, 2, 194, 3], [5, 9, 0, 30, 16, 0, 1], d=d, cache=cache, pad=3, key=d + n_rot)
+    check_append(p, 6, BF16 if cache is I8 else cache, F16 if cache is F16 else BF16, n_rot, layout, amp=1.0 if d < 100 else 1.25)
+
+
+@pytest.mark.parametrize("in_type,out_type,w_type", [(F32, BF16, F32), (F32, F32, F32), (BF16, F32, F32), (F16, F16, BF16)])
+@pytest.mark.parametrize("cache", [BF16, I8])
+def test_append_prompts_types(in_type, out_type, w_type, cache):
+    check_append(Place([511, 2], [7, 100], d=128, cache=cache, page=48, order="wide"), 4, in_type, out_type, 64, w_type=w_type)
+
+
+@pytest.mark.parametrize("norm,in_place", [(False, True), (True, True), (False, False)])
+def test_append_prompts_in_place_of_trees_and_many_sequences(norm, in_place):
+    lengths = synth.rng(6).integers(0, 6, 300)
+    bits, depth = tree(lengths, 4)
+    ctx = synth.rng(7).integers(0, 40, 300)
+    pos = [c + e for c, e in zip(np.repeat(ctx, lengths), depth)]
+    check_append(Place(lengths, ctx, n_kv=1, d=64, pad=1, pos=pos), 3, BF16, BF16, 64, norm=norm, in_place=in_place)
+
+
+def test_append_prompts_keys_alone():
+    p = Place([600], [10], d=64, cache=F16)
+    k, v = randn((600, 128), F16, 1), randn((600, 128), F16, 2)
+    assert B.moe_window_append(p.cache, p.window, None, k, v) is None
+    at = np.arange(600) + 10
+    page, slot = torch.from_numpy(p.table[0, at // 16].astype(np.int64)).to(DEV), torch.from_numpy(at % 16).to(DEV)
+    assert torch.equal(p.k[page, :, slot], k.view(600, 2, 64)) and torch.equal(p.v[page, :, slot], v.view(600, 2, 64))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("d", [80, 128, 256])
+@pytest.mark.parametrize("tokens,group", TILES)
+def test_attention_captured_and_replayed(tokens, group, d, dtype, cache):
+    """Lengths, pages, masks and queries change between replays; two graphs on one workspace, replayed one after the other."""
+    lengths = [tokens, 2, tokens // 2]
+    p = Place(lengths, [900, 40, 300], n_kv=2, d=d, cache=cache, seen=tree(lengths)[0], table_pad=3)
+    q = randn((p.n, 2 * group * d), dtype, 8)
+    ws, outs = B.window_workspace(p.cache, p.window, 2 * group), [torch.zeros_like(q) for _ in range(2)]
+    lses = [torch.zeros((p.n, 2 * group), device=DEV) for _ in range(2)]
+    run = lambda i, s: B.moe_window_attention(p.cache, p.window, q, s, out=outs[i], lse=lses[i], ws=ws)
+    run(0, 0.1)
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, g in enumerate(graphs):
+        with torch.cuda.graph(g):
+            run(i, 0.1 + i)
+    for step in range(3):
+        p.window.ctx_len.copy_(torch.tensor([900 - 280 * step, 3 * step, 300 - step], dtype=torch.int32))
+        p.window.seen.bitwise_or_(1 << step)
+        q.copy_(randn(q.shape, dtype, 20 + step))
+        ws.fill_(255)
+        for t in outs + lses:
+            t.fill_(7)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in outs + lses]
+        for i in range(2):
+            run(i, 0.1 + i)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, outs + lses))
+    assert p.window.errors() == 0
+
+
+@pytest.mark.parametrize("n,offset", [(5000, 1000.0), (50021, -3000.0), (50021, 1000.0), (140000, 20000.0)])
+def test_logits_far_from_zero(n, offset):
+    """Float32 rows of a common offset: most values share their first 16 bits, so that a piece's best are among many."""
+    x = randn((5, n), F32, n, 3, scale=2.0) + offset
+    x[1] = torch.round(x[1] * 4) / 4         # and ties
+    x[2, ::3] = float("-inf")
+    check_logprobs(x, torch.tensor([[0, 7, n - 1]] * 5, dtype=torch.int32, device=DEV), 32)
