@@ -1682,7 +1682,10 @@ int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
   return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, kMaxRuns);
 }
 
-constexpr int kAppendFew = 512;   // tokens whose heads are spread over several workgroups
+// Tokens whose heads are spread over several workgroups (above: four tokens a workgroup). 32 + 2 x 8 heads of 128, bf16, launch
+// and kernel: 512 tokens 10.8 us spread, 19.7 by fours; 1024 16.6, 20.6; 1536 23.2, 25.9; 2048 30.7, 27.2; 8192 101, 62. 8 + 2 x 1
+// heads: 1024 6.6, 9.0; 1536 9.6, 10.0; 2048 10.7, 10.4.
+constexpr int kAppendFew = 1536;
 constexpr int kJoinWide = 1024;   // rows and heads that get four waves each
 
 // Attention's sizes beside those of the cache and the window, for the call and for the size of its workspace.

@@ -1,5 +1,5 @@
-"""Calls on windows that the other tests leave out: prompts of more than 512 tokens in append (four tokens a workgroup), every kind of
-attention's tiles captured and replayed, and logits far from 0. Tolerances are those of test_gpu_window."""
+"""Calls on windows that the other tests leave out: prompts in append, of up to 1536 tokens and of more (four tokens a workgroup), every
+kind of attention's tiles captured and replayed, and logits far from 0. Tolerances are those of test_gpu_window."""
 import numpy as np
 import pytest
 import torch
@@ -13,38 +13,62 @@ from tests.window_util import BF16, DEV, F16, F32, I8, Place, tree
 pytestmark = pytest.mark.gpu
 
 
+@pytest.mark.parametrize("first", [300, 1324])
 @pytest.mark.parametrize("cache", [BF16, F16, I8])
 @pytest.mark.parametrize("d,n_rot,layout", [(64, 64, B.ROPE_HALF), (128, 128, B.ROPE_HALF), (128, 100, B.ROPE_PAIRS), (80, 36, B.ROPE_PAIRS),
                                             (16, 2, B.ROPE_HALF), (96, 0, B.ROPE_HALF), (112, 62, B.ROPE_HALF), (256, 250, B.ROPE_HALF),
                                             (240, 6, B.ROPE_PAIRS)])
-def test_append_prompts(d, n_rot, layout, cache):
-    """513 and more tokens, in sequences that begin and end inside a workgroup's four, some of none."""
-    p = Place([300, 0, 1, 17, 2, 194, 3], [5, 9, 0, 30, 16, 0, 1], d=d, cache=cache, pad=3, key=d + n_rot)
+def test_append_prompts(d, n_rot, layout, cache, first):
+    """517 and 1541 tokens, in sequences that begin and end inside a workgroup's four, some of none."""
+    p = Place([first, 0, 1, 17, 2, 194, 3], [5, 9, 0, 30, 16, 0, 1], d=d, cache=cache, pad=3, key=d + n_rot)
     check_append(p, 6, BF16 if cache is I8 else cache, F16 if cache is F16 else BF16, n_rot, layout, amp=1.0 if d < 100 else 1.25)
 
 
 @pytest.mark.parametrize("in_type,out_type,w_type", [(F32, BF16, F32), (F32, F32, F32), (BF16, F32, F32), (F16, F16, BF16)])
 @pytest.mark.parametrize("cache", [BF16, I8])
 def test_append_prompts_types(in_type, out_type, w_type, cache):
-    check_append(Place([511, 2], [7, 100], d=128, cache=cache, page=48, order="wide"), 4, in_type, out_type, 64, w_type=w_type)
+    for n in (511, 1535):
+        check_append(Place([n, 2], [7, 100], d=128, cache=cache, page=48, order="wide"), 4, in_type, out_type, 64, w_type=w_type)
 
 
 @pytest.mark.parametrize("norm,in_place", [(False, True), (True, True), (False, False)])
 def test_append_prompts_in_place_of_trees_and_many_sequences(norm, in_place):
-    lengths = synth.rng(6).integers(0, 6, 300)
+    lengths = synth.rng(6).integers(0, 9, 450)
     bits, depth = tree(lengths, 4)
-    ctx = synth.rng(7).integers(0, 40, 300)
+    assert sum(lengths) > 1536
+    ctx = synth.rng(7).integers(0, 40, 450)
     pos = [c + e for c, e in zip(np.repeat(ctx, lengths), depth)]
     check_append(Place(lengths, ctx, n_kv=1, d=64, pad=1, pos=pos), 3, BF16, BF16, 64, norm=norm, in_place=in_place)
 
 
-def test_append_prompts_keys_alone():
-    p = Place([600], [10], d=64, cache=F16)
-    k, v = randn((600, 128), F16, 1), randn((600, 128), F16, 2)
+@pytest.mark.parametrize("n", [600, 1600])
+def test_append_prompts_keys_alone(n):
+    p = Place([n], [10], d=64, cache=F16)
+    k, v = randn((n, 128), F16, 1), randn((n, 128), F16, 2)
     assert B.moe_window_append(p.cache, p.window, None, k, v) is None
-    at = np.arange(600) + 10
+    at = np.arange(n) + 10
     page, slot = torch.from_numpy(p.table[0, at // 16].astype(np.int64)).to(DEV), torch.from_numpy(at % 16).to(DEV)
-    assert torch.equal(p.k[page, :, slot], k.view(600, 2, 64)) and torch.equal(p.v[page, :, slot], v.view(600, 2, 64))
+    assert torch.equal(p.k[page, :, slot], k.view(n, 2, 64)) and torch.equal(p.v[page, :, slot], v.view(n, 2, 64))
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("n", [1537, 2051])
+def test_append_prompts_whole_and_in_parts(n, dtype, cache):
+    """The same bits in one call and in calls of 500 tokens behind one another."""
+    q, k, v = randn((n, 512), dtype, 1), randn((n, 256), dtype, 2), randn((n, 256), dtype, 3)
+    w, freq = randn((128,), dtype, 4) + 1, torch.rand(64, device=DEV)
+    got = []
+    for part in (n, 500):
+        p = Place([n], [30], d=128, cache=cache)
+        q_out = torch.zeros_like(q)
+        for i in range(0, n, part):
+            m = min(part, n - i)
+            ints = lambda *x: torch.tensor(x, dtype=torch.int32, device=DEV)
+            one = B.Window(ints(0, m), ints(30 + i), p.window.pages, m)
+            B.moe_window_append(p.cache, one, q[i:i + m], k[i:i + m], v[i:i + m], freq=freq, q_weight=w, k_weight=w, q_out=q_out[i:i + m])
+            assert one.errors() == 0
+        got.append([q_out, p.k, p.v] + ([p.k_scale, p.v_scale] if cache is I8 else []))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
 
 
 @pytest.mark.parametrize("dtype,cache", TYPES)
