@@ -113,3 +113,74 @@ def test_logits_far_from_zero(n, offset):
     x[1] = torch.round(x[1] * 4) / 4         # and ties
     x[2, ::3] = float("-inf")
     check_logprobs(x, torch.tensor([[0, 7, n - 1]] * 5, dtype=torch.int32, device=DEV), 32)
+
+
+def far_apart(rows, n, step, dtype, key):
+    """Rows of n values `step` elements apart, in a buffer that is otherwise not written."""
+    buf = torch.empty(rows * step, dtype=dtype, device=DEV).view(rows, step)[:, :n]
+    buf.copy_(randn((rows, n), dtype, key))
+    return buf
+
+
+@pytest.mark.parametrize("dtype,cache", [(BF16, BF16), (F16, I8)])
+def test_offsets_past_32_bits(dtype, cache):
+    """Pages 2^28 bytes and more apart (their last 10 GB from the first), rows of queries and outputs 2^24 elements apart (the last 2^32 from
+    the first), against the same calls on what lies close together."""
+    pages, n_kv, page, d, n_heads, tokens = 40, 2, 16, 64, 4, [20, 1, 64]
+    ctx = [300, 40, 0]
+    near = Place(tokens, ctx, n_kv=n_kv, d=d, cache=cache)
+    assert near.n_pages <= pages
+    wide = torch.empty(2 * pages << 27, dtype=cache, device=DEV).view(pages, 2, 1 << 27)[:, :, :n_kv * page * d]
+    spread = [pages - 1 - i for i in range(near.n_pages)]
+    pools = []
+    for i, pool in enumerate((near.k, near.v)):
+        far = wide[:, i].view(pages, n_kv, page, d)
+        far[spread] = pool
+        pools.append(far)
+    scales = [None, None]
+    if cache is I8:
+        scales = [torch.zeros((pages, n_kv, page), device=DEV) for _ in range(2)]
+        for far, s in zip(scales, (near.k_scale, near.v_scale)):
+            far[spread] = s
+    far = B.KVCache(*pools, *scales)
+    table = torch.full_like(near.window.pages, -7)
+    for s, row in enumerate(near.table):
+        for c, x in enumerate(row):
+            if x >= 0:
+                table[s, c] = spread[x]
+    w = B.Window(near.window.row_start, near.window.ctx_len, table, near.rows, near.window.max_window)
+    n = near.rows
+    q, k, v = randn((n, n_heads * d), dtype, 1), randn((n, n_kv * d), dtype, 2), randn((n, n_kv * d), dtype, 3)
+    outs = []
+    for cache_, window in ((near.cache, near.window), (far, w)):
+        q_out = B.moe_window_append(cache_, window, q, k, v, freq=torch.ones(32, device=DEV))
+        outs.append([q_out, B.moe_window_attention(cache_, window, q_out, 0.1)])
+        assert window.errors() == 0
+    assert all(torch.equal(a, b) for a, b in zip(*outs))
+    for i, pool in enumerate((near.k, near.v)):
+        assert torch.equal(pools[i][spread], pool)
+    if cache is I8:
+        return
+    step, rows = 1 << 24, 260
+    p = Place([rows - 10, 10], [3, 50], n_kv=1, d=d, cache=cache)
+    small = B.Window(torch.tensor([250, 260], dtype=torch.int32, device=DEV), p.window.ctx_len[1:], p.window.pages[1:], rows, 10)
+    q, q_out = far_apart(rows, 128, step, dtype, 4), far_apart(rows, 128, step, dtype, 5)
+    kv = randn((rows, 64), dtype, 6)
+    close_q = q.contiguous()
+    want = B.moe_window_append(p.cache, p.window, close_q, kv, kv, freq=torch.ones(32, device=DEV))
+    k0 = p.k.clone()
+    B.moe_window_append(p.cache, p.window, q, kv, kv, freq=torch.ones(32, device=DEV), q_out=q_out)
+    assert torch.equal(q_out, want) and torch.equal(p.k, k0) and p.window.errors() == 0
+    got = far_apart(rows, 128, step, dtype, 7)
+    before = got.clone()
+    B.moe_window_attention(p.cache, small, q_out, 0.1, out=got)
+    near_out = before.clone()
+    B.moe_window_attention(p.cache, small, want, 0.1, out=near_out)
+    assert small.errors() == 0 and torch.equal(got, near_out) and torch.equal(got[:250], before[:250]) and not torch.equal(got[250:], before[250:])
+
+
+def test_logits_past_32_bits():
+    x = far_apart(1100, 3000, 1 << 22, F16, 9)
+    t = torch.arange(1100, dtype=torch.int32, device=DEV)[:, None]
+    for a, b in zip(B.moe_token_logprobs(x, tokens=t, k=9, entropy=True), B.moe_token_logprobs(x.contiguous(), tokens=t, k=9, entropy=True)):
+        assert torch.equal(a, b)
