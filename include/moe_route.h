@@ -325,8 +325,8 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * Conventions beside those at the top: row strides (ld*) count elements and are at least the row
  * length and at most MOE_MAX_SPAN / rows; any such stride and any row alignment an element type
  * allows is accepted (16-byte aligned rows are fastest). Row elements past the row length and rows
- * past the last are neither read nor written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row pointers may be
- * NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
+ * past the last are neither read nor written. Offsets are 64-bit. A call of zero rows does nothing and succeeds (its row
+ * pointers may be NULL). Nothing needs a workspace, so calls and captured graphs may overlap on any streams as long
  * as their outputs do not. Outputs may not overlap inputs or each other unless a comment says so (rows of
  * one buffer side by side, of one stride, do not). Results do not depend on the number of rows of the
  * call: a row gives the same bits alone and among others.
@@ -335,7 +335,8 @@ int moe_workspace_layout(const moe_layer* L, const moe_plan* P, size_t off[3]);
  * the q8_1 rule with the row as the block: d = max|y| / 127 (float32), q = clamp(round-half-away(
  * y / d), +-127) with the float32 quotient; d = 0 gives zero codes; a row holding an infinity or a
  * NaN gives d = NaN and zero codes. The value a code stands for is q * d. */
-typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3, MOE_I8 = 4 } moe_dtype;   /* element types of rows; MOE_I8: of a cache alone */
+/* element types of rows; MOE_I8: of a cache alone */
+typedef enum { MOE_F32 = 1, MOE_BF16 = 2, MOE_F16 = 3, MOE_I8 = 4 } moe_dtype;
 #define MOE_MAX_ROW 16384         /* max n of the row calls (moe_add_rmsnorm, moe_swiglu_i8) */
 #define MOE_MAX_ROWS 4194303      /* max rows of those and tokens of moe_route_scores (a launch's threads) */
 #define MOE_MAX_SPAN (1ll << 50)  /* max rows x stride of one operand, elements: more than any memory */
@@ -415,11 +416,11 @@ int moe_matmul_i8(void* stream, const int8_t* a, int64_t lda, const float* sa, c
 
 /* A layer's cache. Row (page p, head h, slot i) of k and of v starts p * page_stride + h * head_stride + i *
  * slot_stride elements from k and v and holds head_dim elements; strides are positive multiples of 16, slot_stride at most
- * 2^24, of any nesting order, and rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k and v are
- * 16-byte aligned.
+ * 2^24, of any nesting order, and rows may not overlap (of k, of v, or of one and the other, which may share a buffer). k
+ * and v are 16-byte aligned.
  * dtype MOE_BF16, MOE_F16, or MOE_I8: i8 rows, one scale a row at [(p * n_kv + h) * page_size + i] of k_scale and v_scale
- * (NULL for the others), outside of the rows' span. page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple of 16 up to 256; n_kv up to
- * MOE_MAX_HEADS. Host struct holding device pointers. */
+ * (NULL for the others), outside of the rows' span. page_size: a multiple of 16 up to MOE_MAX_PAGE; head_dim: a multiple
+ * of 16 up to 256; n_kv up to MOE_MAX_HEADS. Host struct holding device pointers. */
 #define MOE_MAX_PAGE 65536
 #define MOE_MAX_HEADS 1024
 #define MOE_MAX_SEQS 4096
@@ -435,12 +436,12 @@ typedef struct moe_kv_cache {
 } moe_kv_cache;
 
 /* The tokens of one call. Sequence s has rows row_start[s] .. row_start[s + 1] - 1 of the call's n_tokens rows (rows of
- * no sequence, such as padding behind the last, are not written, and what they hold counts for nothing) and ctx_len[s] keys before them in its
- * pages: key i is slot i % page_size of page pages[s * ld_pages + i / page_size], and the window's token j is key
- * ctx_len[s] + j. Pages may be shared between sequences where nothing is written to them. max_pages <= ld_pages columns are
- * read at most, max_pages * page_size < 2^31. max_window: the most tokens of a sequence. pos (NULL: the token's key
- * index): rotary position of each row. seen (NULL: token j sees tokens 0 .. j): bit i of seen[row] set = the row's
- * token sees token i of its window (its own bit too); bits past the window count nothing; every token sees the
+ * no sequence, such as padding behind the last, are not written, and what they hold counts for nothing) and ctx_len[s]
+ * keys before them in its pages: key i is slot i % page_size of page pages[s * ld_pages + i / page_size], and the window's
+ * token j is key ctx_len[s] + j. Pages may be shared between sequences where nothing is written to them. max_pages <=
+ * ld_pages columns are read at most, max_pages * page_size < 2^31. max_window: the most tokens of a sequence. pos (NULL:
+ * the token's key index): rotary position of each row. seen (NULL: token j sees tokens 0 .. j): bit i of seen[row] set =
+ * the row's token sees token i of its window (its own bit too); bits past the window count nothing; every token sees the
  * whole context. Host struct holding device pointers. */
 typedef struct moe_window {
   int32_t n_seqs, n_tokens, max_window, max_pages;
@@ -478,16 +479,16 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
  * A row that sees nothing gets out = 0 and lse = -infinity. Keys that a row does not see, and slots past the last key, count
  * for nothing whatever they hold (infinities and NaN too). Head h reads the cache's head h / (n_heads / n_kv).
  * q, out [n_tokens][ldq], [ldo] in `dtype`: the cache's type, or MOE_BF16 or MOE_F16 over an i8 cache; lse float32
- * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max) is rounded to `dtype` in front of its product,
- * over an i8 cache, times the value's scale, to 16 bits of float32's range (of bfloat16 queries of more than 32 rows a
+ * [n_tokens][n_heads]. Products of `dtype` values with float32 sums; exp(s_i - max) is rounded to `dtype` in front of its
+ * product, over an i8 cache, times the value's scale, to 16 bits of float32's range (of bfloat16 queries of more than 32 rows a
  * cache head, max_window x n_heads / n_kv, to bfloat16). The sum below is of the unrounded ones.
  * A value of a window's key that is not finite reaches the rows that see it, and no others. A sequence's keys are summed in
  * runs whose length depends on its own key count and on the call's sizes (n_seqs, max_window, heads): a token's bits do not
  * depend on what the other sequences of the call hold.
  * workspace: moe_window_attention_bytes, 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type or
- * stride, scale past 2^127 or NaN, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW, n_heads
- * not a multiple of n_kv, n_tokens x n_heads past MOE_MAX_JOIN where max_pages * page_size is more than a run: 256 to 1024
- * by the call's sizes), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
+ * stride, scale past 2^127 or NaN, overlap), MOE_E_SHAPE (sizes out of the limits above, max_window past MOE_MAX_WINDOW,
+ * n_heads not a multiple of n_kv, n_tokens x n_heads past MOE_MAX_JOIN where max_pages * page_size is more than a run: 256
+ * to 1024 by the call's sizes), MOE_E_WS. moe_window_attention_bytes: 0 for sizes that the call refuses. */
 size_t moe_window_attention_bytes(const moe_kv_cache* C, const moe_window* W, int n_heads);   /* host */
 int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* W, int dtype, const void* q, int64_t ldq,
                          int n_heads, float scale, void* out, int64_t ldo, float* lse, void* workspace, size_t ws_bytes);
@@ -496,15 +497,15 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
  * alternatives), beside moe_route_scores:
  *   logp[r][j] = log p(tokens[r][j]) (-infinity for an id out of [0, n): no token);  entropy[r] = -sum p log p;
  *   top_ids[r], top_logp[r] = the k tokens of the largest logits, largest first, ties to the lower id, and their log p.
- * A logit of -infinity or NaN masks its token: p = 0, log p = -infinity, and it comes after every unmasked one in the order, lowest
- * id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. 0 < scale <= 2^127.
- * Each output is written when its pointer is not NULL (tokens and logp, given > 0: all or none; top_ids and top_logp, k > 0:
- * all or none; at least one output). logits [rows][ld] in `dtype`, tokens int32 [rows][given]. n <= MOE_MAX_VOCAB,
- * given <= 64, k <= 32 and k <= n. Sums of up to 2^14 terms in float32 (up to 64 one after the other), of those in 64 bits; a row's bits do not depend on the others.
- * workspace: moe_token_logprobs_bytes (0 for sizes that the call refuses), 16-byte aligned. Errors: MOE_E_ARG (null or
- * misaligned pointer, bad type, stride, count or scale, overlap), MOE_E_SHAPE (rows > MOE_MAX_ROWS, n not in
- * 1..MOE_MAX_VOCAB, or more than MOE_MAX_PIECES pieces: rows x n / 8192, or / 16384 above 65536, n rounded up to a piece),
- * MOE_E_WS. */
+ * A logit of -infinity or NaN masks its token: p = 0, log p = -infinity, and it comes after every unmasked one in the
+ * order, lowest id first. A row with every token masked has entropy 0. +infinity counts as the largest finite float32. 0 <
+ * scale <= 2^127. Each output is written when its pointer is not NULL (tokens and logp, given > 0: all or none; top_ids
+ * and top_logp, k > 0: all or none; at least one output). logits [rows][ld] in `dtype`, tokens int32 [rows][given]. n <=
+ * MOE_MAX_VOCAB, given <= 64, k <= 32 and k <= n. Sums of up to 2^14 terms in float32 (up to 64 one after the other), of
+ * those in 64 bits; a row's bits do not depend on the others. workspace: moe_token_logprobs_bytes (0 for sizes that the
+ * call refuses), 16-byte aligned. Errors: MOE_E_ARG (null or misaligned pointer, bad type, stride, count or scale,
+ * overlap), MOE_E_SHAPE (rows > MOE_MAX_ROWS, n not in 1..MOE_MAX_VOCAB, or more than MOE_MAX_PIECES pieces: rows x n /
+ * 8192, or / 16384 above 65536, n rounded up to a piece), MOE_E_WS. */
 #define MOE_MAX_VOCAB (1 << 22)
 #define MOE_MAX_PIECES 16777215
 size_t moe_token_logprobs_bytes(int rows, int n, int k);   /* host */

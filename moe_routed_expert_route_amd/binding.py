@@ -109,7 +109,8 @@ def lib():
         L.moe_swiglu_i8.argtypes = [_P, _I, _P, _L, _P, _L, _I, _I, _P, _L, _P]
         L.moe_matmul_i8.argtypes = [_P, _P, _L, _P, _P, _L, _P, _I, _I, _I, _I, _P, _L, _I]
         both = [ctypes.POINTER(MoeKvCache), ctypes.POINTER(MoeWindow)]
-        L.moe_window_append.argtypes = [_P, *both, _I, _P, _L, _P, _L, _P, _L, _I, _I, _P, _P, _F, _P, _I, _I, ctypes.c_double, _I, _P, _L]
+        L.moe_window_append.argtypes = [_P, *both, _I, _P, _L, _P, _L, _P, _L, _I, _I, _P, _P, _F, _P, _I, _I, ctypes.c_double, _I,
+                                        _P, _L]
         L.moe_window_attention_bytes.argtypes = [*both, _I]
         L.moe_window_attention_bytes.restype = ctypes.c_size_t
         L.moe_window_attention.argtypes = [_P, *both, _I, _P, _L, _I, _F, _P, _L, _P, _P, ctypes.c_size_t]

@@ -337,7 +337,10 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
     }
     uint32_t most = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = max(most, (e < 4 ? e < p.n0 : e - 4 < p.n1) ? __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu : 0u);
+    for (int e = 0; e < 8; ++e) {
+      const bool there = e < 4 ? e < p.n0 : e - 4 < p.n1;
+      most = max(most, there ? __builtin_bit_cast(uint32_t, f[e]) & 0x7FFFFFFFu : 0u);
+    }
     most = lanes_max<LG>(most);
     const bool finite = most < 0x7F800000u;
     const QScale s = q_scale(__builtin_bit_cast(float, most));
@@ -371,10 +374,14 @@ __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {
 // long as V agrees), and a lane loads the same eight neighbouring values of eight keys, from which a byte permutation
 // makes the eight rows of V^T. Without WIDE there is no LDS until the waves join.
 // Bound by the cache's bytes up to some 32 rows a cache head: 4 tokens x 8 heads over 131072 keys 55 us (4.9 TB/s) and 5 to
-// join, one token 50 us (5.3 TB/s); 64 sequences x 4 tokens of 512 to 8192 keys, int8 136 us (4.4 TB/s) and 8. One token
-// over 4096 keys takes 11 us and 4 to join: loads that wait for each other (lengths, pages, keys) and code that is new to the
-// instruction cache. Trees of 64 tokens x 8 heads over 4096 to 8100 keys 219 us (0.44 PFLOP/s) and 24: some 230 vector and
-// 170 scalar instructions beside 32 matrix instructions a step, which two waves a SIMD overlap only in part.
+// join, one token 50 us (5.3 TB/s); 64 sequences x 4 tokens of 512 to 8192 keys, int8 137 us (4.4 TB/s) and 8, bf16 231
+// (4.9 TB/s). One token over 4096 keys takes 11 us and 4 to join: 64 workgroups, whose waves walk two steps of loads
+// that wait for each other (lengths, pages, keys). Trees of 64 tokens x 8 heads over 4096 to 8100 keys 220 us (0.44 PFLOP/s)
+// and 24: counted over the launch, 328 vector and 115 scalar instructions for every 32 matrix instructions (a step), which
+// two waves a SIMD overlap only in part; some 180 scalars are spilled to lanes. Their runs' results are 104 MB written and
+// read back where the case itself has 207. Registers: two tiles of 128 wide 16-bit heads spill 5 (16 bytes of scratch a
+// lane), two of 144 to 256 values 133 (380 bytes, one wave a SIMD): 4 tokens x 8 heads of 256 over 131072 keys 133 us
+// (4.0 TB/s).
 // Tried and slower: keys and values of two steps in registers (145 us for the int8 batch where this takes 136), three
 // waves a SIMD (spills; 158), values read from the ring when they are needed (265 us for the trees where this takes 219).
 
@@ -462,23 +469,31 @@ struct Keys {
   f32x4 ks[2], vs[2];
 };
 
+// The log of a sum of 2^(x - best), in natural units.
+__device__ __forceinline__ float lse_of(float best, float sum) {
+  return sum == 0.0f ? -__builtin_inff() : (best + __builtin_log2f(sum)) * 0.69314718055994530942f;
+}
+
 constexpr uint32_t kNowhere = 0x80000000u;   // an offset past any buffer: the load gives 0 and touches nothing
 
 // HD: 64, 128 or 256, the least that holds head_dim. NT: a wave's tiles of 16 rows. WIDE: the waves share the keys, which
-// then go through LDS (a ring of stages of 32 keys, loaded straight into it), and have rows of their own; otherwise they share the rows, and a wave takes 64 of every 256 keys. The next
-// keys are loaded as soon as these are multiplied, the next values as soon as these are.
-constexpr int ring_bytes(int hd, bool i8) { return 64 * hd * (i8 ? 1 : 2) * (hd * (i8 ? 1 : 2) > 256 ? 2 : 3); }   // three stages, or two large ones
+// then go through LDS (a ring of stages of 32 keys, loaded straight into it), and have rows of their own; otherwise they
+// share the rows, and a wave takes 64 of every 256 keys. The next keys are loaded as soon as these are multiplied, the
+// next values as soon as these are.
+constexpr int ring_bytes(int hd, bool i8) {   // three stages, or two large ones
+  return 64 * hd * (i8 ? 1 : 2) * (hd * (i8 ? 1 : 2) > 256 ? 2 : 3);
+}
 constexpr int kAttendWaves(int hd) { return hd < 256 ? 2 : 1; }   // of a SIMD: what their registers leave room for
 template <typename T, bool I8, int HD, int NT, bool WIDE>
 __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) {
   using M = Mat<T>;
   using KV = Keys<I8, HD>;
-  // In front of V a weight is rounded to T, which costs bits: the error of bfloat16 outputs of 1 x 4 tokens over 131072 keys against
-  // 64 bits is 2.1e-3 instead of 1.7e-3. (Two parts of 8 bits each, two products: as fast there, but 8 x 64 bf16 258 us
-  // instead of 219.) Over an int8 cache a weight has its value's scale in it, of float32's range and any size next to the
-  // others', and is bfloat16 whatever T: float16 under a common power of two lost the rows whose scales are small. It is
-  // in two parts there (64 x 4 of 8192: 2.4e-3 and 1.7e-3, 136 us and 137), but for bfloat16 queries of many rows, which
-  // the products bound (8 x 64: 261 us, in two parts 290 to 303).
+  // In front of V a weight is rounded to T, which costs bits: the error of bfloat16 outputs of 1 x 4 tokens over 131072 keys
+  // against 64 bits is 2.1e-3 instead of 1.7e-3. (Two parts of 8 bits each, two products: as fast there, but 8 x 64 bf16
+  // 258 us instead of 219.) Over an int8 cache a weight has its value's scale in it, of float32's range and any size next
+  // to the others', and is bfloat16 whatever T: float16 under a common power of two lost the rows whose scales are small.
+  // It is in two parts there (64 x 4 of 8192: 2.4e-3 and 1.7e-3, 136 us and 137), but for bfloat16 queries of many rows,
+  // which the products bound (8 x 64: 261 us, in two parts 290 to 303).
   using MV = Mat<std::conditional_t<I8, bf16_t, T>>;
   constexpr bool PARTS = I8 && (!WIDE || std::is_same_v<T, f16_t>);
   constexpr int ROWS = 16 * NT * (WIDE ? 4 : 1), KS = HD / 32, E0 = HD < 128 ? 4 : 8, NH = HD < 128 ? 1 : HD / 128, DT = E0 * NH;
@@ -490,9 +505,11 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
   // the ring: rows of 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that neighbouring lanes meet other banks
   constexpr int CR = HD * SIZE / 16, HALF = 32 * HD * SIZE, STAGE = 2 * HALF, STAGES = ring_bytes(HD, I8) / STAGE;
   constexpr int RPI = 64 / CR, NI = 32 / RPI, PER = NI / 2;   // rows a load instruction has, loads of K, loads a wave makes
-  extern __shared__ __align__(16) uint8_t s_ring[];            // static, the compiler would have reads wait for the loads on their way
+  // static, the compiler would have reads wait for the loads on their way
+  extern __shared__ __align__(16) uint8_t s_ring[];
   int* const s_end = (int*)(s_ring + (WIDE ? STAGES * STAGE : 0));   // [n_seqs]: items of the sequences up to this one
-  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, col = lane & 15, quad = lane >> 4;
+  const int tid = threadIdx.x, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lane = tid & 63, col = lane & 15, quad = lane >> 4;
   const int G = a.n_heads / a.c.n_kv, d = a.c.d;
   auto items_of = [&](int start, int end, int ctx) {
     if (!seq_ok(a.w, start, end, ctx, a.w.max_window)) {
@@ -664,17 +681,24 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
     };
     const uint64_t k_head = (uint64_t)(a.c.k + head * a.c.head * SIZE), v_head = (uint64_t)(a.c.v + head * a.c.head * SIZE);
     auto lane64 = [](uint32_t lo, uint32_t hi, int i) {
-      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, i) | (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
+      return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, i) |
+             (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
     };
-    auto buffer = [](uint64_t at, bool live) { return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, live ? 0x7FFFFFFF : 0, 0x00027000); };
+    auto buffer = [](uint64_t at, bool live) {
+      return __builtin_amdgcn_make_buffer_rsrc((void*)at, 0, live ? 0x7FFFFFFF : 0, 0x00027000);
+    };
+    auto four = [&](const float* scales, uint64_t at, bool live) {
+      const auto from = buffer((uint64_t)scales + at, live);
+      return __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(from, quad * 16, 0, 0));
+    };
     auto scales = [&](KV& kv, int step, bool k, bool v) {
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int i = 2 * (step & 31) + t;
         const bool live = step < steps && (there >> i & 1);
         const uint64_t at = lane64(sc_lo, sc_hi, i);
-        if (k) kv.ks[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer((uint64_t)a.c.ks + at, live), quad * 16, 0, 0));
-        if (v) kv.vs[t] = __builtin_bit_cast(f32x4, __builtin_amdgcn_raw_buffer_load_b128(buffer((uint64_t)a.c.vs + at, live), quad * 16, 0, 0));
+        if (k) kv.ks[t] = four(a.c.ks, at, live);
+        if (v) kv.vs[t] = four(a.c.vs, at, live);
       }
     };
 
@@ -706,14 +730,15 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
           for (int h = 0; h < NH; ++h) {
             constexpr int W = E0 * SIZE / 4;
             uint32_t* to = &kv.v[4 * t + i][h * W];
+            const int slot = (int)(i * slot_bytes);
             if constexpr (W == 4) {
-              const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[h], (int)(i * slot_bytes), 0));
+              const u32x4 x = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(vr, v_off[h], slot, 0));
               to[0] = x[0], to[1] = x[1], to[2] = x[2], to[3] = x[3];
             } else if constexpr (W == 2) {
-              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[h], (int)(i * slot_bytes), 0));
+              const u32x2 x = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(vr, v_off[h], slot, 0));
               to[0] = x[0], to[1] = x[1];
             } else {
-              to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, v_off[h], (int)(i * slot_bytes), 0);
+              to[0] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(vr, v_off[h], slot, 0);
             }
           }
       }
@@ -739,8 +764,8 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
         const int j = wave + 4 * x, of_v = j >= NI, row0 = (of_v ? j - NI : j) * RPI, i = at + (row0 >> 4);
         const auto from = __builtin_amdgcn_make_buffer_rsrc((void*)((of_v ? v_head : k_head) + lane64(at_lo, at_hi, i)), 0,
                                                             there >> i & 1 ? 0x7FFFFFFF : 0, 0x00027000);
-        if (s_off[x] != kNowhere)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(from, (MOE_LDS void*)(stage + of_v * HALF + row0 * (HD * SIZE)), 16, (int)s_off[x], 0, 0, 0);
+        MOE_LDS void* const to = (MOE_LDS void*)(stage + of_v * HALF + row0 * (HD * SIZE));
+        if (s_off[x] != kNowhere) __builtin_amdgcn_raw_ptr_buffer_load_lds(from, to, 16, (int)s_off[x], 0, 0, 0);
       }
     };
     auto read = [&](KV& kv, int slot) {
@@ -759,7 +784,8 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             const int byte = (h * 128 + col * E0) * SIZE, r = 4 * quad + i;
             constexpr int W = E0 * SIZE / 4;
             using Words = std::conditional_t<W == 4, u32x4, std::conditional_t<W == 2, u32x2, uint32_t>>;
-            const Words x = *(const Words*)(stage + HALF + (16 * t + r) * (HD * SIZE) + ((byte >> 4) ^ swizzle(r)) * 16 + (byte & 15));
+            const uint8_t* const row = stage + HALF + (16 * t + r) * (HD * SIZE);
+            const Words x = *(const Words*)(row + ((byte >> 4) ^ swizzle(r)) * 16 + (byte & 15));
             __builtin_memcpy(&kv.v[4 * t + i][h * W], &x, 4 * W);
           }
       }
@@ -889,7 +915,8 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             const uint32_t hi = MV::pack(y[i], y[i + 1]);
             w[n][2 * t + i / 2] = hi;
             if constexpr (PARTS)
-              w_lo[n][2 * t + i / 2] = MV::pack(y[i] - __builtin_bit_cast(float, hi << 16), y[i + 1] - __builtin_bit_cast(float, hi & 0xFFFF0000u));
+              w_lo[n][2 * t + i / 2] = MV::pack(y[i] - __builtin_bit_cast(float, hi << 16),
+                                                y[i + 1] - __builtin_bit_cast(float, hi & 0xFFFF0000u));
           }
         }
         l[n] += sum;
@@ -903,11 +930,13 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
           for (int y = 0; y < 4; ++y) {
             if constexpr (I8) {
               constexpr int W = E0 / 4;
-              const uint32_t lo = kv.v[2 * y][h * W + e8 / 4] >> (8 * (e8 & 3)), hi = kv.v[2 * y + 1][h * W + e8 / 4] >> (8 * (e8 & 3));
+              const uint32_t lo = kv.v[2 * y][h * W + e8 / 4] >> (8 * (e8 & 3));
+              const uint32_t hi = kv.v[2 * y + 1][h * W + e8 / 4] >> (8 * (e8 & 3));
               f[y] = MV::pack((float)(int8_t)lo, (float)(int8_t)hi);
             } else {
               constexpr int W = E0 / 2;
-              f[y] = __builtin_amdgcn_perm(kv.v[2 * y + 1][h * W + e8 / 2], kv.v[2 * y][h * W + e8 / 2], e8 & 1 ? 0x07060302u : 0x05040100u);
+              f[y] = __builtin_amdgcn_perm(kv.v[2 * y + 1][h * W + e8 / 2], kv.v[2 * y][h * W + e8 / 2],
+                                           e8 & 1 ? 0x07060302u : 0x05040100u);
             }
           }
 #pragma unroll
@@ -1036,7 +1065,7 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
             }
           }
         if (quad == 0 && runs == 1 && a.lse)
-          a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - MV::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
+          a.lse[row * a.n_heads + qh] = lse_of(best * c - MV::kBoost, sum);
         if (quad == 0 && runs > 1) {
           a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - MV::kBoost;
           a.part_ml[2 * idx + 1] = sum;
@@ -1046,77 +1075,77 @@ __global__ __launch_bounds__(256, kAttendWaves(HD)) void k_attend(AttendArgs a) 
       continue;
     }
     if constexpr (!WIDE) {
-    // the waves' results, in their order
+      // the waves' results, in their order
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const float sum = sum4(l[n]);
-      if (quad == 0) {
-        s_m[wave][16 * n + col] = m[n];
-        s_l[wave][16 * n + col] = sum;
-      }
-    }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      auto best_of = [&](int r) {
-        const float x = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
-        return x == -__builtin_inff() ? 0.0f : x;
-      };
-      const float f = __builtin_amdgcn_exp2f((m[n] - best_of(16 * n + col)) * c);
-#pragma unroll
-      for (int h = 0; h < NH; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int e4 = 0; e4 < E0; e4 += 4) {
-            f32x4 y;
-#pragma unroll
-            for (int x = 0; x < 4; ++x) y[x] = acc[n][h * E0 + e4 + x][i] * f;
-            *(f32x4*)&s_o[wave][col * STRIDE + h * 128 + (4 * quad + i) * E0 + e4] = y;
-          }
-      __syncthreads();
-      const int rr = tid >> 4, at = (tid & 15) * (HD / 16), r = tile * ROWS + 16 * n + rr;
-      if (r < rows && at < d) {
-        const float best = best_of(16 * n + rr);
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) sum += s_l[w][16 * n + rr] * __builtin_amdgcn_exp2f((s_m[w][16 * n + rr] - best) * c);
-        const int64_t row = start + r / G;
-        const int qh = head * G + r % G;
-        float o[HD / 16];
-#pragma unroll
-        for (int x = 0; x < HD / 16; x += 4) {
-          f32x4 y = *(const f32x4*)&s_o[0][rr * STRIDE + at + x];
-#pragma unroll
-          for (int w = 1; w < 4; ++w) y += *(const f32x4*)&s_o[w][rr * STRIDE + at + x];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[x + i] = y[i];
-        }
-        if (runs == 1) {
-          T* out = (T*)a.out + row * a.ldo + (int64_t)qh * d + at;
-          const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-          T y[HD / 16];
-#pragma unroll
-          for (int x = 0; x < HD / 16; ++x) y[x] = from_f<T>(sum == 0.0f ? 0.0f : o[x] * inv);
-          __builtin_memcpy(out, y, sizeof y);
-          if (a.lse && at == 0)
-            a.lse[row * a.n_heads + qh] = sum == 0.0f ? -__builtin_inff() : (best * c - MV::kBoost + __builtin_log2f(sum)) * 0.69314718055994530942f;
-        } else {
-          const int64_t idx = (row * a.n_heads + qh) * a.max_runs + part;
-          __builtin_memcpy(a.part + idx * d + at, o, sizeof o);
-          if (at == 0) {
-            a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - MV::kBoost;
-            a.part_ml[2 * idx + 1] = sum;
-          }
+      for (int n = 0; n < NT; ++n) {
+        const float sum = sum4(l[n]);
+        if (quad == 0) {
+          s_m[wave][16 * n + col] = m[n];
+          s_l[wave][16 * n + col] = sum;
         }
       }
       __syncthreads();
-    }
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        auto best_of = [&](int r) {
+          const float x = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
+          return x == -__builtin_inff() ? 0.0f : x;
+        };
+        const float f = __builtin_amdgcn_exp2f((m[n] - best_of(16 * n + col)) * c);
+#pragma unroll
+        for (int h = 0; h < NH; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e4 = 0; e4 < E0; e4 += 4) {
+              f32x4 y;
+#pragma unroll
+              for (int x = 0; x < 4; ++x) y[x] = acc[n][h * E0 + e4 + x][i] * f;
+              *(f32x4*)&s_o[wave][col * STRIDE + h * 128 + (4 * quad + i) * E0 + e4] = y;
+            }
+        __syncthreads();
+        const int rr = tid >> 4, at = (tid & 15) * (HD / 16), r = tile * ROWS + 16 * n + rr;
+        if (r < rows && at < d) {
+          const float best = best_of(16 * n + rr);
+          float sum = 0.0f;
+#pragma unroll
+          for (int w = 0; w < 4; ++w) sum += s_l[w][16 * n + rr] * __builtin_amdgcn_exp2f((s_m[w][16 * n + rr] - best) * c);
+          const int64_t row = start + r / G;
+          const int qh = head * G + r % G;
+          float o[HD / 16];
+#pragma unroll
+          for (int x = 0; x < HD / 16; x += 4) {
+            f32x4 y = *(const f32x4*)&s_o[0][rr * STRIDE + at + x];
+#pragma unroll
+            for (int w = 1; w < 4; ++w) y += *(const f32x4*)&s_o[w][rr * STRIDE + at + x];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[x + i] = y[i];
+          }
+          if (runs == 1) {
+            T* out = (T*)a.out + row * a.ldo + (int64_t)qh * d + at;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            T y[HD / 16];
+#pragma unroll
+            for (int x = 0; x < HD / 16; ++x) y[x] = from_f<T>(sum == 0.0f ? 0.0f : o[x] * inv);
+            __builtin_memcpy(out, y, sizeof y);
+            if (a.lse && at == 0)
+              a.lse[row * a.n_heads + qh] = lse_of(best * c - MV::kBoost, sum);
+          } else {
+            const int64_t idx = (row * a.n_heads + qh) * a.max_runs + part;
+            __builtin_memcpy(a.part + idx * d + at, o, sizeof o);
+            if (at == 0) {
+              a.part_ml[2 * idx] = sum == 0.0f ? -__builtin_inff() : best * c - MV::kBoost;
+              a.part_ml[2 * idx + 1] = sum;
+            }
+          }
+        }
+        __syncthreads();
+      }
     }
   }
 }
 
-// The runs of a row and head, by W waves: 8192 rows 8.4 us by one each, 16.4 by four. Lanes side by side take four neighbouring values, and the groups of lanes every
+// The runs of a row and head, by W waves. Lanes side by side take four neighbouring values, and the groups of lanes every
 // 4 W / (2 W, W)-th run of head_dim up to 64 (128, 256), always in the same order.
 template <typename T, int W>
 __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
@@ -1173,7 +1202,7 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
     for (int i = 0; i < 4; ++i) y[i] = from_f<T>(sum == 0.0f ? 0.0f : o[i] / sum);
     __builtin_memcpy(out, y, sizeof y);
     if (a.lse && at == 0)
-      a.lse[(int64_t)row * a.n_heads + head] = sum == 0.0f ? -__builtin_inff() : (best + __builtin_log2f(sum)) * 0.69314718055994530942f;
+      a.lse[(int64_t)row * a.n_heads + head] = lse_of(best, sum);
   }
 }
 
@@ -1181,10 +1210,11 @@ __global__ __launch_bounds__(256) void k_attend_join(AttendArgs a) {
 //
 // A row is cut into pieces of 256 lanes times EL values (by the row's length alone, so that its sums have one order).
 // k_scores takes a piece into registers, reads it once, and leaves its maximum, its sums of e = exp(z) and of e z, and the best
-// tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The
-// pieces' bound for the best is the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at
-// least that, and few values are above it. 1024 x 131072 bf16: 62 us for k = 8 (4.4 TB/s), 47 for none; the join
-// 7 and 5. Slower: workgroups that go on to further pieces with the next one's values on their way (75; 55 for none).
+// tokens among which the row's k best must be; k_scores_join puts the pieces of a row together. The pieces' bound for the best
+// is the k-th largest of 64 maxima of four lanes each (of its first 16 bits); k of them are at least that, and few values
+// are above it. (Float32 rows far from 0 share these bits: 257 x 50021 with 20 best 25 us, plus 1000 155, as pieces of more
+// than kListed candidates take one best after the other.) 1024 x 131072 bf16: 62 us for k = 8 (4.4 TB/s), 47 for none; the
+// join 7 and 5. Slower: workgroups that go on to further pieces with the next one's values on their way (75; 55 for none).
 
 struct ScoreArgs {
   const void* logits;
@@ -1273,20 +1303,21 @@ struct Eight {
     if constexpr (sizeof(T) == 4) return __builtin_bit_cast(float, w[e]);
     else return to_f(__builtin_bit_cast(T, (uint16_t)(w[e / 2] >> (16 * (e & 1)))));
   }
-  static __device__ __forceinline__ uint32_t none() {   // -infinity, one or two of them
-    const uint32_t v = sizeof(T) == 4 ? 0xFF800000u : (uint32_t)__builtin_bit_cast(uint16_t, from_f<std::conditional_t<sizeof(T) == 4, bf16_t, T>>(-__builtin_inff()));
-    return sizeof(T) == 4 ? v : v | v << 16;
+  static __device__ __forceinline__ uint32_t bits_of(float x) {   // of a word of it: one or two of them
+    if constexpr (sizeof(T) == 4) return __builtin_bit_cast(uint32_t, x);
+    else return (uint32_t)__builtin_bit_cast(uint16_t, from_f<T>(x)) * 0x10001u;
   }
+  static __device__ __forceinline__ uint32_t none() { return bits_of(-__builtin_inff()); }
   // Values of the bits of `top` become -infinity; returns `bits` and the bits of these values.
   __device__ __forceinline__ int take_out(float top, int bits) {
-    const uint32_t t = sizeof(T) == 4 ? __builtin_bit_cast(uint32_t, top)
-                                      : (uint32_t)__builtin_bit_cast(uint16_t, from_f<std::conditional_t<sizeof(T) == 4, bf16_t, T>>(top)) * 0x10001u;
+    const uint32_t t = bits_of(top);
 #pragma unroll
     for (int i = 0; i < W; ++i) {
       const uint32_t d = w[i] ^ t;
       uint32_t m;
       if constexpr (sizeof(T) == 4) m = (uint32_t)((int32_t)((d >> 1 | (d & 1)) - 1) >> 31);
-      else m = ((uint32_t)((int32_t)((d & 0xFFFFu) - 1) >> 31) & 0xFFFFu) | ((uint32_t)((int32_t)((d >> 16) - 1) >> 31) & 0xFFFF0000u);
+      else m = ((uint32_t)((int32_t)((d & 0xFFFFu) - 1) >> 31) & 0xFFFFu) |
+               ((uint32_t)((int32_t)((d >> 16) - 1) >> 31) & 0xFFFF0000u);
       w[i] = (w[i] & ~m) | (none() & m);
       bits += __builtin_popcount(m);
     }
@@ -1468,7 +1499,8 @@ __global__ __launch_bounds__(256) void k_scores(ScoreArgs a) {
       __syncthreads();
       if (tid == 0) best[i] = last;
     }
-  }}
+  }
+}
 
 // A wave a row.
 template <typename T>
@@ -1490,7 +1522,8 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
     const float m = stats[4 * p];
     if (m == -__builtin_inff()) continue;
     // the maxima's z, which the rounding of the reference leaves a little off 0, and their share
-    const double off = (double)m * (double)c - reference(m, c), tops = (double)(__builtin_bit_cast(int, stats[4 * p + 3]) >> 16) * exp64(off * ln2);
+    const double off = (double)m * (double)c - reference(m, c);
+    const double tops = (double)(__builtin_bit_cast(int, stats[4 * p + 3]) >> 16) * exp64(off * ln2);
     const double z = reference(m, c) - ref, f = exp64(z * ln2), s = (double)stats[4 * p + 1] + tops;
     sum = __builtin_fma(s, f, sum);
     dot = __builtin_fma(f, __builtin_fma(s, f > 0.0 ? z : 0.0, __builtin_fma(tops, off, (double)stats[4 * p + 2])), dot);
@@ -1499,7 +1532,8 @@ __global__ __launch_bounds__(64) void k_scores_join(ScoreArgs a) {
   dot = wave_sum(dot);
   const double log_sum = none ? 0.0 : log(sum), base = none ? 0.0 : (double)top;
   const double rest = ((base * (double)c) - ref) * ln2 - log_sum;
-  auto logp_of = [&](float v) { return (float)__builtin_fmin(((double)v - base) * (double)a.scale + rest, 0.0); };   // rest may be 2^-53 above
+  // rest may be 2^-53 above 0
+  auto logp_of = [&](float v) { return (float)__builtin_fmin(((double)v - base) * (double)a.scale + rest, 0.0); };
   if (lane == 0 && a.entropy) a.entropy[row] = none ? 0.0f : (float)__builtin_fmax(log_sum - dot / sum * ln2, 0.0);
   if (lane < a.given) {
     const int id = a.tokens[row * a.given + lane];
@@ -1570,7 +1604,8 @@ struct Extent {
 };
 Extent cache_extent(const moe_kv_cache& c) {
   const int size = c.dtype == MOE_I8 ? 1 : 2;
-  const int64_t apart = (int64_t)((uintptr_t)c.v > (uintptr_t)c.k ? (uintptr_t)c.v - (uintptr_t)c.k : (uintptr_t)c.k - (uintptr_t)c.v);
+  const uintptr_t k = (uintptr_t)c.k, v = (uintptr_t)c.v;
+  const int64_t apart = (int64_t)(v > k ? v - k : k - v);
   struct {
     int64_t count, step;
   } dim[] = {{c.n_pages, c.page_stride}, {c.n_kv, c.head_stride}, {c.page_size, c.slot_stride}};
@@ -1629,8 +1664,8 @@ int check_window(const moe_window* w, const moe_kv_cache& c) {
   if (w->n_seqs == 0 || w->n_tokens == 0) return MOE_OK;
   if (w->max_window < 1 || w->max_pages < 1 || (int64_t)w->max_pages * c.page_size > 0x7FFFFFFF) return MOE_E_SHAPE;
   if (!w->row_start || !w->ctx_len || !w->pages || !w->err || bad_stride(w->ld_pages, w->max_pages, w->n_seqs)) return MOE_E_ARG;
-  if (!aligned(w->row_start, 4) || !aligned(w->ctx_len, 4) || !aligned(w->pages, 4) || !aligned(w->pos, 4) || !aligned(w->seen, 8) ||
-      !aligned(w->err, 4))
+  if (!aligned(w->row_start, 4) || !aligned(w->ctx_len, 4) || !aligned(w->pages, 4) || !aligned(w->pos, 4) ||
+      !aligned(w->seen, 8) || !aligned(w->err, 4))
     return MOE_E_ARG;
   return MOE_OK;
 }
@@ -1670,9 +1705,13 @@ WindowArgs window_args(const moe_window& w, const moe_kv_cache& c) {
 
 // Rows that share a cache head, at most.
 int most_rows(const moe_kv_cache& c, const moe_window& w, int n_heads) { return w.max_window * (n_heads / c.n_kv); }
-// The least keys of a run, by how many sequences, cache heads and tiles of rows there are to spread over the card: 6
-// sequences x 2 heads of up to 1000 keys 18.5 us in runs of 256, 24.0 of 1024; 64 x 8 of up to 8192 196 us in runs of
-// 256 (their results are a quarter of the bytes), 158 of 1024, 160 of 2048.
+// The least keys of a run, by how many sequences, cache heads and tiles of 128 rows there are to spread over the card. Launches
+// and kernels, us in runs of 256 / 512 / 1024 (2048), bf16. One token, four or eight query heads a cache head: 16 units over
+// 1000 keys 14.0 / 16.2 / 16.7, over 16000 32.0 / 29.6 / 29.7; 32 units 13.9 / 16.1 / 16.5 and 52 / 49 / 49; 48 units
+// 14.2 / 16.5 / 16.6 and 90 / 84 / 90; 128 units 21.7 / 21.5 / 18.5 and 224 / 204 / 197; 192 units 29.6 / 27.1 / 22.0 and
+// 330 / 302 / 291. Trees of 64 tokens x 8 heads: 32 units 31 / 38 / 57 and 126 / 98 / 83 (103); 128 units 65 / 53 / 65 and
+// 520 / 361 / 287 (257); 256 units 96 / 93 / 88 (60) and 991 / 709 / 574 (504). So it leans to short contexts: long ones, of
+// trees above all, would take longer runs, whose results are fewer.
 int least_run(const moe_kv_cache& c, const moe_window& w, int n_heads) {
   const int64_t units = (int64_t)w.n_seqs * c.n_kv * ((most_rows(c, w, n_heads) + 127) / 128);
   return units <= 32 ? 256 : units <= 128 ? 512 : 1024;
@@ -1682,11 +1721,14 @@ int max_runs(const moe_kv_cache& c, const moe_window& w, int n_heads) {
   return (int)std::min<int64_t>(((int64_t)w.max_pages * c.page_size + least - 1) / least, kMaxRuns);
 }
 
-// Tokens whose heads are spread over several workgroups (above: four tokens a workgroup). 32 + 2 x 8 heads of 128, bf16, launch
-// and kernel: 512 tokens 10.8 us spread, 19.7 by fours; 1024 16.6, 20.6; 1536 23.2, 25.9; 2048 30.7, 27.2; 8192 101, 62. 8 + 2 x 1
-// heads: 1024 6.6, 9.0; 1536 9.6, 10.0; 2048 10.7, 10.4.
+// Tokens whose heads are spread over several workgroups (above: four tokens a workgroup). A sequence of 32 + 2 x 8 heads of 128,
+// bf16, launch and kernel: 512 tokens 10.8 us spread, 19.7 by fours; 1024 16.6, 20.6; 1536 23.2, 25.9; 2048 30.7, 27.2; 8192
+// 101, 62. Of 8 + 2 x 1 heads: 1024 6.6, 9.0; 1536 9.6, 10.0; 2048 10.7, 10.4. Tokens that are sequences of their own, where
+// each workgroup looks for its sequence: 640 15.0, 22.0; 1024 23.5, 24.3; 1500 34.3, 29.7.
 constexpr int kAppendFew = 1536;
-constexpr int kJoinWide = 1024;   // rows and heads that get four waves each
+// Rows and heads whose runs are joined by four waves each, above by one: 32 rows of 63 runs 4.9 us by four, 6.1 by one; 512 of 64
+// 6.5, 6.7; 1024 8.8, 8.5; 8192 of some 6 16.4, 8.4.
+constexpr int kJoinWide = 1024;
 
 // Attention's sizes beside those of the cache and the window, for the call and for the size of its workspace.
 int check_attend(const moe_kv_cache& c, const moe_window& w, int n_heads) {
@@ -1726,7 +1768,13 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   auto tiles = [&](auto i, auto hd) {
     constexpr bool I8 = decltype(i)::value;
     constexpr int HD = decltype(hd)::value;
-    if (rows > 32) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, HD == 256 && !I8 ? 1 : 2, true>(st, a);
+    // Launches and kernels, us of 32 sequences over 4000 keys, bf16 and int8. 16 rows a cache head: one tile a wave 50 and 34,
+    // two 52 and 40. 20 rows: two tiles 54 and 41, one in two workgroups 65 and 54 (of one sequence over 60000 keys 34, 33). 40
+    // rows: wide 65 and 76, two tiles in two workgroups 76 and 72 (one sequence 47, 37). 64 rows: wide of one tile 72 and 82,
+    // of two 83 and 96; 128 rows: wide of two 105 and 114, of one 127 and 151. 32 rows of heads of 256 over 2000 keys: two
+    // tiles 91, one in two workgroups 80.
+    constexpr int MOST = HD == 256 && !I8 ? 1 : 2;   // tiles that a wave of the wide kernel has registers for
+    if (rows > 32) return rows <= 64 ? launch_attend<T, I8, HD, 1, true>(st, a) : launch_attend<T, I8, HD, MOST, true>(st, a);
     return rows <= 16 ? launch_attend<T, I8, HD, 1, false>(st, a) : launch_attend<T, I8, HD, 2, false>(st, a);
   };
   auto width = [&](auto i) {
@@ -1738,8 +1786,10 @@ int run_attend(hipStream_t st, const AttendArgs& a, bool i8) {
   return i8 ? width(std::true_type{}) : width(std::false_type{});
 }
 
-// Values of a lane: 32 spread short rows over more workgroups; 1024 rows of 131072 with 8 best 53 us with 64, 61 with 32
-// (both with the maxima left in the sum).
+// Values of a lane: 32 spread short rows over more workgroups. Launches and kernels with 8 best, us by 32 and by 64: 1024 rows of
+// bf16 20000 21.2, 24.0; 50021 35.1, 37.0; 65536 37.5, 36.6; 80000 45.0, 42.2; 131072 63.9, 59.1; one row of 32000 9.8, 10.5;
+// 262144 13.7, 12.2. float32: 1024 x 50021 43.4, 50.0; 1024 x 131072 104, 112; 64 x 262144 25.8, 24.1; one row of
+// 262144 13.9, 13.0.
 constexpr int kShortRow = 65536, kLongEl = 64;
 int pieces_of(int n) { return n <= kShortRow ? (n + 8191) / 8192 : (n + 256 * kLongEl - 1) / (256 * kLongEl); }
 // The sizes of log probabilities, for the call and for the size of its workspace.
@@ -1767,7 +1817,8 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
   if ((q_weight || k_weight) && (!type_ok(w_dtype) || !(eps > 0.0f) || !(eps < __builtin_inff()))) return MOE_E_ARG;
   if (!(__builtin_fabs(amp) < __builtin_inff()) || (layout != MOE_ROPE_HALF && layout != MOE_ROPE_PAIRS)) return MOE_E_ARG;
   const int d = C->head_dim, n = W->n_tokens;
-  if (n_rot < 0 || n_rot > d || n_rot % 2 || (q && (n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv))) return MOE_E_SHAPE;
+  if (n_rot < 0 || n_rot > d || n_rot % 2) return MOE_E_SHAPE;
+  if (q && (n_heads < 1 || n_heads > MOE_MAX_HEADS || n_heads % C->n_kv)) return MOE_E_SHAPE;
   if (W->n_seqs == 0 || n == 0) return MOE_OK;
   const int64_t wide = (int64_t)n_heads * d, kv = (int64_t)C->n_kv * d;
   if (!k || !v || (n_rot && !freq) || bad_stride(ldk, kv, n) || bad_stride(ldv, kv, n)) return MOE_E_ARG;
@@ -1792,7 +1843,8 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
   for (int i = 0; i < 5; ++i)
     if (overlap(window[i], window[5])) return MOE_E_ARG;
   const int heads = q ? n_heads : 0, all = heads + 2 * C->n_kv;
-  const int lanes = std::max((d + 7) / 8, (n_rot + 7) / 8 + (d - n_rot + 7) / 8), lg = lanes <= 8 ? 8 : lanes <= 16 ? 16 : lanes <= 32 ? 32 : 64;
+  const int lanes = std::max((d + 7) / 8, (n_rot + 7) / 8 + (d - n_rot + 7) / 8);
+  const int lg = lanes <= 8 ? 8 : lanes <= 16 ? 16 : lanes <= 32 ? 32 : 64;
   const int units = n <= kAppendFew ? 256 / lg : all;
   const AppendArgs a{cache_args(*C), window_args(*W, *C), q, k, v, q_weight, k_weight, freq, q_out, ldq, ldk, ldv, ldqo,
                      heads, n_rot, layout, w_dtype, o_dtype, C->dtype, units, eps, amp};
@@ -1800,8 +1852,10 @@ int moe_window_append(void* stream, const moe_kv_cache* C, const moe_window* W, 
     using T = decltype(t);
     auto go = [&](auto l) {
       constexpr int LG = decltype(l)::value;
-      if (n <= kAppendFew) hipLaunchKernelGGL((k_window_append<T, LG, 1>), dim3(n, (all + units - 1) / units), dim3(256), 0, (hipStream_t)stream, a);
-      else hipLaunchKernelGGL((k_window_append<T, LG, 4>), dim3((n + 3) / 4), dim3(256), 0, (hipStream_t)stream, a);
+      const hipStream_t st = (hipStream_t)stream;
+      const int parts = (all + units - 1) / units;
+      if (n <= kAppendFew) hipLaunchKernelGGL((k_window_append<T, LG, 1>), dim3(n, parts), dim3(256), 0, st, a);
+      else hipLaunchKernelGGL((k_window_append<T, LG, 4>), dim3((n + 3) / 4), dim3(256), 0, st, a);
     };
     using std::integral_constant;
     if (lg == 8) go(integral_constant<int, 8>{});
@@ -1828,8 +1882,8 @@ int moe_window_attention(void* stream, const moe_kv_cache* C, const moe_window* 
   const int n = W->n_tokens;
   if (W->n_seqs == 0 || n == 0) return MOE_OK;
   const int64_t wide = (int64_t)n_heads * C->head_dim;
-  if (!q || !out || bad_stride(ldq, wide, n) || bad_stride(ldo, wide, n) || !aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4))
-    return MOE_E_ARG;
+  if (!q || !out || bad_stride(ldq, wide, n) || bad_stride(ldo, wide, n)) return MOE_E_ARG;
+  if (!aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4)) return MOE_E_ARG;
   const size_t need = moe_window_attention_bytes(C, W, n_heads);
   if (!workspace || ws_bytes < need || !aligned(workspace, 16)) return MOE_E_WS;
   Rows spans[kCacheSpans], window[kWindowSpans];
@@ -1886,7 +1940,8 @@ int moe_token_logprobs(void* stream, int dtype, const void* logits, int64_t ld, 
   const int pieces = pieces_of(n);
   const int64_t blocks = (int64_t)rows * pieces;
   float* const stats = (float*)workspace;
-  const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, stats, (uint64_t*)(stats + 4 * blocks), ld, n, given, k, pieces, scale};
+  const ScoreArgs a{logits, tokens, logp, entropy, top_logp, top_ids, stats, (uint64_t*)(stats + 4 * blocks), ld, n, given, k,
+                    pieces, scale};
   with_type(dtype, [&](auto t) {
     using T = decltype(t);
     if (n <= kShortRow) hipLaunchKernelGGL((k_scores<T, 32>), dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
