@@ -194,7 +194,7 @@ __device__ __forceinline__ double inverse_sqrt64(double x) {
 // four partners), or eight values that do not turn. A workgroup takes `units` heads of a token, or all of TK tokens, which
 // it looks up side by side, a wave each; the next head's values are on their way while it works on one, the first before
 // the sequences are known. Everything is in 64 bits: sums and products at full rate, conversions at a quarter, which bound
-// 8192 tokens of 48 heads of 128 (77 us, 2.6 TB/s; without the norm 69). One token takes 5.1 us: loads that wait for each other.
+// 8192 tokens of 48 heads of 128 (77 us, 2.6 TB/s; without the norm 69). One token takes 5.3 us: loads that wait for each other.
 // Slower for the 8192: one token a workgroup (99 us), two to four heads on their way (82 to 98), weights kept in 64 bits (101).
 template <typename T, int LG, int TK>
 __global__ __launch_bounds__(256) void k_window_append(AppendArgs a) {

@@ -1,5 +1,7 @@
 """Calls on windows that the other tests leave out: prompts in append, of up to 1536 tokens and of more (four tokens a workgroup), every
 kind of attention's tiles captured and replayed, and logits far from 0. Tolerances are those of test_gpu_window."""
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -8,7 +10,7 @@ from moe_routed_expert_route_amd import binding as B
 from moe_routed_expert_route_amd import synth
 from tests.test_gpu_window import TYPES, check_append, check_logprobs, randn
 from tests.test_gpu_window_tiles import TILES
-from tests.window_util import BF16, DEV, F16, F32, I8, Place, tree
+from tests.window_util import BF16, DEV, F16, F32, I8, Place, attend_ref, host, tree
 
 pytestmark = pytest.mark.gpu
 
@@ -184,3 +186,25 @@ def test_logits_past_32_bits():
     t = torch.arange(1100, dtype=torch.int32, device=DEV)[:, None]
     for a, b in zip(B.moe_token_logprobs(x, tokens=t, k=9, entropy=True), B.moe_token_logprobs(x.contiguous(), tokens=t, k=9, entropy=True)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("n,group", [(200, 4), (129, 1)])
+def test_a_prompt_appended_whole_and_attended_in_parts(n, group, dtype, cache):
+    """A prompt longer than attention's windows: appended in one call, then attended as sequences of up to 64 tokens that share its
+    pages, each with the ones before it as its context."""
+    p = Place([n], [30], n_kv=2, d=128, cache=cache, page=32)
+    q, k, v = randn((n, 2 * group * 128), dtype, 1), randn((n, 256), dtype, 2), randn((n, 256), dtype, 3)
+    q_out = B.moe_window_append(p.cache, p.window, q, k, v, freq=torch.ones(64, device=DEV) / 7)
+    parts = copy.copy(p)
+    parts.tokens = [min(64, n - i) for i in range(0, n, 64)]
+    parts.ctx = [30 + i for i in range(0, n, 64)]
+    parts.start = np.concatenate([[0], np.cumsum(parts.tokens)])
+    parts.table = np.repeat(p.table, len(parts.tokens), 0)
+    ints = lambda x: torch.tensor(x, dtype=torch.int32, device=DEV)
+    parts.window = B.Window(ints(parts.start), ints(parts.ctx), p.window.pages.expand(len(parts.tokens), -1).contiguous(), n, 64)
+    lse = torch.zeros((n, 2 * group), device=DEV)
+    out = B.moe_window_attention(p.cache, parts.window, q_out, 128 ** -0.5, lse=lse)
+    want, want_lse, tol, lse_tol = attend_ref(parts, q_out, 2 * group, 128 ** -0.5)
+    assert (np.abs(host(out) - want) <= tol).all() and (np.abs(host(lse) - want_lse) <= lse_tol).all()
+    assert p.window.errors() == 0 and parts.window.errors() == 0
