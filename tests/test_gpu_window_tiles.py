@@ -126,3 +126,20 @@ def test_the_most_sequences(d, dtype, cache, tokens, n_heads):
     out = check_attention(p, n_heads, dtype)[0]
     again = B.moe_window_attention(p.cache, p.window, randn((p.rows, n_heads * d), dtype, 1, 5), d ** -0.5)
     assert torch.equal(out, again)
+
+
+@pytest.mark.parametrize("dtype,cache", TYPES)
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("tokens,group", TILES)
+def test_keys_that_end_at_every_place_of_a_step(tokens, group, d, dtype, cache):
+    """Windows that begin and end at each of the 32 keys of a step, of tokens that see themselves, the context and some others: each
+    place of a tile masked for some rows, or past the last key, where the slots hold NaN."""
+    lengths = [1 + s % min(tokens, 7) for s in range(40)]
+    rng = np.random.default_rng(d + tokens)
+    seen = [int(rng.integers(0, 1 << t)) | 1 << j for t in lengths for j in range(t)]
+    p = Place(lengths, [s if s < 8 else 57 + s for s in range(40)], n_kv=1, d=d, cache=cache, seen=seen, max_window=tokens)
+    keep = {(int(a), b) for s in range(40) for a, b in (p.key_at(s, i) for i in range(lengths[s] + p.ctx[s]))}
+    bad = [(a, b) for a in range(p.n_pages) for b in range(p.page) if (a, b) not in keep]
+    for pool in (p.k_scale, p.v_scale) if cache is I8 else (p.k, p.v):
+        pool[[a for a, _ in bad], :, [b for _, b in bad]] = math.nan
+    check_attention(p, group, dtype, key=d)
